@@ -82,6 +82,12 @@ typedef enum moe_precision {
     MOE_FP8 = 2               /* E4M3 operands, one power-of-two scale per tensor */
 } moe_precision;
 
+/* Element type of a tensor that may be either (the layer norm's rows and weights). */
+typedef enum moe_type {
+    MOE_TYPE_BF16 = 0,
+    MOE_TYPE_F32 = 1
+} moe_type;
+
 /* moe_route flags */
 #define MOE_ROUTE_RENORM 0u       /* softmax over the k picked logits (default) */
 #define MOE_ROUTE_SOFTMAX_ALL 1u  /* softmax over all E logits, taken at the picks */
@@ -618,6 +624,97 @@ int grouped_linear_bwd(int precision, int E, int N, int K, int64_t rows, const u
                        const uint16_t* x, const int32_t* split_sizes, const uint16_t* const* w,
                        uint16_t* dx, uint16_t* const* dw, void* workspace,
                        size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_layernorm_fwd -- the layer norm in front of the router and the experts.
+ * [AutoModel, "MoE 微调的痛点": the MoE layer takes the place of the block's
+ *  feed-forward.  The pages do not give the block's norm; it is read as the
+ *  layer norm of a pre-norm transformer block.]
+ *
+ * Per row t:  mean = sum_h x / H,  var = sum_h (x - mean)^2 / H,
+ *   rstd = (var + eps)^-1/2,  xh = (x - mean) rstd,  y = bf16(xh gamma + beta).
+ * Statistics and xh in fp32; the variance is summed around the mean.
+ *
+ * x_type       MOE_TYPE_BF16 or MOE_TYPE_F32: x (a residual stream may be fp32).
+ * w_type       MOE_TYPE_BF16 or MOE_TYPE_F32: gamma and beta.
+ * T, H         rows (0 <= T <= INT32_MAX) and width: a multiple of 8, 8..32768;
+ *              with a checkpoint a multiple of 32.
+ * x            [T, H].   gamma, beta: [H], or NULL for 1 and 0.   eps >= 0.
+ * y            bf16 [T, H] out.
+ * mean, rstd   fp32 [T] out, each may be NULL (inference).
+ * xhat_codes, xhat_scales   both or neither (MOE_ERR_ARG): the 8-bit
+ *              checkpoint of xh that moe_layernorm_bwd takes in place of x,
+ *              uint8 [T, H] and [T, H/32]: MXFP8 in the layout and by the rule
+ *              of mxfp8_quantize axis=1, from the fp32 xh.
+ * A row with a NaN or an infinity gives NaN in its own y, mean and rstd; its
+ * checkpoint is unspecified.
+ */
+int moe_layernorm_fwd(int x_type, int w_type, int64_t T, int H, const void* x, const void* gamma,
+                      const void* beta, float eps, uint16_t* y, float* mean, float* rstd,
+                      uint8_t* xhat_codes, uint8_t* xhat_scales, hipStream_t stream);
+
+/*
+ * moe_layernorm_bwd -- backward of moe_layernorm_fwd.
+ * [The same passage.]
+ *
+ *   g = dy gamma;  dx = rstd (g - mean_h(g) - xh mean_h(g xh)) + dres
+ *   dgamma = sum_t dy xh;   dbeta = sum_t dy
+ * xh is decoded from the checkpoint when it is given (x and mean are then not
+ * read and may be NULL), else computed from x, mean and rstd.  Sums in fp32;
+ * dgamma and dbeta are added up in a fixed order (the same bits every time)
+ * and rounded once to w_type.
+ *
+ * x_type       type of x, dres and dx.   w_type: of gamma, dgamma and dbeta.
+ * dy           bf16 [T, H].   rstd: fp32 [T] from the forward.
+ * dres         [T, H] gradient that reaches x past the norm (the residual
+ *              path), added before dx's one rounding; or NULL.  May be dx.
+ * dx           [T, H] out.
+ * dgamma, dbeta  [H] out, each may be NULL (not wanted); zeros when T = 0.
+ * workspace    moe_layernorm_workspace_bytes(T, H) bytes when dgamma or dbeta
+ *              is given, else not used.
+ */
+int moe_layernorm_bwd(int x_type, int w_type, int64_t T, int H, const uint16_t* dy, const void* x,
+                      const float* mean, const float* rstd, const uint8_t* xhat_codes,
+                      const uint8_t* xhat_scales, const void* gamma, const void* dres, void* dx,
+                      void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream);
+
+/* Workspace bytes of moe_layernorm_bwd; 0 for sizes it refuses. */
+size_t moe_layernorm_workspace_bytes(int64_t T, int H);
+
+/*
+ * moe_swiglu_fwd -- ScaledSwiGLU by itself, for experts built from two
+ * grouped_linear_fwd calls (grouped_mlp_fwd does it in its GEMM).
+ * [BioNeMo, "MXFP8与融合MLP": ScaledSwiGLU is SwiGLU times the routing
+ *  probability.]
+ *
+ * a1           bf16 [rows, 2I]: gate in columns [0, I), up in [I, 2I).
+ * prob         fp32 [rows] (prob_perm of moe_permute), or NULL for 1.
+ * a2           bf16 [rows, I] out: bf16(prob silu(gate) up), fp32 inside (a
+ *              sigmoid below 2^-126 counts as 0).
+ * I            a multiple of 8, 8..2^20; with a checkpoint a multiple of 32.
+ * a1_codes, a1_scales   both or neither (MOE_ERR_ARG): the 8-bit checkpoint
+ *              of a1 that moe_swiglu_bwd takes in its place, uint8 [rows, 2I]
+ *              and [rows, 2I/32]: byte for byte mxfp8_quantize(a1, axis=1).
+ */
+int moe_swiglu_fwd(int64_t rows, int I, const uint16_t* a1, const float* prob, uint16_t* a2,
+                   uint8_t* a1_codes, uint8_t* a1_scales, hipStream_t stream);
+
+/*
+ * moe_swiglu_bwd -- backward of moe_swiglu_fwd.
+ * [BioNeMo, "MXFP8与融合MLP": the fused forward has a matching backward, and
+ *  the probabilities, being scales, receive a gradient.]
+ *
+ * g, u from a1 or from its checkpoint (one of the two; both: MOE_ERR_ARG);
+ * s = silu(g), sig = sigmoid(g):
+ *   dg = da2 p u sig (1 + g (1 - sig)),  du = da2 p s,  dprob = sum_i da2 s u
+ * da2          bf16 [rows, I].   prob: as in the forward.
+ * da1          bf16 [rows, 2I] out: [dg, du].
+ * dprob        fp32 [rows] out, or NULL.  Summed in a fixed order.
+ */
+int moe_swiglu_bwd(int64_t rows, int I, const uint16_t* da2, const uint16_t* a1,
+                   const uint8_t* a1_codes, const uint8_t* a1_scales, const float* prob,
+                   uint16_t* da1, float* dprob, hipStream_t stream);
 
 
 /*

@@ -9,8 +9,9 @@ device is not a gfx950.
 The functions carry the names of the C entry points (include/moe_mi355x.h):
 moe_route, moe_route_bwd, moe_router_fwd, moe_router_bwd, moe_permute,
 moe_unpermute, mxfp8_quantize, mxfp8_quantize_both, mxfp8_dequantize, grouped_mlp_fwd,
-grouped_mlp_bwd, grouped_linear_fwd, grouped_linear_bwd, moe_workspace_bytes,
-moe_workspace_region.
+grouped_mlp_bwd, grouped_mlp_fwd_ckpt, grouped_mlp_bwd_ckpt, grouped_linear_fwd,
+grouped_linear_bwd, moe_layernorm_fwd, moe_layernorm_bwd, moe_swiglu_fwd, moe_swiglu_bwd,
+moe_workspace_bytes, moe_workspace_region.
 """
 from __future__ import annotations
 
@@ -88,6 +89,11 @@ def lib() -> ctypes.CDLL:
             "moe_saved_bytes": (SZ, [I32, I32, I64, I32, I32, I32]),
             "moe_workspace_region": (I32, [I32, I32, I64, I32, I32, I32, I32,
                                            ctypes.POINTER(SZ), ctypes.POINTER(SZ)]),
+            "moe_layernorm_workspace_bytes": (SZ, [I64, I32]),
+            "moe_layernorm_fwd": (I32, [I32, I32, I64, I32, P, P, P, ctypes.c_float, P, P, P, P, P, P]),
+            "moe_layernorm_bwd": (I32, [I32, I32, I64, I32, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+            "moe_swiglu_fwd": (I32, [I64, I32, P, P, P, P, P, P]),
+            "moe_swiglu_bwd": (I32, [I64, I32, P, P, P, P, P, P, P, P]),
             "moe_trace_enable": (I32, [I32]),
             "moe_trace_filter": (None, [ctypes.c_char_p]),
             "moe_trace_disable": (None, []),
@@ -522,6 +528,158 @@ def grouped_linear_bwd(dy, x, split_sizes, w, precision=MOE_BF16, want_dx=True, 
                                     _ptr(workspace), workspace.numel(), _stream(dev)),
            "grouped_linear_bwd")
     return dx, dw
+
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}      # moe_type
+
+
+def _arg(t, name: str, dtype, shape, device) -> None:
+    """A tensor argument of this type (or one of these), shape and device, dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MoEError(f"{name} must be a device tensor")
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    if t.dtype not in dtypes:
+        raise MoEError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise MoEError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise MoEError(f"{name} must be contiguous")
+    if t.device != device:
+        raise MoEError(f"{name} is on {t.device}, not on {device}")
+
+
+def _first(t, name: str, dtype) -> tuple:
+    """The first tensor argument, a matrix: (rows, columns, device)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise MoEError(f"{name} must be a matrix")
+    _arg(t, name, dtype, t.shape, t.device)
+    return t.shape[0], t.shape[1], t.device
+
+
+def _checkpoint(rows: int, cols: int, device):
+    """(codes [rows, cols], scales [rows, cols/32]) of an 8-bit checkpoint."""
+    return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+            torch.empty((rows, cols // 32), dtype=torch.uint8, device=device))
+
+
+def _saved_pair(saved: dict, name: str, rows: int, cols: int, device):
+    """The checkpoint `name` of a saved dict, or (None, None)."""
+    codes, scales = saved.get(name + "_codes"), saved.get(name + "_scales")
+    if codes is None and scales is None:
+        return None, None
+    _arg(codes, name + "_codes", torch.uint8, (rows, cols), device)
+    _arg(scales, name + "_scales", torch.uint8, (rows, cols // 32), device)
+    return codes, scales
+
+
+def moe_layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, checkpoint: bool = False):
+    """Layer norm of the rows of x (bf16 or fp32 [T, H]); gamma and beta bf16
+    or fp32 [H], or None.  Returns (y bf16 [T, H], saved): saved holds mean and
+    rstd (fp32 [T]) and, with checkpoint, the normalized rows in 8 bits
+    (xhat_codes, xhat_scales); without it the backward needs x."""
+    T, H, dev = _first(x, "x", tuple(_TYPES))
+    for t, n in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _arg(t, n, tuple(_TYPES), (H,), dev)
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise MoEError("gamma and beta must have one type")
+    w = gamma if gamma is not None else beta
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    saved = {"mean": torch.empty(T, dtype=torch.float32, device=dev),
+             "rstd": torch.empty(T, dtype=torch.float32, device=dev)}
+    codes = scales = None
+    if checkpoint:
+        codes, scales = _checkpoint(T, H, dev)
+        saved["xhat_codes"], saved["xhat_scales"] = codes, scales
+    with torch.cuda.device(dev):
+        _check(lib().moe_layernorm_fwd(_TYPES[x.dtype], _TYPES[w.dtype] if w is not None else 1, T,
+                                       H, _ptr(x), _ptr(gamma), _ptr(beta), eps, _ptr(y),
+                                       _ptr(saved["mean"]), _ptr(saved["rstd"]), _ptr(codes),
+                                       _ptr(scales), _stream(dev)), "moe_layernorm_fwd")
+    return y, saved
+
+
+def moe_layernorm_bwd(dy, saved: dict, gamma=None, x=None, dres=None, dx_dtype=None,
+                      want_dgamma: bool = True, want_dbeta: bool = True, workspace=None):
+    """Returns (dx [T, H], dgamma [H] or None, dbeta [H] or None).  The
+    normalized rows come from saved's checkpoint when it has one, else from x.
+    dres: gradient added to dx (its type).  dx_dtype: type of dx, of x and
+    dres when they are given.  dgamma and dbeta have gamma's type (fp32
+    without gamma)."""
+    T, H, dev = _first(dy, "dy", torch.bfloat16)
+    codes, scales = _saved_pair(saved, "xhat", T, H, dev)
+    _arg(saved.get("rstd"), "rstd", torch.float32, (T,), dev)
+    mean = None
+    if codes is None:
+        if x is None:
+            raise MoEError("without a checkpoint x is needed")
+        _arg(x, "x", tuple(_TYPES), (T, H), dev)
+        mean = saved.get("mean")
+        _arg(mean, "mean", torch.float32, (T,), dev)
+    else:
+        x = None        # the checkpoint takes its place
+    if dx_dtype is None:
+        dx_dtype = next((t.dtype for t in (x, dres) if t is not None), torch.bfloat16)
+    if dx_dtype not in _TYPES or (x is not None and x.dtype != dx_dtype):
+        raise MoEError(f"dx_dtype must be x's, torch.bfloat16 or torch.float32, got {dx_dtype}")
+    if dres is not None:
+        _arg(dres, "dres", dx_dtype, (T, H), dev)
+    if gamma is not None:
+        _arg(gamma, "gamma", tuple(_TYPES), (H,), dev)
+    wt = gamma.dtype if gamma is not None else torch.float32
+    dx = torch.empty((T, H), dtype=dx_dtype, device=dev)
+    dgamma = torch.empty(H, dtype=wt, device=dev) if want_dgamma else None
+    dbeta = torch.empty(H, dtype=wt, device=dev) if want_dbeta else None
+    with torch.cuda.device(dev):
+        if workspace is None and (want_dgamma or want_dbeta):
+            workspace = _workspace(int(lib().moe_layernorm_workspace_bytes(T, H)), dev)
+        _check(lib().moe_layernorm_bwd(_TYPES[dx_dtype], _TYPES[wt], T, H, _ptr(dy), _ptr(x),
+                                       _ptr(mean), _ptr(saved["rstd"]), _ptr(codes), _ptr(scales),
+                                       _ptr(gamma), _ptr(dres), _ptr(dx), _ptr(dgamma),
+                                       _ptr(dbeta), _ptr(workspace),
+                                       0 if workspace is None else workspace.numel(),
+                                       _stream(dev)), "moe_layernorm_bwd")
+    return dx, dgamma, dbeta
+
+
+def moe_swiglu_fwd(a1, prob=None, checkpoint: bool = False):
+    """a2 = prob silu(gate) up of a1 = [gate, up] (bf16 [rows, 2I]); prob fp32
+    [rows] or None.  Returns (a2 bf16 [rows, I], saved): saved holds a1 itself
+    or, with checkpoint, a1 in 8 bits (a1_codes, a1_scales)."""
+    rows, cols, dev = _first(a1, "a1", torch.bfloat16)
+    if cols % 2:
+        raise MoEError("a1 must have an even number of columns")
+    if prob is not None:
+        _arg(prob, "prob", torch.float32, (rows,), dev)
+    a2 = torch.empty((rows, cols // 2), dtype=torch.bfloat16, device=dev)
+    codes = scales = None
+    if checkpoint:
+        codes, scales = _checkpoint(rows, cols, dev)
+    with torch.cuda.device(dev):
+        _check(lib().moe_swiglu_fwd(rows, cols // 2, _ptr(a1), _ptr(prob), _ptr(a2), _ptr(codes),
+                                    _ptr(scales), _stream(dev)), "moe_swiglu_fwd")
+    return a2, ({"a1_codes": codes, "a1_scales": scales} if checkpoint else {"a1": a1})
+
+
+def moe_swiglu_bwd(da2, saved: dict, prob=None):
+    """Returns (da1 bf16 [rows, 2I], dprob fp32 [rows] or None without prob),
+    from saved's checkpoint of a1 when it has one, else from its a1."""
+    rows, I, dev = _first(da2, "da2", torch.bfloat16)
+    codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
+    a1 = None
+    if codes is None:
+        a1 = saved.get("a1")
+        _arg(a1, "a1", torch.bfloat16, (rows, 2 * I), dev)
+    dprob = None
+    if prob is not None:
+        _arg(prob, "prob", torch.float32, (rows,), dev)
+        dprob = torch.empty(rows, dtype=torch.float32, device=dev)
+    da1 = torch.empty((rows, 2 * I), dtype=torch.bfloat16, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().moe_swiglu_bwd(rows, I, _ptr(da2), _ptr(a1), _ptr(codes), _ptr(scales),
+                                    _ptr(prob), _ptr(da1), _ptr(dprob), _stream(dev)),
+               "moe_swiglu_bwd")
+    return da1, dprob
 
 
 def trace_enable(capacity: int) -> None:

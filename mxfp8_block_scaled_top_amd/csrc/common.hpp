@@ -110,6 +110,45 @@ __device__ __forceinline__ float mx_decode(uint32_t code, uint32_t S) {
     return (code & 0x80u) ? -v : v;
 }
 
+// Largest of the four lanes 4q..4q+3 (quad permutes; no LDS).
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xf, 0xf, true)));
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xf, 0xf, true)));
+}
+
+// MXFP8 of 8 neighbouring values per lane: the four lanes 4q..4q+3 hold a
+// block of 32 (all four active or none).  Each stores its 8 codes; the first
+// stores the scale byte.
+__device__ __forceinline__ void mx_store8(const float (&x)[8], uint8_t* codes, uint8_t* scale) {
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, __builtin_fabsf(x[k]));
+    const uint32_t S = mx_scale_byte(quad_max(m));
+    const u32x2 w = {mx_encode4(x[0], x[1], x[2], x[3], S), mx_encode4(x[4], x[5], x[6], x[7], S)};
+    __builtin_nontemporal_store(w, (u32x2*)codes);
+    if ((threadIdx.x & 3) == 0) *scale = (uint8_t)S;
+}
+
+// The values of 8 neighbouring codes of one block.
+__device__ __forceinline__ void mx_decode8(u32x2 w, uint32_t S, float (&x)[8]) {
+    const float scale = __builtin_ldexpf(1.f, (int)S - 127);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], scale, false);
+        const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], scale, true);
+        x[4 * h] = a[0];
+        x[4 * h + 1] = a[1];
+        x[4 * h + 2] = b[0];
+        x[4 * h + 3] = b[1];
+    }
+}
+
+__device__ __forceinline__ void mx_load8(const uint8_t* codes, const uint8_t* scale,
+                                         float (&x)[8]) {
+    const u32x2 w = __builtin_nontemporal_load((const u32x2*)codes);
+    mx_decode8(w, *scale, x);
+}
+
 // Row-pair layout of the 8-bit GEMM operands: rows 2p and 2p+1 of a matrix
 // with K bytes per row share 128-byte lines, one line per 64 K-bytes, so that
 // one K step (64 bytes) of a tile's row pair is one whole line:

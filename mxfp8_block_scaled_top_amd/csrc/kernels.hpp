@@ -105,4 +105,23 @@ hipError_t launch_dequant_cols(const uint8_t* codes, const uint8_t* scales, cons
                                int ngroups, int64_t rows, int64_t cols, bf16_t* out,
                                hipStream_t s);
 
+// ---- layer norm, ScaledSwiGLU
+// xh as MXFP8 rows (codes [T, H], scales [T, H/32]) when codes is given.
+constexpr int kMaxNormH = 32768;
+constexpr int kMaxSwigluI = 1 << 20;
+size_t layernorm_workspace_bytes(int64_t T, int H);
+hipError_t launch_layernorm_fwd(const void* x, bool x_f32, int64_t T, int H, const void* gamma,
+                                const void* beta, bool w_f32, float eps, bf16_t* y, float* mean,
+                                float* rstd, uint8_t* codes, uint8_t* scales, hipStream_t s);
+// xh from codes and scales when given, else from x, mean and rstd.
+hipError_t launch_layernorm_bwd(const bf16_t* dy, const void* x, bool x_f32, const float* mean,
+                                const float* rstd, const uint8_t* codes, const uint8_t* scales,
+                                int64_t T, int H, const void* gamma, bool w_f32, const void* dres,
+                                void* dx, void* dgamma, void* dbeta, void* ws, hipStream_t s);
+hipError_t launch_swiglu_fwd(const bf16_t* a1, const float* prob, int64_t rows, int I, bf16_t* a2,
+                             uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_swiglu_bwd(const bf16_t* da2, const bf16_t* a1, const uint8_t* codes,
+                             const uint8_t* scales, const float* prob, int64_t rows, int I,
+                             bf16_t* da1, float* dprob, hipStream_t s);
+
 }  // namespace moe
