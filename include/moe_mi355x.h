@@ -530,6 +530,48 @@ int grouped_mlp_bwd_gather(int precision, int E, int H, int I, int64_t rows, con
                            hipStream_t stream);
 
 /*
+ * grouped_mlp_fwd_ckpt -- grouped_mlp_fwd (src_token NULL) or
+ * grouped_mlp_fwd_gather (src_token given; MOE_BF16: MOE_ERR_ARG) with the
+ * gate_up output A1, the largest saved tensor, kept in 8 bits.
+ * [BioNeMo, "MXFP8与融合MLP": the fused operators quantize in the epilogue, so
+ *  that no intermediate goes to memory in a wider format than its reader
+ *  needs.]
+ *
+ * a1_codes     uint8 [rows, 2I] out and
+ * a1_scales    uint8 [rows, 2I/32] out (both 16-byte aligned): MXFP8 of the
+ *              fp32 A1 in the layout and by the rule of mxfp8_quantize axis=1,
+ *              33/32 bytes a value in place of saved->a1's 2.
+ * saved        as in grouped_mlp_fwd; saved->a1 is neither read nor written
+ *              and may be NULL.
+ * yp and the other saved tensors are bit for bit those of grouped_mlp_fwd.
+ */
+int grouped_mlp_fwd_ckpt(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp,
+                         const int32_t* src_token, const int32_t* split_sizes,
+                         const uint16_t* const* w_gate_up, const uint16_t* const* w_down,
+                         const float* prob_perm, uint16_t* yp, const moe_saved* saved,
+                         uint8_t* a1_codes, uint8_t* a1_scales, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * grouped_mlp_bwd_ckpt -- grouped_mlp_bwd (src_token NULL) or
+ * grouped_mlp_bwd_gather (src_token given) from the 8-bit A1: g and u are the
+ * values that the codes stand for, decoded in the GEMM's epilogue.
+ * [The same passage.]
+ *
+ * a1_codes, a1_scales   as grouped_mlp_fwd_ckpt wrote them.
+ * Results are bit for bit those of grouped_mlp_bwd on a saved->a1 that holds
+ * the decoded values (which bf16 represents).  A2 is not recomputed: dW_down
+ * does not depend on the 8-bit A1.
+ */
+int grouped_mlp_bwd_ckpt(int precision, int E, int H, int I, int64_t rows, const uint16_t* dyp,
+                         const int32_t* src_token, const uint16_t* xp, const int32_t* split_sizes,
+                         const uint16_t* const* w_gate_up, const uint16_t* const* w_down,
+                         const float* prob_perm, const moe_saved* saved, const uint8_t* a1_codes,
+                         const uint8_t* a1_scales, uint16_t* dxp, uint16_t* const* dw_gate_up,
+                         uint16_t* const* dw_down, float* dprob_perm, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Workspace bytes for op (MOE_OP_ROUTE: T, E, k used; MLP ops: rows = T*k,
  * H, I, E, precision used).  Returns 0 for an invalid op.
  */

@@ -84,6 +84,10 @@ def lib() -> ctypes.CDLL:
                                              ctypes.POINTER(_Saved), P, SZ, P]),
             "grouped_mlp_bwd_gather": (I32, [I32, I32, I32, I32, I64, P, P, P, P, P, P,
                                              ctypes.POINTER(_Saved), P, P, P, P, P, SZ, P]),
+            "grouped_mlp_fwd_ckpt": (I32, [I32, I32, I32, I32, I64, P, P, P, P, P, P, P,
+                                           ctypes.POINTER(_Saved), P, P, P, SZ, P]),
+            "grouped_mlp_bwd_ckpt": (I32, [I32, I32, I32, I32, I64, P, P, P, P, P, P, P,
+                                           ctypes.POINTER(_Saved), P, P, P, P, P, P, P, SZ, P]),
             "grouped_linear_fwd": (I32, [I32, I32, I32, I32, I64, P, P, P, P, P, SZ, P]),
             "grouped_linear_bwd": (I32, [I32, I32, I32, I32, I64, P, P, P, P, P, P, P, SZ, P]),
             "moe_saved_bytes": (SZ, [I32, I32, I64, I32, I32, I32]),
@@ -366,13 +370,17 @@ def _ptr_array(ts):
 
 
 def alloc_saved(rows: int, H: int, I: int, E: int, precision: int, device,
-                weight_cols: bool = True) -> dict:
+                weight_cols: bool = True, checkpoint: bool = False) -> dict:
     """Caller-owned tensors the forward saves for the backward, sized by
     moe_saved_bytes.  weight_cols (MXFP8/FP8): also the buffers for the
     weights' columnwise copies, so that the forward quantizes each weight once
-    for both passes."""
+    for both passes.  checkpoint: A1 in 8 bits (a1_codes, a1_scales) in place
+    of a1, for grouped_mlp_fwd_ckpt."""
     L = lib()
-    s = {"a1": torch.empty((rows, 2 * I), dtype=torch.bfloat16, device=device)}
+    if checkpoint:
+        s = dict(zip(("a1_codes", "a1_scales"), _checkpoint(rows, 2 * I, device)))
+    else:
+        s = {"a1": torch.empty((rows, 2 * I), dtype=torch.bfloat16, device=device)}
     if precision == MOE_BF16:
         s["a2"] = torch.empty((rows, I), dtype=torch.bfloat16, device=device)
         return s
@@ -386,6 +394,80 @@ def alloc_saved(rows: int, H: int, I: int, E: int, precision: int, device,
 
 def _saved_struct(s: dict) -> _Saved:
     return _Saved(*[_ptr(s.get(n)) for n, _ in _Saved._fields_])
+
+
+def grouped_mlp_fwd_ckpt(xp, split_sizes, w_gate_up, w_down, prob_perm, precision=MOE_MXFP8,
+                         saved=None, workspace=None, src_token=None):
+    """grouped_mlp_fwd (with src_token: grouped_mlp_fwd_gather) that keeps A1
+    in 8 bits: saved holds a1_codes and a1_scales (alloc_saved(...,
+    checkpoint=True)) in place of a1.  Returns (yp, saved)."""
+    _dev(xp, torch.bfloat16, "xp")
+    rows, H = xp.shape
+    if src_token is not None:
+        _dev(src_token, torch.int32, "src_token")
+        rows = src_token.numel()
+    E = len(w_gate_up)
+    I = w_down[0].shape[1]
+    dev = xp.device
+    if saved is None:
+        saved = alloc_saved(rows, H, I, E, precision, dev, checkpoint=True)
+    codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
+    if codes is None:
+        raise MoEError("saved has no a1_codes: use alloc_saved(..., checkpoint=True)")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = _workspace(moe_workspace_bytes(MOE_OP_MLP_FWD, rows, H, I, E, 1, precision), dev)
+        yp = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
+        w1, w2 = _ptr_array(w_gate_up), _ptr_array(w_down)
+        st = _saved_struct(saved)
+        _check(lib().grouped_mlp_fwd_ckpt(precision, E, H, I, rows, _ptr(xp), _ptr(src_token),
+                                          _ptr(split_sizes), ctypes.cast(w1, ctypes.c_void_p),
+                                          ctypes.cast(w2, ctypes.c_void_p), _ptr(prob_perm),
+                                          _ptr(yp), ctypes.byref(st), _ptr(codes), _ptr(scales),
+                                          _ptr(workspace), workspace.numel(), _stream(dev)),
+               "grouped_mlp_fwd_ckpt")
+    return yp, saved
+
+
+def grouped_mlp_bwd_ckpt(dyp, xp, split_sizes, w_gate_up, w_down, prob_perm, saved,
+                         precision=MOE_MXFP8, workspace=None, dw_gate_up=None, dw_down=None,
+                         src_token=None):
+    """grouped_mlp_bwd (with src_token: grouped_mlp_bwd_gather, dyp the
+    per-token gradient) from the 8-bit A1 of grouped_mlp_fwd_ckpt.  Returns
+    (dxp, dw_gate_up list, dw_down list, dprob_perm)."""
+    _dev(dyp, torch.bfloat16, "dyp")
+    rows, H = dyp.shape
+    if src_token is not None:
+        _dev(src_token, torch.int32, "src_token")
+        rows = src_token.numel()
+    E = len(w_gate_up)
+    I = w_down[0].shape[1]
+    dev = dyp.device
+    codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
+    if codes is None:
+        raise MoEError("saved has no a1_codes (grouped_mlp_fwd_ckpt)")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = _workspace(moe_workspace_bytes(MOE_OP_MLP_BWD, rows, H, I, E, 1, precision), dev)
+        dxp = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
+        if dw_gate_up is None:
+            dw_gate_up = [torch.empty((2 * I, H), dtype=torch.bfloat16, device=dev) for _ in range(E)]
+        if dw_down is None:
+            dw_down = [torch.empty((H, I), dtype=torch.bfloat16, device=dev) for _ in range(E)]
+        dpp = torch.empty(rows, dtype=torch.float32, device=dev)
+        w1, w2 = _ptr_array(w_gate_up), _ptr_array(w_down)
+        d1, d2 = _ptr_array(dw_gate_up), _ptr_array(dw_down)
+        st = _saved_struct(saved)
+        _check(lib().grouped_mlp_bwd_ckpt(precision, E, H, I, rows, _ptr(dyp), _ptr(src_token),
+                                          _ptr(xp), _ptr(split_sizes),
+                                          ctypes.cast(w1, ctypes.c_void_p),
+                                          ctypes.cast(w2, ctypes.c_void_p), _ptr(prob_perm),
+                                          ctypes.byref(st), _ptr(codes), _ptr(scales), _ptr(dxp),
+                                          ctypes.cast(d1, ctypes.c_void_p),
+                                          ctypes.cast(d2, ctypes.c_void_p), _ptr(dpp),
+                                          _ptr(workspace), workspace.numel(), _stream(dev)),
+               "grouped_mlp_bwd_ckpt")
+    return dxp, dw_gate_up, dw_down, dpp
 
 
 def grouped_mlp_fwd_gather(x, src_token, split_sizes, w_gate_up, w_down, prob_perm,

@@ -532,7 +532,12 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {
     return max(m, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
 }
 
-template <int DT>
+// kCk: A1 leaves as MXFP8 rows (codes [rows, 2I], scales [rows, 2I/32]) instead
+// of bf16, from the fp32 values that the activation reads anyway: the lane
+// that has 32 gate and 32 up values of a row encodes both blocks.  33/32 bytes
+// a value instead of 2, and no second read of the staged values; ordinary
+// stores, since a wave's 64-byte row pieces meet their neighbours' in L2.
+template <int DT, bool kCk>
 __device__ __forceinline__ void swiglu_fwd_rows(const EpiCtx& c, float* R, const f32x16& f0,
                                                 const f32x16& f1, const f32x16& f2,
                                                 const f32x16& f3, int fi, uint32_t& amx) {
@@ -544,7 +549,7 @@ __device__ __forceinline__ void swiglu_fwd_rows(const EpiCtx& c, float* R, const
     wave_lds_sync();
     const int frow0 = tl.m0 + c.wm * 128 + fi * 32;      // row inside the expert
     const int valid = min(32, tl.rows_e - frow0);          // rows of this slice that exist
-    {
+    if constexpr (!kCk) {
         // A1, gate and up of the wave's 64 j: 8 lanes write one row's
         // 128-byte line, 8 rows per instruction, streamed past L2 (whole
         // lines, read again only by the backward)
@@ -571,13 +576,34 @@ __device__ __forceinline__ void swiglu_fwd_rows(const EpiCtx& c, float* R, const
         if (row < valid) {
             const int64_t gr = tl.row0 + frow0 + row;
             const float p = c.pr[fi];
+            float gq[32], uq[32];                    // the row's blocks of A1 (kCk)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 float gt[8], up[8];
                 load_row8(R, row, 64 * q + 8 * b, gt);
                 load_row8(R, row, 64 * q + 32 + 8 * b, up);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a2[8 * b + i] = p * silu_f(gt[i]) * up[i];
+                for (int i = 0; i < 8; ++i) {
+                    a2[8 * b + i] = p * silu_f(gt[i]) * up[i];
+                    if constexpr (kCk) {
+                        gq[8 * b + i] = gt[i];
+                        uq[8 * b + i] = up[i];
+                    }
+                }
+            }
+            if constexpr (kCk) {
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {
+                    u32x4 c0, c1;
+                    const uint32_t S = quant32(s2 ? uq : gq, c0, c1);
+                    const int64_t at = gr * 2 * I + (s2 ? I : 0) + j0;
+                    u32x4* o = (u32x4*)(g.a1_codes + at);
+                    o[0] = c0;
+                    o[1] = c1;
+                    // the row's other block is the neighbouring lane's (q = 1)
+                    const uint32_t S1 = (uint32_t)__builtin_amdgcn_mov_dpp((int)S, 0xB1, 0xf, 0xf, true);
+                    if (q == 0) *(uint16_t*)(g.a1_scales + at / 32) = (uint16_t)(S | (S1 << 8));
+                }
             }
             if (DT != DT_MX) {          // bf16 A2 (BF16, and FP8: cast later)
                 u32x4* o = (u32x4*)(g.act + gr * I + j0);
@@ -628,6 +654,41 @@ __device__ __forceinline__ void swiglu_fwd_rows(const EpiCtx& c, float* R, const
 // (float4 accesses throughout, like the du stores that later reuse the
 // slots, so the compiler keeps their order.)
 struct A1Words { u32x4 g[4][2], u[4][2]; };
+// The 8-bit form: 16 codes of gate and of up per row (8 lanes per 128-byte
+// line) and the 4 scale bytes of the row's 128 columns.
+struct A1Codes { u32x4 g[4], u[4]; uint32_t sg[4], su[4]; };
+
+// A buffer resource at a uniform address.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* p, int nbytes) {
+    const uint64_t a = (uint64_t)p;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)hi << 32) | lo), (short)0,
+                                             __builtin_amdgcn_readfirstlane(nbytes), 0x00020000);
+}
+
+__device__ __forceinline__ void load_a1(const GemmArgs& g, const Tile& tl, int wm, int wn, int fi,
+                                        int lane, A1Codes& w) {
+    const int I = g.I;
+    const int frow0 = tl.m0 + wm * 128 + fi * 32;
+    const int valid = max(0, min(32, tl.rows_e - frow0));
+    const int jw = tl.n0 + wn * 128;
+    const int live = jw < I ? valid : 0;
+    const int64_t row0 = tl.row0 + frow0;
+    const int rowb = 2 * I, rows_ = I / 16;            // code and scale bytes per row
+    const __amdgpu_buffer_rsrc_t rc = uniform_rsrc(g.a1_codes + row0 * rowb, live * rowb);
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(g.a1_scales + row0 * rows_, live * rows_);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (lane >> 3) + 8 * i;
+        const int o = row * rowb + jw + 16 * (lane & 7);
+        w.g[i] = __builtin_amdgcn_raw_buffer_load_b128(rc, o, 0, 2);   // nt
+        w.u[i] = __builtin_amdgcn_raw_buffer_load_b128(rc, o + I, 0, 2);
+        const int os = row * rows_ + jw / 32;
+        w.sg[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, os, 0, 0);
+        w.su[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, os + I / 32, 0, 0);
+    }
+}
 
 __device__ __forceinline__ void load_a1(const GemmArgs& g, const Tile& tl, int wm, int wn, int fi,
                                         int lane, A1Words& w) {
@@ -680,6 +741,39 @@ __device__ __forceinline__ void stage_a1_pairs(float* R2, const A1Words& w, int 
         }
 }
 
+// bf16 pairs of 4 codes times their block's scale (exact: a code has 4
+// significant bits)
+__device__ __forceinline__ u32x2 codes_bf16(uint32_t w, float scale) {
+    return (u32x2){
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true))};
+}
+
+__device__ __forceinline__ void stage_a1_pairs(float* R2, const A1Codes& w, int lane) {
+    const int c16 = lane & 7, sh = (c16 >> 1) * 8;         // 2 lanes per block of 32
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (lane >> 3) + 8 * i;
+        const float sg = __builtin_ldexpf(1.f, (int)((w.sg[i] >> sh) & 0xffu) - 127);
+        const float su = __builtin_ldexpf(1.f, (int)((w.su[i] >> sh) & 0xffu) - 127);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float x[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x2 gw = codes_bf16(w.g[i][2 * s + h], sg);
+                const u32x2 uw = codes_bf16(w.u[i][2 * s + h], su);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    x[4 * h + 2 * k] = __uint_as_float((gw[k] & 0xffffu) | (uw[k] << 16));
+                    x[4 * h + 2 * k + 1] = __uint_as_float((gw[k] >> 16) | (uw[k] & 0xffff0000u));
+                }
+            }
+            store_row8(R2, row, 16 * c16 + 8 * s, x);
+        }
+    }
+}
+
 // (gate, up) of staged pair x
 __device__ __forceinline__ float pair_gate(float x) { return lo_bf16(__float_as_uint(x)); }
 __device__ __forceinline__ float pair_up(float x) { return hi_bf16(__float_as_uint(x)); }
@@ -687,11 +781,12 @@ __device__ __forceinline__ float pair_up(float x) { return hi_bf16(__float_as_ui
 // SwiGLU backward of row slice fi: staged columns are dA2 for j = n0 + wn*128
 // + col.  Writes dA1 (bf16, or rowwise + columnwise MXFP8) and the row's
 // probability-gradient partial over these 128 columns into red.
-template <int DT>
+// The saved A1 comes as bf16 (A1Words) or as MXFP8 codes (A1Codes).
+template <int DT, class Saved>
 __device__ __forceinline__ void swiglu_bwd_rows(const EpiCtx& c, float* R, float* R2,
                                                 float* red, const f32x16& f0, const f32x16& f1,
                                                 const f32x16& f2, const f32x16& f3, int fi,
-                                                uint32_t& amx, A1Words& w) {
+                                                uint32_t& amx, Saved& w) {
     const GemmArgs& g = c.g;
     const Tile& tl = c.tl;
     const int lane = c.lane;
@@ -866,7 +961,7 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     const int G8 = gridDim.x >> 3;
     const int t = (blockIdx.x & 7) * G8 + (blockIdx.x >> 3);
 
-    constexpr bool kAmax = DT == DT_FP8 && (EPI == EPI_SWIGLU_FWD || EPI == EPI_SWIGLU_BWD);
+    constexpr bool kAmax = DT == DT_FP8 && (epi_fwd(EPI) || epi_bwd(EPI));
     Tile tl;
     if (!decode_tile<GRP>(g, ntn, mtm, t, sched, tl)) {
         if (kAmax && tid == 0) g.amax_part[blockIdx.x] = 0;
@@ -904,9 +999,9 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
             kb.base = (const uint8_t*)g.b.p[tl.e];
             kb.stride = kP2 ? p2_stride(g.K) : g.ldb * kElemB;
             kb.row_first = tl.n0;
-            kb.rows_valid = EPI == EPI_SWIGLU_FWD ? 2 * g.I : g.N;
+            kb.rows_valid = epi_fwd(EPI) ? 2 * g.I : g.N;
             kb.kbytes = g.K * kElemB;
-            kb.pair_I = EPI == EPI_SWIGLU_FWD ? g.I : 0;
+            kb.pair_I = epi_fwd(EPI) ? g.I : 0;
             kb.j0 = tl.n_tile * (kGemmBN / 2);
         } else {
             mb.base = (const uint8_t*)g.b.p[tl.e] + (int64_t)tl.n0 * 2;
@@ -1236,10 +1331,10 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     // the routing probability of the lane's row in each 32-row slice, loaded
     // once for the whole epilogue (rows past the expert are never used)
     const int ln = lane_after_loop();
-    A1Words a1w;
-    if (EPI == EPI_SWIGLU_BWD) load_a1(g, tl, wm, wn, 3, ln, a1w);   // the first slice's saved A1
+    std::conditional_t<epi_ck(EPI), A1Codes, A1Words> a1w;
+    if (epi_bwd(EPI)) load_a1(g, tl, wm, wn, 3, ln, a1w);   // the first slice's saved A1
     float pr[4] = {0.f, 0.f, 0.f, 0.f};
-    if (EPI == EPI_SWIGLU_FWD || EPI == EPI_SWIGLU_BWD) {
+    if (epi_fwd(EPI) || epi_bwd(EPI)) {
 #pragma unroll
         for (int fi = 0; fi < 4; ++fi) {
             const int frow = tl.m0 + wm * 128 + fi * 32 + (ln >> 1);
@@ -1247,21 +1342,21 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
         }
     }
 
-    if (EPI == EPI_SWIGLU_FWD) {
+    if (epi_fwd(EPI)) {
         EpiCtx c{g, tl, wm, wn, ntn, {pr[0], pr[1], pr[2], pr[3]}, ln};
         float* R = (float*)(wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3);
         uint32_t amx = 0;
         // (slices in reverse order, as in the plain-store epilogue: no
         // accumulator fragment is parked in scratch memory)
-        swiglu_fwd_rows<DT>(c, R, acc[3][0], acc[3][1], acc[3][2], acc[3][3], 3, amx);
-        swiglu_fwd_rows<DT>(c, R, acc[2][0], acc[2][1], acc[2][2], acc[2][3], 2, amx);
-        swiglu_fwd_rows<DT>(c, R, acc[1][0], acc[1][1], acc[1][2], acc[1][3], 1, amx);
-        swiglu_fwd_rows<DT>(c, R, acc[0][0], acc[0][1], acc[0][2], acc[0][3], 0, amx);
+        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc[3][0], acc[3][1], acc[3][2], acc[3][3], 3, amx);
+        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc[2][0], acc[2][1], acc[2][2], acc[2][3], 2, amx);
+        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc[1][0], acc[1][1], acc[1][2], acc[1][3], 1, amx);
+        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc[0][0], acc[0][1], acc[0][2], acc[0][3], 0, amx);
         if (kAmax) amax_to_part(amx, (uint32_t*)sched, g.amax_part);
         return;
     }
 
-    if (EPI == EPI_SWIGLU_BWD) {
+    if (epi_bwd(EPI)) {
         EpiCtx c{g, tl, wm, wn, ntn, {pr[0], pr[1], pr[2], pr[3]}, ln};
         float* R = (float*)(wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3);
         float* R2 = R + 32 * 128;
@@ -1292,8 +1387,8 @@ __global__ void dprob_reduce_kernel(const float* __restrict__ part, int64_t rows
 
 // ---------------------------------------------------------------- launcher
 int gemm_n_tiles(int epi, int N, int I) {
-    if (epi == EPI_SWIGLU_FWD) return I / (kGemmBN / 2);
-    if (epi == EPI_SWIGLU_BWD) return (I + kGemmBN - 1) / kGemmBN;
+    if (epi_fwd(epi)) return I / (kGemmBN / 2);
+    if (epi_bwd(epi)) return (I + kGemmBN - 1) / kGemmBN;
     return (N + kGemmBN - 1) / kGemmBN;
 }
 
@@ -1332,6 +1427,14 @@ hipError_t launch_gemm(int dtype, int use, const GemmArgs& g, hipStream_t s) {
     if (dtype == DT_FP8 && use != U_GATEUP_FWD && use != U_DOWN_DGRAD) dtype = DT_MX;
 #define MOE_GEMM_CASE(DT, USE, LA, LB, GRP, EPI) \
     if (dtype == DT && use == USE) return run<DT, LA, LB, GRP, EPI, USE>(g, s);
+    if (g.a1_codes) {   // A1 as MXFP8 rows
+        MOE_GEMM_CASE(DT_BF16, U_GATEUP_FWD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_FWD_CK)
+        MOE_GEMM_CASE(DT_BF16, U_DOWN_DGRAD, L_KMAJ, L_MNMAJ, G_M, EPI_SWIGLU_BWD_CK)
+        MOE_GEMM_CASE(DT_MX, U_GATEUP_FWD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_FWD_CK)
+        MOE_GEMM_CASE(DT_MX, U_DOWN_DGRAD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_BWD_CK)
+        MOE_GEMM_CASE(DT_FP8, U_GATEUP_FWD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_FWD_CK)
+        MOE_GEMM_CASE(DT_FP8, U_DOWN_DGRAD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_BWD_CK)
+    }
     // bf16: the backward reads W1, W2 and both weight-gradient operands in
     // their natural (M/N-contiguous) layout
     MOE_GEMM_CASE(DT_BF16, U_GATEUP_FWD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_FWD)

@@ -287,27 +287,52 @@ size_t moe_saved_bytes(int precision, int member, int64_t rows, int H, int I, in
 
 namespace {
 
+// A1 kept as MXFP8 rows in place of saved->a1 (grouped_mlp_*_ckpt), or nothing.
+struct A1Ckpt {
+    uint8_t* codes = nullptr;
+    uint8_t* scales = nullptr;
+    bool used = false;
+};
+
+// What the saved A1 has to be for `rows` > 0 rows.
+int check_a1(const moe_saved* s, const A1Ckpt& ck) {
+    if (!ck.used) return s->a1 ? MOE_OK : MOE_ERR_NULL;
+    return ck.codes && ck.scales ? MOE_OK : MOE_ERR_NULL;
+}
+
+void set_a1(GemmArgs& g, const moe_saved* s, const A1Ckpt& ck) {
+    if (ck.used) {
+        g.a1_codes = ck.codes;
+        g.a1_scales = ck.scales;
+    } else {
+        g.a1 = s->a1;
+    }
+}
+
 // The forward of grouped_mlp_fwd (gather == NULL: xp holds the grouped rows)
 // and of grouped_mlp_fwd_gather (grouped row r is row gather[r] of xp; 8-bit
 // modes only, where xp is read only by the quantizer).
 int mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp,
             const int32_t* gather, const int32_t* split_sizes, const uint16_t* const* w_gate_up,
             const uint16_t* const* w_down, const float* prob_perm, uint16_t* yp,
-            const moe_saved* saved, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+            const moe_saved* saved, const A1Ckpt& ck, void* workspace, size_t workspace_bytes,
+            hipStream_t stream) {
     int st = check_common(precision, E, H, I, rows);
     if (st != MOE_OK) return st;
     if (!split_sizes || !w_gate_up || !w_down || !saved || !workspace) return MOE_ERR_NULL;
     for (int e = 0; e < E; ++e)
         if (!w_gate_up[e] || !w_down[e]) return MOE_ERR_NULL;
     if (rows > 0) {
-        if (!xp || !prob_perm || !yp || !saved->a1) return MOE_ERR_NULL;
+        if (!xp || !prob_perm || !yp) return MOE_ERR_NULL;
+        if ((st = check_a1(saved, ck)) != MOE_OK) return st;
         if (precision == MOE_BF16 && !saved->a2) return MOE_ERR_NULL;
         if (precision != MOE_BF16 && (!saved->a2_col_codes || !saved->a2_col_scales ||
                                       !saved->xp_col_codes || !saved->xp_col_scales))
             return MOE_ERR_NULL;
     }
     if ((st = check_weight_cols(saved)) != MOE_OK) return st;
-    if (!aligned16(xp) || !aligned16(yp) || !aligned16(saved->a1) || !aligned16(saved->a2))
+    if (!aligned16(xp) || !aligned16(yp) || (!ck.used && !aligned16(saved->a1)) ||
+        !aligned16(saved->a2) || !aligned16(ck.codes) || !aligned16(ck.scales))
         return MOE_ERR_ALIGN;
     for (int e = 0; e < E; ++e)
         if (!aligned16(w_gate_up[e]) || !aligned16(w_down[e])) return MOE_ERR_ALIGN;
@@ -331,7 +356,7 @@ int mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp
         g.ldb = H;
         g.N = 2 * I;
         g.K = H;
-        g.a1 = saved->a1;
+        set_a1(g, saved, ck);
         g.act = saved->a2;
         g.name = "gemm_bf16_gateup_fwd_swiglu";
         MOE_TRY(launch_gemm(DT_BF16, U_GATEUP_FWD, g, stream));
@@ -411,7 +436,7 @@ int mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp
     g.ldb_s = H / 32;
     g.N = 2 * I;
     g.K = H;
-    g.a1 = saved->a1;
+    set_a1(g, saved, ck);
     if (fp8) {
         g.act = (bf16_t*)w.a2bf;
         g.amax_part = w.a2_part;
@@ -465,7 +490,7 @@ int mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp
 int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dyp,
             const int32_t* gather, const uint16_t* xp, const int32_t* split_sizes,
             const uint16_t* const* w_gate_up, const uint16_t* const* w_down,
-            const float* prob_perm, const moe_saved* saved, uint16_t* dxp,
+            const float* prob_perm, const moe_saved* saved, const A1Ckpt& ck, uint16_t* dxp,
             uint16_t* const* dw_gate_up, uint16_t* const* dw_down, float* dprob_perm,
             void* workspace, size_t workspace_bytes, hipStream_t stream) {
     int st = check_common(precision, E, H, I, rows);
@@ -476,7 +501,8 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
     for (int e = 0; e < E; ++e)
         if (!w_gate_up[e] || !w_down[e] || !dw_gate_up[e] || !dw_down[e]) return MOE_ERR_NULL;
     if (rows > 0) {
-        if (!dyp || !prob_perm || !dxp || !dprob_perm || !saved->a1) return MOE_ERR_NULL;
+        if (!dyp || !prob_perm || !dxp || !dprob_perm) return MOE_ERR_NULL;
+        if ((st = check_a1(saved, ck)) != MOE_OK) return st;
         if (precision == MOE_BF16 && !xp) return MOE_ERR_NULL;
         if (precision == MOE_BF16 && !saved->a2) return MOE_ERR_NULL;
         if (precision != MOE_BF16 && (!saved->a2_col_codes || !saved->a2_col_scales ||
@@ -484,8 +510,9 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             return MOE_ERR_NULL;
     }
     if ((st = check_weight_cols(saved)) != MOE_OK) return st;
-    if (!aligned16(dyp) || !aligned16(xp) || !aligned16(dxp) || !aligned16(saved->a1) ||
-        !aligned16(saved->a2))
+    if (!aligned16(dyp) || !aligned16(xp) || !aligned16(dxp) ||
+        (!ck.used && !aligned16(saved->a1)) || !aligned16(saved->a2) || !aligned16(ck.codes) ||
+        !aligned16(ck.scales))
         return MOE_ERR_ALIGN;
     for (int e = 0; e < E; ++e)
         if (!aligned16(w_gate_up[e]) || !aligned16(w_down[e]) || !aligned16(dw_gate_up[e]) ||
@@ -520,7 +547,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             g.ldb = I;            // W2 [H, I] read as [K = H, N = I]
             g.N = I;
             g.K = H;
-            g.a1 = saved->a1;
+            set_a1(g, saved, ck);
             g.act = (bf16_t*)w.da1;
             g.dprob_part = w.part;
             g.name = "gemm_bf16_down_dgrad_swiglu_bwd";
@@ -654,7 +681,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         g.ldb_s = H / 32;
         g.N = I;
         g.K = H;
-        g.a1 = saved->a1;
+        set_a1(g, saved, ck);
         g.dprob_part = w.part;
         if (fp8) {
             g.act = (bf16_t*)w.da1;
@@ -748,7 +775,7 @@ int grouped_mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint
                     const moe_saved* saved, void* workspace, size_t workspace_bytes,
                     hipStream_t stream) {
     return mlp_fwd(precision, E, H, I, rows, xp, nullptr, split_sizes, w_gate_up, w_down,
-                   prob_perm, yp, saved, workspace, workspace_bytes, stream);
+                   prob_perm, yp, saved, A1Ckpt{}, workspace, workspace_bytes, stream);
 }
 
 int grouped_mlp_fwd_gather(int precision, int E, int H, int I, int64_t rows, const uint16_t* x,
@@ -759,7 +786,7 @@ int grouped_mlp_fwd_gather(int precision, int E, int H, int I, int64_t rows, con
     if (precision == MOE_BF16) return MOE_ERR_ARG;
     if (rows > 0 && !src_token) return MOE_ERR_NULL;
     return mlp_fwd(precision, E, H, I, rows, x, src_token, split_sizes, w_gate_up, w_down,
-                   prob_perm, yp, saved, workspace, workspace_bytes, stream);
+                   prob_perm, yp, saved, A1Ckpt{}, workspace, workspace_bytes, stream);
 }
 
 int grouped_mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dyp,
@@ -769,7 +796,7 @@ int grouped_mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint
                     uint16_t* const* dw_gate_up, uint16_t* const* dw_down, float* dprob_perm,
                     void* workspace, size_t workspace_bytes, hipStream_t stream) {
     return mlp_bwd(precision, E, H, I, rows, dyp, nullptr, xp, split_sizes, w_gate_up, w_down,
-                   prob_perm, saved, dxp, dw_gate_up, dw_down, dprob_perm, workspace,
+                   prob_perm, saved, A1Ckpt{}, dxp, dw_gate_up, dw_down, dprob_perm, workspace,
                    workspace_bytes, stream);
 }
 
@@ -783,8 +810,33 @@ int grouped_mlp_bwd_gather(int precision, int E, int H, int I, int64_t rows, con
     if (precision == MOE_BF16) return MOE_ERR_ARG;
     if (rows > 0 && !src_token) return MOE_ERR_NULL;
     return mlp_bwd(precision, E, H, I, rows, dy, src_token, nullptr, split_sizes, w_gate_up,
-                   w_down, prob_perm, saved, dxp, dw_gate_up, dw_down, dprob_perm, workspace,
+                   w_down, prob_perm, saved, A1Ckpt{}, dxp, dw_gate_up, dw_down, dprob_perm,
+                   workspace, workspace_bytes, stream);
+}
+
+int grouped_mlp_fwd_ckpt(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp,
+                         const int32_t* src_token, const int32_t* split_sizes,
+                         const uint16_t* const* w_gate_up, const uint16_t* const* w_down,
+                         const float* prob_perm, uint16_t* yp, const moe_saved* saved,
+                         uint8_t* a1_codes, uint8_t* a1_scales, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream) {
+    if (precision == MOE_BF16 && src_token) return MOE_ERR_ARG;
+    return mlp_fwd(precision, E, H, I, rows, xp, src_token, split_sizes, w_gate_up, w_down,
+                   prob_perm, yp, saved, A1Ckpt{a1_codes, a1_scales, true}, workspace,
                    workspace_bytes, stream);
+}
+
+int grouped_mlp_bwd_ckpt(int precision, int E, int H, int I, int64_t rows, const uint16_t* dyp,
+                         const int32_t* src_token, const uint16_t* xp, const int32_t* split_sizes,
+                         const uint16_t* const* w_gate_up, const uint16_t* const* w_down,
+                         const float* prob_perm, const moe_saved* saved, const uint8_t* a1_codes,
+                         const uint8_t* a1_scales, uint16_t* dxp, uint16_t* const* dw_gate_up,
+                         uint16_t* const* dw_down, float* dprob_perm, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream) {
+    if (precision == MOE_BF16 && src_token) return MOE_ERR_ARG;
+    return mlp_bwd(precision, E, H, I, rows, dyp, src_token, xp, split_sizes, w_gate_up, w_down,
+                   prob_perm, saved, A1Ckpt{(uint8_t*)a1_codes, (uint8_t*)a1_scales, true}, dxp,
+                   dw_gate_up, dw_down, dprob_perm, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

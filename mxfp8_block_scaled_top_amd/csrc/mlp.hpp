@@ -11,7 +11,17 @@ namespace moe {
 enum GemmDType { DT_BF16 = 0, DT_MX = 1, DT_FP8 = 2 };
 enum GemmLayout { L_KMAJ = 0, L_MNMAJ = 1 };   // operand contiguous along K / along M or N
 enum GemmGroup { G_M = 0, G_K = 1 };           // ragged rows (fwd, dgrad) / ragged K (wgrad)
-enum GemmEpi { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2 };
+// The _CK forms of the SwiGLU epilogues keep A1 as MXFP8 rows instead of bf16.
+enum GemmEpi {
+    EPI_STORE = 0,
+    EPI_SWIGLU_FWD = 1,
+    EPI_SWIGLU_BWD = 2,
+    EPI_SWIGLU_FWD_CK = 3,
+    EPI_SWIGLU_BWD_CK = 4
+};
+constexpr bool epi_fwd(int epi) { return epi == EPI_SWIGLU_FWD || epi == EPI_SWIGLU_FWD_CK; }
+constexpr bool epi_bwd(int epi) { return epi == EPI_SWIGLU_BWD || epi == EPI_SWIGLU_BWD_CK; }
+constexpr bool epi_ck(int epi) { return epi == EPI_SWIGLU_FWD_CK || epi == EPI_SWIGLU_BWD_CK; }
 // The six grouped GEMMs of the layer; each gets a kernel symbol of its own so
 // that profiles attribute time per GEMM.
 enum GemmUse {
@@ -59,6 +69,8 @@ struct GemmArgs {
     // epilogue
     const float* prob;  // prob_perm [rows]
     bf16_t* a1;         // SWIGLU_FWD: out [rows, 2I]; SWIGLU_BWD: in
+    uint8_t* a1_codes;  // the same as MXFP8 rows: codes [rows, 2I] and scales [rows, 2I/32];
+    uint8_t* a1_scales; // when given, the _CK epilogues use them in place of a1
     bf16_t* act;        // SWIGLU_FWD: A2 bf16 [rows, I]; SWIGLU_BWD: dA1 bf16 [rows, 2I]
     uint8_t* q_row;     // MXFP8 rowwise codes of the epilogue output
     uint8_t* q_row_s;

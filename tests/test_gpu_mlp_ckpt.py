@@ -1,0 +1,340 @@
+"""GPU: the grouped expert MLP with its gate_up output A1 kept in 8 bits, and
+the pre-norm sublayer built on it.
+
+The forward's other outputs are those of grouped_mlp_fwd bit for bit, and the
+backward's are those of grouped_mlp_bwd on the decoded A1 bit for bit, so what
+the tests of those calls show carries over; the codes themselves are held
+against A1 in float64."""
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_block_scaled_top_amd as moe
+from mxfp8_block_scaled_top_amd.layer import LayerBuffers, layer_step, layer_step_norm, layer_step_router
+from oracle import mlp as omlp
+from oracle import mx as omx
+from oracle import sublayer as S
+from tests.helpers import need_gpu, np_, rel_frob, say
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, U = torch.bfloat16, torch.float32, 2.0 ** -24
+ALL, IDS = [moe.MOE_BF16, moe.MOE_MXFP8, moe.MOE_FP8], ["bf16", "mxfp8", "fp8"]
+NAME = dict(zip(ALL, IDS))
+TOL = {moe.MOE_BF16: 1e-2, moe.MOE_MXFP8: 2e-2, moe.MOE_FP8: 2e-2}   # as the layer's own tests
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _inputs(sizes, H, I, seed, wstd=0.05):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).to(BF)     # noqa: E731
+    rows, E = sum(sizes), len(sizes)
+    return {"xp": r(rows, H), "dyp": r(rows, H), "split": torch.tensor(sizes, dtype=torch.int32),
+            "w1": [r(2 * I, H, std=wstd) for _ in range(E)], "w2": [r(H, I, std=wstd) for _ in range(E)],
+            "pp": torch.rand(rows, generator=g)}
+
+
+def _cuda(inp):
+    return {k: [w.cuda() for w in v] if isinstance(v, list) else v.cuda() for k, v in inp.items()}
+
+
+SIZES = [([300, 0, 1, 399], 384, 640), ([1], 128, 128), ([0, 0, 5], 256, 384), ([257, 31, 513], 128, 1408),
+         ([64] * 16, 256, 256)]
+
+
+@pytest.mark.parametrize("sizes,H,I", SIZES)
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+def test_against_the_bf16_form(precision, sizes, H, I):
+    say(f"mlp ckpt {NAME[precision]} sizes={sizes} H={H} I={I}")
+    d = _cuda(_inputs(sizes, H, I, seed=len(sizes) + I))
+    rows = sum(sizes)
+    args = (d["split"], d["w1"], d["w2"], d["pp"])
+    yp0, s0 = moe.grouped_mlp_fwd(d["xp"], *args, precision)
+    yp, s = moe.grouped_mlp_fwd_ckpt(d["xp"], *args, precision)
+    torch.cuda.synchronize()
+    assert "a1" not in s and torch.equal(yp, yp0)
+    for k in s:
+        if k == "a2":
+            assert torch.equal(s[k], s0[k]), k
+    # the codes against the bf16 A1 of the other form: half a step of each format
+    v = torch.from_numpy(omx.dequantize_rows(np_(s["a1_codes"]), np_(s["a1_scales"]))).double()
+    a1 = s0["a1"].double().cpu()
+    X = torch.from_numpy(2.0 ** (np_(s["a1_scales"]).astype(np.float64) - 127)).repeat_interleave(32, 1)
+    half = 2.0 ** -8 * a1.abs() * 1.01
+    assert ((v - a1).abs() <= torch.maximum(2.0 ** -4 * (a1.abs() + half), 2.0 ** -10 * X) + half).all()
+    # backward from the codes = backward of the bf16 form on what they stand for
+    s0["a1"] = moe.mxfp8_dequantize(s["a1_codes"], s["a1_scales"], rows, 2 * I)
+    assert torch.equal(s0["a1"].double().cpu(), v)
+    want = moe.grouped_mlp_bwd(d["dyp"], d["xp"], *args, s0, precision)
+    got = moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s, precision)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+    for e in range(len(sizes)):
+        assert torch.equal(got[1][e], want[1][e]) and torch.equal(got[2][e], want[2][e]), e
+        if sizes[e] == 0:
+            assert not got[1][e].any() and not got[2][e].any()
+
+
+@pytest.mark.parametrize("precision", [moe.MOE_BF16, moe.MOE_MXFP8], ids=["bf16", "mxfp8"])
+def test_codes_against_float64(precision):
+    """A1 = x W1^T in float64 (MXFP8: of the quantized operands, whose values
+    are exact): fp32 accumulation is off by at most H u sum|x w|, a code by
+    half a step, and the scale is the smallest power of two that fits."""
+    sizes, H, I = [130, 0, 70], 256, 384
+    say(f"mlp ckpt codes {NAME[precision]}")
+    inp = _inputs(sizes, H, I, seed=3)
+    _, s = moe.grouped_mlp_fwd_ckpt(*[_cuda(inp)[k] for k in ("xp", "split", "w1", "w2", "pp")], precision)
+    torch.cuda.synchronize()
+    q = (lambda t: omx.qdq_rows(t).double()) if precision == moe.MOE_MXFP8 else (lambda t: t.double())
+    x, at, a1, mag = q(inp["xp"]), 0, [], []
+    for n, w in zip(sizes, inp["w1"]):
+        w = q(w)
+        a1.append(x[at:at + n] @ w.T)
+        mag.append(x[at:at + n].abs() @ w.abs().T)
+        at += n
+    a1, err = torch.cat(a1), H * U * torch.cat(mag)
+    scales = np_(s["a1_scales"]).astype(np.float64)
+    v = torch.from_numpy(omx.dequantize_rows(np_(s["a1_codes"]), np_(s["a1_scales"]))).double()
+    Xb = torch.from_numpy(2.0 ** (scales - 127))
+    X = Xb.repeat_interleave(32, 1)
+    assert ((v - a1).abs() <= torch.maximum(2.0 ** -4 * a1.abs(), 2.0 ** -10 * X) + 1.0625 * err).all()
+    top = a1.abs().reshape(*scales.shape, 32).amax(2)
+    slack = err.reshape(*scales.shape, 32).amax(2)
+    assert (top <= 448 * Xb + slack).all() and (top >= 224 * Xb - slack).all()
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+def test_backward_against_the_oracle(precision):
+    sizes, H, I = [200, 0, 1, 99], 256, 384
+    say(f"mlp ckpt oracle {NAME[precision]}")
+    inp = _inputs(sizes, H, I, seed=4)
+    d = _cuda(inp)
+    args = (d["split"], d["w1"], d["w2"], d["pp"])
+    yp, s = moe.grouped_mlp_fwd_ckpt(d["xp"], *args, precision)
+    got = moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s, precision)
+    torch.cuda.synchronize()
+    ref = omlp.grouped_mlp_fwd(inp["xp"], sizes, inp["w1"], inp["w2"], inp["pp"].numpy(), NAME[precision])
+    assert rel_frob(yp, ref["yp"]) <= TOL[precision]
+    ref["a1"] = torch.from_numpy(omx.dequantize_rows(np_(s["a1_codes"]), np_(s["a1_scales"]))).to(BF)
+    back = omlp.grouped_mlp_bwd(inp["dyp"], inp["xp"], sizes, inp["w1"], inp["w2"], inp["pp"].numpy(), ref,
+                                NAME[precision])
+    for g, k in ((got[0], "dxp"), (got[3], "dpp")):
+        assert rel_frob(g, back[k]) <= TOL[precision], k
+    for e, n in enumerate(sizes):
+        if n:
+            assert rel_frob(got[1][e], back["dw1"][e]) <= TOL[precision], e
+            assert rel_frob(got[2][e], back["dw2"][e]) <= TOL[precision], e
+
+
+@pytest.mark.parametrize("precision", [moe.MOE_MXFP8, moe.MOE_FP8], ids=["mxfp8", "fp8"])
+def test_gathered_form(precision):
+    say(f"mlp ckpt gathered {NAME[precision]}")
+    sizes, H, I, T = [150, 20, 230], 256, 256, 200
+    inp = _inputs(sizes, H, I, seed=5)
+    src = torch.randperm(400, generator=torch.Generator().manual_seed(1)) % T
+    x, dy = inp["xp"][:T].cuda(), inp["dyp"][:T].cuda()
+    d, src = _cuda(inp), src.int().cuda()
+    xp, dyp = x[src.long()].contiguous(), dy[src.long()].contiguous()
+    args = (d["split"], d["w1"], d["w2"], d["pp"])
+    yp0, s0 = moe.grouped_mlp_fwd_ckpt(xp, *args, precision)
+    yp1, s1 = moe.grouped_mlp_fwd_ckpt(x, *args, precision, src_token=src)
+    g0 = moe.grouped_mlp_bwd_ckpt(dyp, None, *args, s0, precision)
+    g1 = moe.grouped_mlp_bwd_ckpt(dy, None, *args, s1, precision, src_token=src)
+    torch.cuda.synchronize()
+    assert torch.equal(yp0, yp1) and torch.equal(s0["a1_codes"], s1["a1_codes"])
+    assert torch.equal(s0["a1_scales"], s1["a1_scales"]) and torch.equal(g0[0], g1[0]) and torch.equal(g0[3], g1[3])
+
+
+def test_no_rows():
+    say("mlp ckpt rows=0")
+    d = _cuda(_inputs([0, 0], 128, 256, seed=6))
+    args = (d["split"], d["w1"], d["w2"], d["pp"])
+    for precision in ALL:
+        yp, s = moe.grouped_mlp_fwd_ckpt(d["xp"], *args, precision)
+        dxp, dw1, dw2, _ = moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s, precision)
+        torch.cuda.synchronize()
+        assert yp.shape == (0, 128) and dxp.shape == (0, 128)
+        assert not any(w.any() for w in dw1 + dw2)
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+def test_rows_behind_the_last_expert_stay(precision):
+    """Split sizes that sum to fewer rows than the buffers have."""
+    say(f"mlp ckpt rows behind {NAME[precision]}")
+    H, I, rows, used = 128, 256, 300, 177
+    d = _cuda(_inputs([100, 77, 123], H, I, seed=7))
+    split = torch.tensor([100, 77], dtype=torch.int32).cuda()
+    saved = moe.alloc_saved(rows, H, I, 2, precision, "cuda", checkpoint=True)
+    saved["a1_codes"].fill_(77)
+    saved["a1_scales"].fill_(78)
+    moe.grouped_mlp_fwd_ckpt(d["xp"], split, d["w1"][:2], d["w2"][:2], d["pp"], precision, saved)
+    torch.cuda.synchronize()
+    assert (saved["a1_codes"][used:] == 77).all() and (saved["a1_scales"][used:] == 78).all()
+    assert not (saved["a1_scales"][:used] == 78).any()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 codes: the last row tile is what it is by itself."""
+    say("mlp ckpt with 2^31 codes")
+    H, I, rows, n = 128, 14336, 256 * 320, 256
+    g = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(BF)   # noqa: E731
+    w1, w2 = [r(2 * I, H, std=0.1)], [r(H, I, std=0.05)]
+    xp, dyp, pp = r(rows, H), r(rows, H), torch.rand(rows, generator=g, device="cuda")
+    run = []
+    for a in (0, rows - n):
+        sp = torch.tensor([rows - a], dtype=torch.int32, device="cuda")
+        x, dy, p = xp[a:].contiguous(), dyp[a:].contiguous(), pp[a:].contiguous()
+        yp, s = moe.grouped_mlp_fwd_ckpt(x, sp, w1, w2, p, moe.MOE_BF16)
+        dxp, _, _, dp = moe.grouped_mlp_bwd_ckpt(dy, x, sp, w1, w2, p, s, moe.MOE_BF16)
+        torch.cuda.synchronize()
+        run.append([t[-n:].clone() for t in (yp, s["a1_codes"], s["a1_scales"], dxp, dp)])
+        del s, yp, dxp
+    for a, b in zip(*run):
+        assert torch.equal(a, b)
+
+
+def _layer_inputs(T, H, I, E, seed, xt=BF):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s, std=1.0: torch.randn(*s, generator=g) * std     # noqa: E731
+    return {"x": (r(T, H) * 2 + 0.3).to(xt), "gamma": 1 + r(H, std=0.2), "beta": r(H, std=0.1),
+            "wr": r(E, H, std=H ** -0.5).to(BF), "w1": [r(2 * I, H, std=0.05).to(BF) for _ in range(E)],
+            "w2": [r(H, I, std=0.05).to(BF) for _ in range(E)], "dy": r(T, H).to(BF), "dres": r(T, H).to(xt)}
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+@pytest.mark.parametrize("xt,ckpt", [(BF, True), (F32, True), (BF, False)], ids=["bf16", "f32", "bf16_wide"])
+def test_prenorm_sublayer(precision, xt, ckpt):
+    """Norm, router, experts and all their gradients together.  The experts'
+    part is checked through its own calls bit for bit, the norm's gradient
+    against float64, and the whole against differences below."""
+    T, H, I, E, k = 300, 256, 384, 5, 2
+    say(f"prenorm sublayer {NAME[precision]} x={xt} ckpt={ckpt}")
+    d = _cuda(_layer_inputs(T, H, I, E, 9, xt))
+    out = layer_step_norm(d["x"], d["gamma"], d["beta"], d["wr"], d["w1"], d["w2"], d["dy"], k, precision,
+                          checkpoint=ckpt, dres=d["dres"])
+    bufs = LayerBuffers(T, H, I, E, k, precision, "cuda", checkpoint=ckpt)
+    ref = layer_step_router(out["n"], d["wr"], d["w1"], d["w2"], d["dy"], k, precision, bufs)
+    torch.cuda.synchronize()
+    for key in ("y", "dlogits", "dpp", "dw_router"):
+        assert torch.equal(out[key], ref[key]), key
+    assert torch.equal(out["dn"], ref["dx"])
+    for e in range(E):
+        assert torch.equal(out["dw1"][e], ref["dw1"][e]) and torch.equal(out["dw2"][e], ref["dw2"][e])
+    f = S.layernorm_fwd(d["x"].cpu(), d["gamma"].cpu(), d["beta"].cpu())
+    assert rel_frob(out["n"], f["y"]) <= 2.0 ** -8
+    b = S.layernorm_bwd(out["dn"].cpu(), f["xh"], f["rstd"], d["gamma"].cpu(), d["dres"].cpu())
+    # from 8 bits xh is off by at most 2^-4 of each value and 2^-10 of its block's
+    # largest / 224: dx gets that times |c2| rstd, dgamma times |dy|
+    loose = 2.0 ** -4 * (1 + 2.0 ** -6) if ckpt else 0.0
+    dx_norm = b["dx"].norm()
+    part = (f["rstd"][:, None] * (f["xh"].abs() * b["c2"].abs() + f["xh"].abs() *
+                                  (b["g"].abs() * f["xh"].abs()).mean(1, keepdim=True))).norm()
+    assert (out["dx"].double().cpu() - b["dx"]).norm() <= 2.0 ** -8 * dx_norm + 1.1 * loose * part + 1e-5 * dx_norm
+    dg = (out["dn"].double().cpu().abs() * f["xh"].abs()).sum(0)
+    assert ((out["dgamma"].double().cpu() - b["dgamma"]).abs() <= (loose + 1e-5) * dg + 1e-6).all()
+    assert rel_frob(out["dbeta"], b["dbeta"]) <= 1e-5
+
+
+def test_prenorm_sublayer_against_autograd():
+    """BF16 experts, everything kept wide: dx and dgamma against autograd in
+    float64 through the same picks (every bf16 rounding on the way adds 2^-8
+    at most; a handful of them meet in one gradient: 1e-2 as the layer's
+    tests)."""
+    T, H, I, E, k = 120, 128, 256, 4, 2
+    say("prenorm sublayer autograd")
+    inp = _layer_inputs(T, H, I, E, 10, F32)
+    d = _cuda(inp)
+    out = layer_step_norm(d["x"], d["gamma"], d["beta"], d["wr"], d["w1"], d["w2"], d["dy"], k, moe.MOE_BF16,
+                          checkpoint=False)
+    torch.cuda.synchronize()
+    x, ga, be = (inp[n].double().requires_grad_() for n in ("x", "gamma", "beta"))
+    n = torch.nn.functional.layer_norm(x, (H,), ga, be, 1e-5)
+    pick = out["route"]["topk_expert"].long().cpu()
+    prob = torch.softmax((n @ inp["wr"].double().T).gather(1, pick), 1)
+    y = torch.zeros(T, H, dtype=torch.float64)
+    for j in range(k):
+        for e in range(E):
+            t = (pick[:, j] == e).nonzero().flatten()
+            a = n[t] @ inp["w1"][e].double().T
+            h = torch.nn.functional.silu(a[:, :I]) * a[:, I:] * prob[t, j:j + 1]
+            y = y.index_add(0, t, h @ inp["w2"][e].double().T)
+    (y * inp["dy"].double()).sum().backward()
+    errs = {"y": rel_frob(out["y"], y.detach()), "dx": rel_frob(out["dx"], x.grad),
+            "dgamma": rel_frob(out["dgamma"], ga.grad), "dbeta": rel_frob(out["dbeta"], be.grad)}
+    say("  " + str(errs))
+    assert max(errs.values()) <= 1e-2, errs
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+def test_layer_step_with_checkpoint_in_a_graph(precision):
+    T, H, I, E, k = 333, 256, 384, 5, 2
+    say(f"prenorm sublayer in a graph {NAME[precision]}")
+    d, o = _cuda(_layer_inputs(T, H, I, E, 11)), _cuda(_layer_inputs(T, H, I, E, 12))
+    bufs = LayerBuffers(T, H, I, E, k, precision, "cuda", checkpoint=True)
+    other = LayerBuffers(T, H, I, E, k, precision, "cuda", checkpoint=True)
+    step = lambda d, bufs: layer_step_norm(d["x"], d["gamma"], d["beta"], d["wr"], d["w1"], d["w2"],   # noqa: E731
+                                           d["dy"], k, precision, bufs, dres=d["dres"])
+    keys = ("y", "dx", "dgamma", "dbeta", "dlogits", "dw_router")
+    ref = step(d, bufs)
+    torch.cuda.synchronize()
+    ref = {n: ref[n].clone() for n in keys} | {"dw1": [w.clone() for w in ref["dw1"]]}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(d, bufs)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(d, bufs)
+    for rep in range(3):
+        step(o, other)
+        torch.cuda.synchronize()
+        for n in keys:
+            out[n].fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in keys:
+            assert torch.equal(out[n], ref[n]), (rep, n)
+        for a, b in zip(out["dw1"], ref["dw1"]):
+            assert torch.equal(a, b), rep
+
+
+def test_layer_step_checkpoint_buffers_change_only_the_backward():
+    say("layer_step with checkpoint buffers")
+    T, H, I, E, k = 200, 128, 256, 4, 2
+    d = _cuda(_layer_inputs(T, H, I, E, 13))
+    logits = torch.randn(T, E, generator=torch.Generator().manual_seed(1)).cuda()
+    run = [layer_step(logits, d["x"], d["w1"], d["w2"], d["dy"], k, moe.MOE_MXFP8,
+                      LayerBuffers(T, H, I, E, k, moe.MOE_MXFP8, "cuda", checkpoint=c)) for c in (False, True)]
+    torch.cuda.synchronize()
+    assert torch.equal(run[0]["y"], run[1]["y"])
+    for e in range(E):
+        assert torch.equal(run[0]["dw2"][e], run[1]["dw2"][e])     # dW_down does not read A1
+    assert not torch.equal(run[0]["dx"], run[1]["dx"])
+    fwd = layer_step(logits, d["x"], d["w1"], d["w2"], None, k, moe.MOE_MXFP8,
+                     LayerBuffers(T, H, I, E, k, moe.MOE_MXFP8, "cuda", checkpoint=True), with_backward=False)
+    torch.cuda.synchronize()
+    assert torch.equal(fwd["y"], run[0]["y"])
+
+
+def test_binding_refusals():
+    say("mlp ckpt binding refusals")
+    d = _cuda(_inputs([3, 5], 128, 128, seed=14))
+    args = (d["split"], d["w1"], d["w2"], d["pp"])
+    _, s = moe.grouped_mlp_fwd_ckpt(d["xp"], *args, moe.MOE_BF16)
+    wide = moe.alloc_saved(8, 128, 128, 2, moe.MOE_BF16, "cuda")
+    src = torch.zeros(8, dtype=torch.int32, device="cuda")
+    for call in (lambda: moe.grouped_mlp_fwd_ckpt(d["xp"], *args, moe.MOE_BF16, wide),
+                 lambda: moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, wide, moe.MOE_BF16),
+                 lambda: moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s | {"a1_codes": s["a1_codes"][:4]},
+                                                  moe.MOE_BF16),
+                 lambda: moe.grouped_mlp_fwd_ckpt(d["xp"], *args, moe.MOE_BF16, src_token=src),
+                 lambda: moe.grouped_mlp_bwd_ckpt(d["dyp"], None, *args, s, moe.MOE_BF16)):
+        with pytest.raises(moe.MoEError):
+            call()

@@ -97,3 +97,33 @@ def test_binding_refuses_host_tensors():
                  lambda: moe.moe_layernorm_fwd(None), lambda: moe.moe_swiglu_fwd(x[0])):
         with pytest.raises(moe.MoEError):
             call()
+
+
+def _mlp(L, bwd, **k):
+    saved = moe._Saved(None, 4096, 4096, 4096, 4096, 4096)
+    tab = (ctypes.c_void_p * 2)(4096, 4096)
+    common = dict(prec=0, E=2, H=128, I=256, rows=8)
+    if bwd:
+        a = common | dict(dyp=P, src=None, xp=P, split=P, w1=tab, w2=tab, prob=P, saved=ctypes.byref(saved),
+                          codes=P, scales=P, dxp=P, dw1=tab, dw2=tab, dprob=P, ws=P, n=1 << 30) | k
+        return L.grouped_mlp_bwd_ckpt(*a.values(), None)
+    a = common | dict(xp=P, src=None, split=P, w1=tab, w2=tab, prob=P, yp=P, saved=ctypes.byref(saved),
+                      codes=P, scales=P, ws=P, n=1 << 30) | k
+    return L.grouped_mlp_fwd_ckpt(*a.values(), None)
+
+
+@pytest.mark.parametrize("bwd", [False, True], ids=["fwd", "bwd"])
+@pytest.mark.parametrize("change,status", [
+    ({"codes": None}, NULL), ({"scales": None}, NULL), ({"codes": MIS}, ALIGN), ({"scales": MIS}, ALIGN),
+    ({"src": P}, ARG), ({"prec": 3}, ARG), ({"H": 100}, SHAPE), ({"I": 200}, SHAPE), ({"E": 65}, SHAPE),
+    ({"rows": -1}, SHAPE), ({"split": None}, NULL), ({"saved": None}, NULL), ({"n": 1}, WS),
+])
+def test_grouped_mlp_ckpt_refuses(L, bwd, change, status):
+    assert _mlp(L, bwd, **change) == status
+
+
+def test_grouped_mlp_ckpt_needs_no_bf16_a1(L):
+    """saved->a1 is NULL above: a call that is refused for its workspace alone got past it."""
+    for bwd in (False, True):
+        assert _mlp(L, bwd, n=1) == WS
+        assert _mlp(L, bwd, prec=1, src=P, n=1) == WS
