@@ -118,8 +118,28 @@ def _check(status: int, what: str) -> None:
         raise MoEError(f"{what} failed: status {status} ({msg})")
 
 
+# the current stream's handle without building a stream object (a few
+# microseconds a call), where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device=None) -> int:
+    if _raw_stream is not None and device is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _call(name: str, device, *args) -> None:
+    """The C entry point `name` on the device of its tensors (the current one
+    or not) and on that device's current stream."""
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        status = f(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, _stream(device))
+    if status:
+        _check(status, name)
 
 
 def _ptr(t) -> int:
@@ -414,18 +434,14 @@ def grouped_mlp_fwd_ckpt(xp, split_sizes, w_gate_up, w_down, prob_perm, precisio
     codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
     if codes is None:
         raise MoEError("saved has no a1_codes: use alloc_saved(..., checkpoint=True)")
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = _workspace(moe_workspace_bytes(MOE_OP_MLP_FWD, rows, H, I, E, 1, precision), dev)
-        yp = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
-        w1, w2 = _ptr_array(w_gate_up), _ptr_array(w_down)
-        st = _saved_struct(saved)
-        _check(lib().grouped_mlp_fwd_ckpt(precision, E, H, I, rows, _ptr(xp), _ptr(src_token),
-                                          _ptr(split_sizes), ctypes.cast(w1, ctypes.c_void_p),
-                                          ctypes.cast(w2, ctypes.c_void_p), _ptr(prob_perm),
-                                          _ptr(yp), ctypes.byref(st), _ptr(codes), _ptr(scales),
-                                          _ptr(workspace), workspace.numel(), _stream(dev)),
-               "grouped_mlp_fwd_ckpt")
+    if workspace is None:
+        workspace = _workspace(moe_workspace_bytes(MOE_OP_MLP_FWD, rows, H, I, E, 1, precision), dev)
+    yp = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
+    w1, w2 = _ptr_array(w_gate_up), _ptr_array(w_down)
+    _call("grouped_mlp_fwd_ckpt", dev, precision, E, H, I, rows, _ptr(xp), _ptr(src_token),
+          _ptr(split_sizes), ctypes.addressof(w1), ctypes.addressof(w2), _ptr(prob_perm), _ptr(yp),
+          ctypes.byref(_saved_struct(saved)), _ptr(codes), _ptr(scales), _ptr(workspace),
+          workspace.numel())
     return yp, saved
 
 
@@ -446,27 +462,21 @@ def grouped_mlp_bwd_ckpt(dyp, xp, split_sizes, w_gate_up, w_down, prob_perm, sav
     codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
     if codes is None:
         raise MoEError("saved has no a1_codes (grouped_mlp_fwd_ckpt)")
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = _workspace(moe_workspace_bytes(MOE_OP_MLP_BWD, rows, H, I, E, 1, precision), dev)
-        dxp = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
-        if dw_gate_up is None:
-            dw_gate_up = [torch.empty((2 * I, H), dtype=torch.bfloat16, device=dev) for _ in range(E)]
-        if dw_down is None:
-            dw_down = [torch.empty((H, I), dtype=torch.bfloat16, device=dev) for _ in range(E)]
-        dpp = torch.empty(rows, dtype=torch.float32, device=dev)
-        w1, w2 = _ptr_array(w_gate_up), _ptr_array(w_down)
-        d1, d2 = _ptr_array(dw_gate_up), _ptr_array(dw_down)
-        st = _saved_struct(saved)
-        _check(lib().grouped_mlp_bwd_ckpt(precision, E, H, I, rows, _ptr(dyp), _ptr(src_token),
-                                          _ptr(xp), _ptr(split_sizes),
-                                          ctypes.cast(w1, ctypes.c_void_p),
-                                          ctypes.cast(w2, ctypes.c_void_p), _ptr(prob_perm),
-                                          ctypes.byref(st), _ptr(codes), _ptr(scales), _ptr(dxp),
-                                          ctypes.cast(d1, ctypes.c_void_p),
-                                          ctypes.cast(d2, ctypes.c_void_p), _ptr(dpp),
-                                          _ptr(workspace), workspace.numel(), _stream(dev)),
-               "grouped_mlp_bwd_ckpt")
+    if workspace is None:
+        workspace = _workspace(moe_workspace_bytes(MOE_OP_MLP_BWD, rows, H, I, E, 1, precision), dev)
+    dxp = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
+    if dw_gate_up is None:
+        dw_gate_up = [torch.empty((2 * I, H), dtype=torch.bfloat16, device=dev) for _ in range(E)]
+    if dw_down is None:
+        dw_down = [torch.empty((H, I), dtype=torch.bfloat16, device=dev) for _ in range(E)]
+    dpp = torch.empty(rows, dtype=torch.float32, device=dev)
+    w1, w2 = _ptr_array(w_gate_up), _ptr_array(w_down)
+    d1, d2 = _ptr_array(dw_gate_up), _ptr_array(dw_down)
+    _call("grouped_mlp_bwd_ckpt", dev, precision, E, H, I, rows, _ptr(dyp), _ptr(src_token),
+          _ptr(xp), _ptr(split_sizes), ctypes.addressof(w1), ctypes.addressof(w2),
+          _ptr(prob_perm), ctypes.byref(_saved_struct(saved)), _ptr(codes), _ptr(scales),
+          _ptr(dxp), ctypes.addressof(d1), ctypes.addressof(d2), _ptr(dpp), _ptr(workspace),
+          workspace.numel())
     return dxp, dw_gate_up, dw_down, dpp
 
 
@@ -617,25 +627,28 @@ _TYPES = {torch.bfloat16: 0, torch.float32: 1}      # moe_type
 
 def _arg(t, name: str, dtype, shape, device) -> None:
     """A tensor argument of this type (or one of these), shape and device, dense."""
+    dtypes = dtype if dtype.__class__ is tuple else (dtype,)
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_cuda
+            and t.device == device and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MoEError(f"{name} must be a device tensor")
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
     if t.dtype not in dtypes:
         raise MoEError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise MoEError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise MoEError(f"{name} must be contiguous")
     if t.device != device:
         raise MoEError(f"{name} is on {t.device}, not on {device}")
+    raise MoEError(f"{name} must be contiguous")
 
 
 def _first(t, name: str, dtype) -> tuple:
     """The first tensor argument, a matrix: (rows, columns, device)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise MoEError(f"{name} must be a matrix")
-    _arg(t, name, dtype, t.shape, t.device)
-    return t.shape[0], t.shape[1], t.device
+    device = t.device
+    _arg(t, name, dtype, t.shape, device)
+    return *t.shape, device
 
 
 def _checkpoint(rows: int, cols: int, device):
@@ -667,17 +680,16 @@ def moe_layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, checkpoint: b
         raise MoEError("gamma and beta must have one type")
     w = gamma if gamma is not None else beta
     y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    saved = {"mean": torch.empty(T, dtype=torch.float32, device=dev),
-             "rstd": torch.empty(T, dtype=torch.float32, device=dev)}
+    mean = torch.empty(T, dtype=torch.float32, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    saved = {"mean": mean, "rstd": rstd}
     codes = scales = None
     if checkpoint:
         codes, scales = _checkpoint(T, H, dev)
         saved["xhat_codes"], saved["xhat_scales"] = codes, scales
-    with torch.cuda.device(dev):
-        _check(lib().moe_layernorm_fwd(_TYPES[x.dtype], _TYPES[w.dtype] if w is not None else 1, T,
-                                       H, _ptr(x), _ptr(gamma), _ptr(beta), eps, _ptr(y),
-                                       _ptr(saved["mean"]), _ptr(saved["rstd"]), _ptr(codes),
-                                       _ptr(scales), _stream(dev)), "moe_layernorm_fwd")
+    _call("moe_layernorm_fwd", dev, _TYPES[x.dtype], _TYPES[w.dtype] if w is not None else 1, T, H,
+          _ptr(x), _ptr(gamma), _ptr(beta), eps, _ptr(y), _ptr(mean), _ptr(rstd), _ptr(codes),
+          _ptr(scales))
     return y, saved
 
 
@@ -712,15 +724,12 @@ def moe_layernorm_bwd(dy, saved: dict, gamma=None, x=None, dres=None, dx_dtype=N
     dx = torch.empty((T, H), dtype=dx_dtype, device=dev)
     dgamma = torch.empty(H, dtype=wt, device=dev) if want_dgamma else None
     dbeta = torch.empty(H, dtype=wt, device=dev) if want_dbeta else None
-    with torch.cuda.device(dev):
-        if workspace is None and (want_dgamma or want_dbeta):
-            workspace = _workspace(int(lib().moe_layernorm_workspace_bytes(T, H)), dev)
-        _check(lib().moe_layernorm_bwd(_TYPES[dx_dtype], _TYPES[wt], T, H, _ptr(dy), _ptr(x),
-                                       _ptr(mean), _ptr(saved["rstd"]), _ptr(codes), _ptr(scales),
-                                       _ptr(gamma), _ptr(dres), _ptr(dx), _ptr(dgamma),
-                                       _ptr(dbeta), _ptr(workspace),
-                                       0 if workspace is None else workspace.numel(),
-                                       _stream(dev)), "moe_layernorm_bwd")
+    if workspace is None and (want_dgamma or want_dbeta):
+        workspace = _workspace(lib().moe_layernorm_workspace_bytes(T, H), dev)
+    _call("moe_layernorm_bwd", dev, _TYPES[dx_dtype], _TYPES[wt], T, H, _ptr(dy), _ptr(x),
+          _ptr(mean), _ptr(saved["rstd"]), _ptr(codes), _ptr(scales), _ptr(gamma), _ptr(dres),
+          _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+          0 if workspace is None else workspace.numel())
     return dx, dgamma, dbeta
 
 
@@ -737,9 +746,8 @@ def moe_swiglu_fwd(a1, prob=None, checkpoint: bool = False):
     codes = scales = None
     if checkpoint:
         codes, scales = _checkpoint(rows, cols, dev)
-    with torch.cuda.device(dev):
-        _check(lib().moe_swiglu_fwd(rows, cols // 2, _ptr(a1), _ptr(prob), _ptr(a2), _ptr(codes),
-                                    _ptr(scales), _stream(dev)), "moe_swiglu_fwd")
+    _call("moe_swiglu_fwd", dev, rows, cols // 2, _ptr(a1), _ptr(prob), _ptr(a2), _ptr(codes),
+          _ptr(scales))
     return a2, ({"a1_codes": codes, "a1_scales": scales} if checkpoint else {"a1": a1})
 
 
@@ -757,10 +765,8 @@ def moe_swiglu_bwd(da2, saved: dict, prob=None):
         _arg(prob, "prob", torch.float32, (rows,), dev)
         dprob = torch.empty(rows, dtype=torch.float32, device=dev)
     da1 = torch.empty((rows, 2 * I), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().moe_swiglu_bwd(rows, I, _ptr(da2), _ptr(a1), _ptr(codes), _ptr(scales),
-                                    _ptr(prob), _ptr(da1), _ptr(dprob), _stream(dev)),
-               "moe_swiglu_bwd")
+    _call("moe_swiglu_bwd", dev, rows, I, _ptr(da2), _ptr(a1), _ptr(codes), _ptr(scales),
+          _ptr(prob), _ptr(da1), _ptr(dprob))
     return da1, dprob
 
 

@@ -110,6 +110,38 @@ __device__ __forceinline__ float mx_decode(uint32_t code, uint32_t S) {
     return (code & 0x80u) ? -v : v;
 }
 
+// v plus the value that the DPP control brings (0 where it brings none).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, kRows, 0xf,
+                                                          false));
+}
+
+// Sum over the 64 lanes, the same for all of them: shifts inside the rows of
+// 16 lanes, then the rows' sums passed on (six dependent adds and no LDS; the
+// order is fixed).
+__device__ __forceinline__ float wave_sum(float v) {
+    v = dpp_add<0x111, 0xf>(v);     // row_shr:1, 2, 4, 8
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);     // row_bcast:15 into rows 1 and 3
+    v = dpp_add<0x143, 0xc>(v);     // row_bcast:31 into rows 2 and 3
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sum over each 16 (or 32) neighbouring lanes, the same for all of them.
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float v) {
+    static_assert(kLanes == 16 || kLanes == 32, "part of a wave");
+    v = dpp_add<0xB1, 0xf>(v);      // quad_perm: lane ^ 1, lane ^ 2
+    v = dpp_add<0x4E, 0xf>(v);
+    v = dpp_add<0x141, 0xf>(v);     // row_half_mirror, row_mirror
+    v = dpp_add<0x140, 0xf>(v);
+    if (kLanes == 32) v += __shfl_xor(v, 16);
+    return v;
+}
+
 // Largest of the four lanes 4q..4q+3 (quad permutes; no LDS).
 __device__ __forceinline__ float quad_max(float v) {
     v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xf, 0xf, true)));

@@ -8,17 +8,22 @@
 //             dgamma = sum_t dy xh,  dbeta = sum_t dy
 //
 // Both are bound by HBM bytes (about 10 operations per element).  Every row
-// is read once: kWpr waves hold it in registers, 8 neighbouring values per
-// lane and step (16 bytes of bf16), and all sums over the row come from the
-// registers, the variance around the mean already known, so nothing cancels.
-// Sums are fp32; the only roundings to fewer bits are the stored y, dx and
-// codes.
+// is read once: one or several waves (or a part of one) hold it in registers,
+// 8 neighbouring values per lane and step (16 bytes of bf16), and all sums
+// over the row come from the registers, the variance around the mean already
+// known, so nothing cancels.  Sums are fp32; the only roundings to fewer bits
+// are the stored y, dx and codes.
 //
 // A workgroup walks over rows with gamma (and beta) in registers: read per
 // row they would be more bytes from L2 than the row itself.  The backward
 // keeps its workgroup's dgamma and dbeta in registers over that walk and
 // writes them once, as one partial row per workgroup; a second kernel adds
 // the partial rows in a fixed order (no atomics: the same bits every time).
+//
+// Measured with bf16 rows, 168 MB a pass: forward with checkpoint 31 us at
+// 16384 x 2048 and 8192 x 4096 (5.4 TB/s; a large copy reaches 5.2); backward
+// from the checkpoint 43 us (3.9 TB/s), of which dx alone 35 us, the rest
+// the partial rows (4 us for the second kernel and its launch).
 #include "common.hpp"
 #include "kernels.hpp"
 #include "trace.hpp"
@@ -27,30 +32,38 @@ namespace moe {
 
 namespace {
 
-// 8 values of a row of bf16 or fp32, as fp32
+// 8 neighbouring values of a row of bf16 or fp32, as loaded
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-    if (F32) {
-        const u32x4 a = __builtin_nontemporal_load((const u32x4*)((const float*)p + i));
-        const u32x4 b = __builtin_nontemporal_load((const u32x4*)((const float*)p + i) + 1);
+struct Raw8 {
+    u32x4 w[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw(const void* p, int64_t i) {
+    Raw8<F32> r;
+    const u32x4* q = (const u32x4*)((const char*)p + i * (F32 ? 4 : 2));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = __uint_as_float(a[k]);
-            v[4 + k] = __uint_as_float(b[k]);
-        }
-    } else {
-        const u32x4 a = __builtin_nontemporal_load((const u32x4*)((const bf16_t*)p + i));
+    for (int k = 0; k < (F32 ? 2 : 1); ++k) r.w[k] = __builtin_nontemporal_load(q + k);
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void unpack(const Raw8<F32>& r, float (&v)[8]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[2 * k] = lo_bf16(a[k]);
-            v[2 * k + 1] = hi_bf16(a[k]);
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (F32) {
+            v[k] = __uint_as_float(r.w[0][k]);
+            v[4 + k] = __uint_as_float(r.w[1][k]);
+        } else {
+            v[2 * k] = lo_bf16(r.w[0][k]);
+            v[2 * k + 1] = hi_bf16(r.w[0][k]);
         }
     }
 }
 
 template <bool F32>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
-    if (F32) {
+    if constexpr (F32) {
         u32x4 a, b;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -70,39 +83,82 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
 // 8 weights (gamma or beta) of either type; `fill` where there are none
 __device__ __forceinline__ void load_w8(const void* p, int f32, int64_t i, float fill,
                                         float (&v)[8]) {
+    if (!p) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = fill;
-    if (!p) return;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        v[k] = f32 ? ((const float*)p)[i + k] : bf16_to_f32(((const bf16_t*)p)[i + k]);
-}
-
-// Sum of N values over the kWpr waves of a row; every lane gets it.  `red`
-// holds the partial sums of the workgroup's waves; two calls in a row use
-// different ones, so one barrier per call is enough.
-template <int kWpr, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N]) {
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) v[n] += __shfl_xor(v[n], o);
-    if (kWpr == 1) return;
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0)
-#pragma unroll
-        for (int n = 0; n < N; ++n) red[wave][n] = v[n];
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        v[n] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWpr; ++w) v[n] += red[w][n];
+        for (int k = 0; k < 8; ++k) v[k] = fill;
+    } else if (f32) {
+        Raw8<true> r;
+        r.w[0] = ((const u32x4*)((const float*)p + i))[0];
+        r.w[1] = ((const u32x4*)((const float*)p + i))[1];
+        unpack<true>(r, v);
+    } else {
+        Raw8<false> r;
+        r.w[0] = *(const u32x4*)((const bf16_t*)p + i);
+        unpack<false>(r, v);
     }
 }
 
-constexpr int rows_per_wg(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }
-constexpr int threads_per_wg(int wpr) { return wpr >= 4 ? 64 * wpr : 256; }
+// A kernel's shape: kRows rows side by side in a workgroup, on each kWpr waves
+// or, where a row is short, kLanes lanes of a wave; kV steps of 8 values per
+// lane.
+template <int kLanes_, int kWpr_, int kV_, int kRows_>
+struct Shape {
+    static constexpr int kLanes = kLanes_, kWpr = kWpr_, kV = kV_, kRows = kRows_;
+    static_assert(kLanes == 64 || kWpr == 1, "whole waves on a long row");
+    static constexpr int kPer = kLanes * kWpr;         // lanes on a row
+    static constexpr int kThreads = kPer * kRows;
+    // Rows so wide (above 16384) that gamma and a prefetched row no longer fit
+    // beside the row: gamma and beta are read again for every row (from L2),
+    // and nothing is prefetched.
+    static constexpr bool kLean = kV * kWpr > 32;
+
+    // The thread's row in the workgroup, the same for a whole wave when a row
+    // has one, and its place on it.
+    static __device__ __forceinline__ int row() {
+        if (kLanes < 64) return (int)threadIdx.x / kPer;
+        return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) / kWpr;
+    }
+    static __device__ __forceinline__ int place() { return (int)threadIdx.x % kPer; }
+};
+
+// Sum of N values over the lanes of a row; every lane gets it.  `red` holds
+// the partial sums of the workgroup's waves; two calls in a row use different
+// ones, so one barrier per call is enough.
+template <class S, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N]) {
+    if constexpr (S::kLanes < 64) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = group_sum<S::kLanes>(v[n]);
+        return;
+    } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
+        if constexpr (S::kWpr > 1) {
+            const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+            if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                for (int n = 0; n < N; ++n) red[wave][n] = v[n];
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                v[n] = 0.f;
+#pragma unroll
+                for (int w = 0; w < S::kWpr; ++w) v[n] += red[S::row() * S::kWpr + w][n];
+            }
+        }
+    }
+}
+
+// v^-1/2 to half an ulp: the hardware's estimate and one Newton step with the
+// product's rounding error carried along (the ends of the range go through
+// the division).
+__device__ __forceinline__ float inv_sqrt(float v) {
+    if (!(v >= 1.17549435e-38f && v <= 3.0e38f)) return 1.f / sqrtf(v);
+    const float y = __builtin_amdgcn_rsqf(v);
+    const float h = v * y;
+    const float e = __builtin_fmaf(-h, y, 1.f) - __builtin_fmaf(v, y, -h) * y;
+    return __builtin_fmaf(0.5f * e, y, y);
+}
 
 struct LnFwd {
     const void* x;
@@ -119,70 +175,82 @@ struct LnFwd {
     float eps;
 };
 
-template <bool XF32, int kWpr, int kV>
-__global__ __launch_bounds__(threads_per_wg(kWpr)) void ln_fwd_kernel(LnFwd a) {
+template <bool XF32, class S>
+__global__ __launch_bounds__(S::kThreads) void ln_fwd_kernel(LnFwd a) {
+    constexpr int kV = S::kV, kPer = S::kPer;
     __shared__ float red[2][16][1];
-    constexpr int kRows = rows_per_wg(kWpr);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int l = (wave % kWpr) * 64 + lane;
+    const int l = S::place();
     const int nc = a.H / 8;
-    float gm[kV][8], bt[kV][8];
+    const float inv = 1.f / (float)a.H;
+    const int64_t step = (int64_t)gridDim.x * S::kRows;
+    int64_t r0 = (int64_t)blockIdx.x * S::kRows;    // the same for the workgroup
+    const int mine = S::row();
+    Raw8<XF32> next[kV];
+    auto load = [&](int64_t row) {
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-        const int c = l + v * 64 * kWpr;
+        for (int v = 0; v < kV; ++v) {
+            const int c = l + v * kPer;
+            next[v] = Raw8<XF32>{};
+            if (row < a.T && c < nc) next[v] = load_raw<XF32>(a.x, row * a.H + c * 8);
+        }
+    };
+    load(r0 + mine);
+    float gm[kV][8], bt[kV][8];
+    auto load_w = [&](int v) {
+        const int c = l + v * kPer;
         load_w8(c < nc ? a.gamma : nullptr, a.w_f32, (int64_t)c * 8, 1.f, gm[v]);
         load_w8(c < nc ? a.beta : nullptr, a.w_f32, (int64_t)c * 8, 0.f, bt[v]);
-    }
-    const float inv = 1.f / (float)a.H;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.T; r0 += (int64_t)gridDim.x * kRows) {
-        const int64_t r = r0 + wave / kWpr;      // one row for all waves of a barrier
-        const bool live = r < a.T;
+    };
+    if (!S::kLean)
+#pragma unroll
+        for (int v = 0; v < kV; ++v) load_w(v);
+    for (; r0 < a.T; r0 += step) {
+        const int64_t r = r0 + mine;
         float x[kV][8];
         float s[1] = {0.f};
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            const int c = l + v * 64 * kWpr;
-            if (live && c < nc)
-                load8<XF32>(a.x, r * a.H + c * 8, x[v]);
-            else
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[v][k] = 0.f;
+            unpack<XF32>(next[v], x[v]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) s[0] += x[v][k];
         }
-        row_sum<kWpr, 1>(s, red[0]);
+        if (!S::kLean) load(r + step);      // the next row's, in flight through this row's work
+        row_sum<S, 1>(s, red[0]);
         const float mean = s[0] * inv;
         float q[1] = {0.f};
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            const bool in = l + v * 64 * kWpr < nc;
+            const bool in = l + v * kPer < nc;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 x[v][k] = in ? x[v][k] - mean : 0.f;
                 q[0] += x[v][k] * x[v][k];
             }
         }
-        row_sum<kWpr, 1>(q, red[1]);
-        const float rstd = 1.f / sqrtf(q[0] * inv + a.eps);
-        if (!live) continue;
-        if (l == 0) {
-            if (a.mean) a.mean[r] = mean;
-            if (a.rstd) a.rstd[r] = rstd;
-        }
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            const int c = l + v * 64 * kWpr;
-            if (c >= nc) continue;
-            float y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                x[v][k] *= rstd;
-                y[k] = x[v][k] * gm[v][k] + bt[v][k];
+        row_sum<S, 1>(q, red[1]);
+        const float rstd = inv_sqrt(q[0] * inv + a.eps);
+        if (r < a.T) {
+            if (l == 0) {
+                if (a.mean) a.mean[r] = mean;
+                if (a.rstd) a.rstd[r] = rstd;
             }
-            store8<false>(a.y, r * a.H + c * 8, y);
-            if (a.codes) mx_store8(x[v], a.codes + r * a.H + c * 8,
-                                   a.scales + r * (a.H / 32) + c / 4);
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                const int c = l + v * kPer;
+                if (c >= nc) continue;
+                if (S::kLean) load_w(v);
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    x[v][k] *= rstd;
+                    y[k] = x[v][k] * gm[v][k] + bt[v][k];
+                }
+                store8<false>(a.y, r * a.H + c * 8, y);
+                if (a.codes) mx_store8(x[v], a.codes + r * a.H + c * 8,
+                                       a.scales + r * (a.H / 32) + c / 4);
+            }
         }
+        if (S::kLean) load(r + step);
     }
 }
 
@@ -204,127 +272,288 @@ struct LnBwd {
 
 enum LnSaved { LN_BF16 = 0, LN_F32 = 1, LN_MX_BF16 = 2, LN_MX_F32 = 3 };  // xh from x or from codes; dx type
 
-template <int kSaved, int kWpr, int kV>
-__global__ __launch_bounds__(threads_per_wg(kWpr)) void ln_bwd_kernel(LnBwd a) {
+// 8 values of xh as they are kept: x's words, or 8 codes and their scale
+template <int kSaved>
+struct SavedRaw {
+    Raw8<kSaved == LN_F32> x;
+};
+template <>
+struct SavedRaw<LN_MX_BF16> {
+    u32x2 codes;
+    uint32_t scale;
+};
+template <>
+struct SavedRaw<LN_MX_F32> : SavedRaw<LN_MX_BF16> {};
+
+// Hides from the compiler that the words are those it has seen: it would keep
+// the unpacked values of the first use, instead of the words, for the second.
+__device__ __forceinline__ void forget(u32x4& w) { asm volatile("" : "+v"(w)); }
+__device__ __forceinline__ void forget(u32x2& w) { asm volatile("" : "+v"(w)); }
+template <bool F32>
+__device__ __forceinline__ void forget(Raw8<F32>& r) {
+#pragma unroll
+    for (int k = 0; k < (F32 ? 2 : 1); ++k) forget(r.w[k]);
+}
+template <int kSaved>
+__device__ __forceinline__ void forget(SavedRaw<kSaved>& r) {
+    if constexpr (kSaved >= LN_MX_BF16) forget(r.codes);
+    else forget(r.x);
+}
+
+// What a row brings: dy, the saved row and the residual's gradient, as loaded.
+// They are unpacked twice, for the sums and for dx: fewer registers than the
+// fp32 values would hold over the sums.
+template <int kSaved, int kV>
+struct LnRow {
+    float rstd, mean;
+    Raw8<false> dy[kV];
+    SavedRaw<kSaved> x[kV];
+};
+
+// kSums: also the weights' gradients, one partial row of 2H floats per workgroup.
+template <int kSaved, class S, bool kSums>
+__global__ __launch_bounds__(S::kThreads) void ln_bwd_kernel(LnBwd a) {
     constexpr bool XF32 = kSaved == LN_F32 || kSaved == LN_MX_F32;
     constexpr bool kMx = kSaved >= LN_MX_BF16;
-    constexpr int kRows = rows_per_wg(kWpr);
+    constexpr int kV = S::kV, kRows = S::kRows, kPer = S::kPer;
+    constexpr int kPart = kRows * S::kLanes / 64;   // rows left after each wave has added its own
+    // The next row is loaded during the current one where dx is fp32; with
+    // the smaller bf16 rows the other waves hide the loads as well, with
+    // fewer registers (16384 x 2048: fp32 69 against 73 us without, bf16 45.5
+    // against 44.0).
+    constexpr bool kPrefetch = XF32 && !S::kLean;
     __shared__ float red[2][16][2];
-    __shared__ float comb[kRows > 1 ? kRows : 1][kRows > 1 ? 64 * kV * 8 : 1];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int l = (wave % kWpr) * 64 + lane;
+    __shared__ float comb[kSums && kPart > 1 ? 8 * kPer * kV : 1];
+    const int l = S::place();
     const int nc = a.H / 8;
-    float gm[kV][8], dg[kV][8], db[kV][8];
+    const float inv = 1.f / (float)a.H;
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t r0 = (int64_t)blockIdx.x * kRows;       // the same for the workgroup
+    const int mine = S::row();
+    using Row = LnRow<kSaved, kV>;
+    auto load = [&](int64_t row, Row& n) {
+        const bool live = row < a.T;
+        n.rstd = live ? a.rstd[row] : 0.f;
+        n.mean = !kMx && live ? a.mean[row] : 0.f;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            const int c = l + v * kPer;
+            n.dy[v] = Raw8<false>{};
+            n.x[v] = SavedRaw<kSaved>{};
+            if (live && c < nc) {
+                const int64_t at = row * a.H + c * 8;
+                n.dy[v] = load_raw<false>(a.dy, at);
+                if constexpr (kMx) {
+                    n.x[v].codes = __builtin_nontemporal_load((const u32x2*)(a.codes + at));
+                    n.x[v].scale = a.scales[row * (a.H / 32) + c / 4];
+                } else {
+                    n.x[v].x = load_raw<XF32>(a.x, at);
+                }
+            }
+        }
+    };
+    // step v of a row: dy and xh.  (A lane past the row's end holds dy = 0 and
+    // some finite xh, which adds nothing to any sum.)
+    auto values = [&](const Row& w, int v, float (&dy)[8], float (&xh)[8]) {
+        unpack<false>(w.dy[v], dy);
+        if constexpr (kMx) {
+            mx_decode8(w.x[v].codes, w.x[v].scale, xh);
+        } else {
+            unpack<XF32>(w.x[v].x, xh);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) xh[k] = (xh[k] - w.mean) * w.rstd;
+        }
+    };
+    Row next;
+    load(r0 + mine, next);
+    float gm[kV][8];
+    float dg[kSums ? kV : 1][8], db[kSums ? kV : 1][8];
+    auto load_w = [&](int v) {
+        const int c = l + v * kPer;
+        load_w8(c < nc ? a.gamma : nullptr, a.w_f32, (int64_t)c * 8, 1.f, gm[v]);
+    };
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-        const int c = l + v * 64 * kWpr;
-        load_w8(c < nc ? a.gamma : nullptr, a.w_f32, (int64_t)c * 8, 1.f, gm[v]);
+        if (!S::kLean) load_w(v);
+        if constexpr (kSums)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dg[v][k] = db[v][k] = 0.f;
+            for (int k = 0; k < 8; ++k) dg[v][k] = db[v][k] = 0.f;
     }
-    const float inv = 1.f / (float)a.H;
     int flip = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.T; r0 += (int64_t)gridDim.x * kRows) {
-        const int64_t r = r0 + wave / kWpr;
-        const bool live = r < a.T;
-        const float rstd = live ? a.rstd[r] : 0.f;
-        const float mean = (!kMx && live) ? a.mean[r] : 0.f;
-        float xh[kV][8], dy[kV][8];
+    for (; r0 < a.T; r0 += step) {
+        const int64_t r = r0 + mine;
+        Row row = next;
+        Raw8<XF32> res[kV];                     // the residual's gradient, used last
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            const int c = l + v * kPer;
+            res[v] = Raw8<XF32>{};
+            if (a.dres && r < a.T && c < nc) res[v] = load_raw<XF32>(a.dres, r * a.H + c * 8);
+        }
+        if (kPrefetch) load(r + step, next);    // in flight through this row's work
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            const int c = l + v * 64 * kWpr;
-            if (live && c < nc) {
-                load8<false>(a.dy, r * a.H + c * 8, dy[v]);
-                if (kMx) {
-                    mx_load8(a.codes + r * a.H + c * 8, a.scales + r * (a.H / 32) + c / 4, xh[v]);
-                } else {
-                    load8<XF32>(a.x, r * a.H + c * 8, xh[v]);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) xh[v][k] = (xh[v][k] - mean) * rstd;
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) dy[v][k] = xh[v][k] = 0.f;
-            }
+            float dy[8], xh[8];
+            if (S::kLean) load_w(v);
+            values(row, v, dy, xh);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float g = dy[v][k] * gm[v][k];
+                const float g = dy[k] * gm[v][k];
                 s[0] += g;
-                s[1] += g * xh[v][k];
-                dg[v][k] += dy[v][k] * xh[v][k];
-                db[v][k] += dy[v][k];
+                s[1] += g * xh[k];
+                if constexpr (kSums) {
+                    dg[v][k] += dy[k] * xh[k];
+                    db[v][k] += dy[k];
+                }
             }
         }
-        row_sum<kWpr, 2>(s, red[flip]);
+        row_sum<S, 2>(s, red[flip]);
         flip ^= 1;
-        if (!live) continue;
         const float c1 = s[0] * inv, c2 = s[1] * inv;
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            const int c = l + v * 64 * kWpr;
-            if (c >= nc) continue;
-            float d[8], o[8];
-            if (a.dres)
-                load8<XF32>(a.dres, r * a.H + c * 8, d);
-            else
-#pragma unroll
-                for (int k = 0; k < 8; ++k) d[k] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                o[k] = rstd * (dy[v][k] * gm[v][k] - c1 - xh[v][k] * c2) + d[k];
-            store8<XF32>(a.dx, r * a.H + c * 8, o);
+            forget(row.dy[v]);
+            forget(row.x[v]);
         }
-    }
-    if (!a.part) return;
-    float* out = a.part + (int64_t)blockIdx.x * 2 * a.H;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (kRows > 1) {   // the workgroup's rows are added in wave order
-            if (which) __syncthreads();
-#pragma unroll
-            for (int v = 0; v < kV; ++v)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    comb[wave][(v * 64 + lane) * 8 + k] = which ? db[v][k] : dg[v][k];
-            __syncthreads();
-            for (int i = threadIdx.x; i < a.H; i += threads_per_wg(kWpr)) {
-                float t = 0.f;
-#pragma unroll
-                for (int w = 0; w < kRows; ++w) t += comb[w][i];
-                out[which * a.H + i] = t;
-            }
-        } else {
+        if (r < a.T) {
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
-                const int c = l + v * 64 * kWpr;
+                const int c = l + v * kPer;
                 if (c >= nc) continue;
-                float4* o = (float4*)(out + which * a.H + c * 8);
-                const float* t = which ? db[v] : dg[v];
-                o[0] = make_float4(t[0], t[1], t[2], t[3]);
-                o[1] = make_float4(t[4], t[5], t[6], t[7]);
+                float dy[8], xh[8], d[8], o[8];
+                if (S::kLean) load_w(v);
+                values(row, v, dy, xh);
+                unpack<XF32>(res[v], d);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    o[k] = row.rstd * (dy[k] * gm[v][k] - c1 - xh[k] * c2) + d[k];
+                store8<XF32>(a.dx, r * a.H + c * 8, o);
+            }
+        }
+        if (!kPrefetch) load(r + step, next);
+    }
+    if constexpr (!kSums) return;
+    float* out = a.part + (int64_t)blockIdx.x * 2 * a.H;
+    const int part = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) / S::kWpr;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        // the rows of a wave, then the workgroup's in order through LDS
+        if constexpr (S::kLanes < 64)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float& t = which ? db[0][k] : dg[0][k];
+                static_assert(S::kLanes == 64 || kV == 1, "short rows have one step");
+                if (S::kLanes == 16) t += __shfl_xor(t, 16);
+                t += __shfl_xor(t, 32);
+            }
+#pragma unroll
+        for (int w = 0; w < kPart; ++w) {
+            if (kPart > 1) __syncthreads();
+            if (part != w || (S::kLanes < 64 && (threadIdx.x & 63) >= S::kLanes)) continue;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                const int c = l + v * kPer;
+                if (c >= nc) continue;
+                float4 t[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float* q = which ? &db[v][4 * h] : &dg[v][4 * h];
+                    t[h] = make_float4(q[0], q[1], q[2], q[3]);
+                    if (kPart > 1) {
+                        float4* m = (float4*)comb + 2 * c + h;
+                        if (w > 0) {
+                            const float4 o = *m;
+                            t[h] = make_float4(o.x + t[h].x, o.y + t[h].y, o.z + t[h].z, o.w + t[h].w);
+                        }
+                        if (w < kPart - 1) *m = t[h];
+                    }
+                    if (w == kPart - 1) ((float4*)(out + which * a.H))[2 * c + h] = t[h];
+                }
             }
         }
     }
 }
 
+// The weights' gradients of rows too wide for a workgroup to hold their sums
+// beside the row: a second read of dy and of the saved rows.  A wave has 512
+// columns; workgroup (x, y) adds rows y, y + gridDim.y, .. of 4 waves each and
+// writes its columns of partial row y.
+template <int kSaved>
+__global__ __launch_bounds__(256) void ln_cols_kernel(LnBwd a) {
+    constexpr bool kMx = kSaved >= LN_MX_BF16;
+    __shared__ float comb[3][2][512];
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int lane = threadIdx.x & 63;
+    const int c = blockIdx.x * 64 + lane;
+    const bool in = c < a.H / 8;
+    float dg[8], db[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dg[k] = db[k] = 0.f;
+#pragma unroll 4
+    for (int64_t r = (int64_t)blockIdx.y * 4 + wave; r < a.T; r += (int64_t)gridDim.y * 4) {
+        if (!in) continue;
+        const int64_t at = r * a.H + c * 8;
+        float dy[8], xh[8];
+        unpack<false>(load_raw<false>(a.dy, at), dy);
+        if constexpr (kMx) {
+            mx_load8(a.codes + at, a.scales + r * (a.H / 32) + c / 4, xh);
+        } else {
+            unpack<kSaved == LN_F32>(load_raw<kSaved == LN_F32>(a.x, at), xh);
+            const float mean = a.mean[r], rstd = a.rstd[r];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) xh[k] = (xh[k] - mean) * rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            dg[k] += dy[k] * xh[k];
+            db[k] += dy[k];
+        }
+    }
+    if (wave > 0)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            comb[wave - 1][0][k * 64 + lane] = dg[k];
+            comb[wave - 1][1][k * 64 + lane] = db[k];
+        }
+    __syncthreads();
+    if (wave > 0 || !in) return;
+    float* out = a.part + (int64_t)blockIdx.y * 2 * a.H + c * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+            dg[k] += comb[w][0][k * 64 + lane];
+            db[k] += comb[w][1][k * 64 + lane];
+        }
+        out[k] = dg[k];
+        out[a.H + k] = db[k];
+    }
+}
+
 // dgamma (columns [0, H)) and dbeta ([H, 2H)): the np partial rows added in a
-// fixed order, 64 columns per workgroup, 16 waves over the rows.
+// fixed order.  A workgroup has 16 columns (64 bytes of a partial row) and 64
+// threads on each, every one with every 64th row: few dependent loads, and
+// enough workgroups to cover the chip at usual widths.
 __global__ __launch_bounds__(1024) void ln_dw_reduce_kernel(const float* __restrict__ part, int np,
                                                             int H, int w_f32, void* dgamma,
                                                             void* dbeta) {
-    __shared__ float red[16][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int i = blockIdx.x * 64 + lane;
+    __shared__ float red[64][17];
+    const int q = threadIdx.x >> 4, col = threadIdx.x & 15;
+    const int i = blockIdx.x * 16 + col;                 // 2H is a multiple of 16
     float t = 0.f;
-    if (i < 2 * H)
-        for (int p = wave; p < np; p += 16) t += part[(int64_t)p * 2 * H + i];
-    red[wave][lane] = t;
+#pragma unroll 8
+    for (int p = q; p < np; p += 64) t += part[(int64_t)p * 2 * H + i];
+    red[q][col] = t;
     __syncthreads();
-    if (wave != 0 || i >= 2 * H) return;
+    if (threadIdx.x >= 64) return;
+    const int q4 = threadIdx.x >> 4;                     // 4 threads per column, 16 rows each
     t = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) t += red[w][lane];
+    for (int w = 0; w < 16; ++w) t += red[q4 * 16 + w][col];
+    t += __shfl_xor(t, 16);
+    t += __shfl_xor(t, 32);
+    if (q4) return;
     void* o = i < H ? dgamma : dbeta;
     const int c = i < H ? i : i - H;
     if (!o) return;
@@ -332,56 +561,99 @@ __global__ __launch_bounds__(1024) void ln_dw_reduce_kernel(const float* __restr
     else ((bf16_t*)o)[c] = (bf16_t)f32_to_bf16(t);
 }
 
-// Waves per row: as few as hold a row with at most 4 steps (32 values) per
-// lane, so that a row's sums need few or no barriers.
-int ln_wpr(int H) { return H <= 2048 ? 1 : H <= 8192 ? 4 : 16; }
-int ln_steps(int H, int wpr) {
-    const int per = 512 * wpr;
-    const int v = (H + per - 1) / per;
-    return v <= 1 ? 1 : v <= 2 ? 2 : 4;
+// The forward's shapes by width: few waves on a row and 2 steps.
+template <class F>
+void with_fwd_shape(int H, F&& f) {
+    if (H <= 128) f(Shape<16, 1, 1, 16>{});
+    else if (H <= 256) f(Shape<32, 1, 1, 16>{});
+    else if (H <= 512) f(Shape<64, 1, 1, 8>{});
+    else if (H <= 1024) f(Shape<64, 1, 2, 8>{});
+    else if (H <= 2048) f(Shape<64, 2, 2, 4>{});
+    else if (H <= 4096) f(Shape<64, 4, 2, 2>{});
+    else if (H <= 8192) f(Shape<64, 8, 2, 1>{});
+    else if (H <= 16384) f(Shape<64, 16, 2, 1>{});
+    else f(Shape<64, 16, 4, 1>{});
 }
 
-// Workgroups of the backward: each writes a partial row of 2H floats.
-int ln_bwd_groups(int64_t T, int H) {
-    const int rows = rows_per_wg(ln_wpr(H));
-    const int64_t need = (T + rows - 1) / rows;
-    const int64_t cap = 512;
-    return (int)(need < cap ? need : cap);
+// The backward's: one step per lane, since every column of a row also has two
+// running sums, and many rows side by side, since every workgroup writes a
+// partial row of them.  (16384 x 2048 from codes: 42 us; with 4 steps of one
+// wave on a row 83 us, the registers leaving one wave per SIMD; with half as
+// many rows in a workgroup and twice the workgroups 47 us.)  Rows above 8192
+// would spill their sums: those are added by a kernel of their own, which
+// reads the rows again (2048 x 16384: 60 us; with the sums beside the row 76).
+constexpr int kLnSumsH = 8192;      // wider: the sums in a kernel of their own
+template <class F>
+void with_bwd_shape(int H, F&& f) {
+    if (H <= 128) f(Shape<16, 1, 1, 32>{});
+    else if (H <= 256) f(Shape<32, 1, 1, 16>{});
+    else if (H <= 512) f(Shape<64, 1, 1, 8>{});
+    else if (H <= 1024) f(Shape<64, 2, 1, 8>{});
+    else if (H <= 2048) f(Shape<64, 4, 1, 4>{});
+    else if (H <= 4096) f(Shape<64, 8, 1, 2>{});
+    else if (H <= 8192) f(Shape<64, 16, 1, 1>{});
+    else if (H <= 16384) f(Shape<64, 16, 2, 1>{});
+    else f(Shape<64, 16, 4, 1>{});
 }
 
-template <bool XF32, int kWpr, int kV>
-void run_fwd(const LnFwd& a, hipStream_t s) {
-    const int64_t need = (a.T + rows_per_wg(kWpr) - 1) / rows_per_wg(kWpr);
-    const int64_t cap = kWpr == 16 ? 512 : 2048;
-    ln_fwd_kernel<XF32, kWpr, kV>
-        <<<(unsigned)(need < cap ? need : cap), threads_per_wg(kWpr), 0, s>>>(a);
+// Workgroups: enough to fill the chip's waves once (each walks over rows).
+template <class S>
+unsigned groups_of(int64_t T, int per_cu) {
+    const int64_t need = (T + S::kRows - 1) / S::kRows, cap = 256 * per_cu;
+    return (unsigned)(need < cap ? need : cap);
 }
-template <int kSaved, int kWpr, int kV>
-void run_bwd(const LnBwd& a, int groups, hipStream_t s) {
-    ln_bwd_kernel<kSaved, kWpr, kV><<<(unsigned)groups, threads_per_wg(kWpr), 0, s>>>(a);
+template <class S>
+unsigned fwd_groups(int64_t T) {
+    return groups_of<S>(T, S::kThreads >= 1024 ? 1 : S::kThreads >= 512 ? 2 : 4);
+}
+template <class S>
+unsigned bwd_groups(int64_t T) {
+    return groups_of<S>(T, S::kThreads >= 1024 ? 1 : 2);
+}
+
+// Partial rows of the weights' gradients.
+int ln_parts(int64_t T, int H) {
+    if (H > kLnSumsH) {     // about 1024 workgroups of the column kernel
+        const int64_t need = (T + 3) / 4, cap = 1024 / ((H + 511) / 512);
+        return (int)(need < cap ? need : cap);
+    }
+    int n = 0;
+    with_bwd_shape(H, [&](auto s) { n = (int)bwd_groups<decltype(s)>(T); });
+    return n;
 }
 
 template <bool XF32>
-void pick_fwd(const LnFwd& a, hipStream_t s) {
-    const int w = ln_wpr(a.H), v = ln_steps(a.H, w);
-#define LN_CASE(W, V) if (w == W && v == V) return run_fwd<XF32, W, V>(a, s);
-    LN_CASE(1, 1) LN_CASE(1, 2) LN_CASE(1, 4) LN_CASE(4, 2) LN_CASE(4, 4) LN_CASE(16, 2)
-    LN_CASE(16, 4)
-#undef LN_CASE
+void run_fwd(const LnFwd& a, hipStream_t s) {
+    with_fwd_shape(a.H, [&](auto sh) {
+        using S = decltype(sh);
+        ln_fwd_kernel<XF32, S><<<fwd_groups<S>(a.T), S::kThreads, 0, s>>>(a);
+    });
 }
 template <int kSaved>
-void pick_bwd(const LnBwd& a, int groups, hipStream_t s) {
-    const int w = ln_wpr(a.H), v = ln_steps(a.H, w);
-#define LN_CASE(W, V) if (w == W && v == V) return run_bwd<kSaved, W, V>(a, groups, s);
-    LN_CASE(1, 1) LN_CASE(1, 2) LN_CASE(1, 4) LN_CASE(4, 2) LN_CASE(4, 4) LN_CASE(16, 2)
-    LN_CASE(16, 4)
-#undef LN_CASE
+hipError_t run_bwd(const LnBwd& a, hipStream_t s) {
+    const bool sums = a.part && a.H <= kLnSumsH;
+    if (a.part && !sums) {
+        TraceScope ts("layernorm_cols", s);
+        ln_cols_kernel<kSaved><<<dim3((unsigned)((a.H + 511) / 512), (unsigned)ln_parts(a.T, a.H)),
+                                 256, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    TraceScope ts("layernorm_bwd", s);
+    with_bwd_shape(a.H, [&](auto sh) {
+        using S = decltype(sh);
+        if (!sums)
+            ln_bwd_kernel<kSaved, S, false><<<bwd_groups<S>(a.T), S::kThreads, 0, s>>>(a);
+        else if constexpr (8 * S::kPer * S::kV <= kLnSumsH)
+            ln_bwd_kernel<kSaved, S, true><<<bwd_groups<S>(a.T), S::kThreads, 0, s>>>(a);
+    });
+    return hipGetLastError();
 }
 
 }  // namespace
 
 size_t layernorm_workspace_bytes(int64_t T, int H) {
-    return (size_t)ln_bwd_groups(T, H) * 2 * (size_t)H * sizeof(float) + 256;
+    return (size_t)ln_parts(T, H) * 2 * (size_t)H * sizeof(float) + 256;
 }
 
 hipError_t launch_layernorm_fwd(const void* x, bool x_f32, int64_t T, int H, const void* gamma,
@@ -390,8 +662,8 @@ hipError_t launch_layernorm_fwd(const void* x, bool x_f32, int64_t T, int H, con
     if (T == 0) return hipSuccess;
     LnFwd a{x, gamma, beta, y, mean, rstd, codes, scales, T, H, w_f32 ? 1 : 0, eps};
     TraceScope ts("layernorm_fwd", s);
-    if (x_f32) pick_fwd<true>(a, s);
-    else pick_fwd<false>(a, s);
+    if (x_f32) run_fwd<true>(a, s);
+    else run_fwd<false>(a, s);
     return hipGetLastError();
 }
 
@@ -400,25 +672,17 @@ hipError_t launch_layernorm_bwd(const bf16_t* dy, const void* x, bool x_f32, con
                                 int64_t T, int H, const void* gamma, bool w_f32, const void* dres,
                                 void* dx, void* dgamma, void* dbeta, void* ws, hipStream_t s) {
     const bool want = dgamma || dbeta;
-    const int groups = ln_bwd_groups(T, H);
     if (T > 0) {
         LnBwd a{dy, x, mean, rstd, codes, scales, gamma, dres, dx, want ? (float*)ws : nullptr,
                 T, H, w_f32 ? 1 : 0};
-        TraceScope ts("layernorm_bwd", s);
-        if (codes) {
-            if (x_f32) pick_bwd<LN_MX_F32>(a, groups, s);
-            else pick_bwd<LN_MX_BF16>(a, groups, s);
-        } else {
-            if (x_f32) pick_bwd<LN_F32>(a, groups, s);
-            else pick_bwd<LN_BF16>(a, groups, s);
-        }
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = codes ? (x_f32 ? run_bwd<LN_MX_F32>(a, s) : run_bwd<LN_MX_BF16>(a, s))
+                                   : (x_f32 ? run_bwd<LN_F32>(a, s) : run_bwd<LN_BF16>(a, s));
         if (e != hipSuccess) return e;
     }
     if (!want) return hipSuccess;
     TraceScope ts("layernorm_dw_reduce", s);
-    ln_dw_reduce_kernel<<<(unsigned)((2 * H + 63) / 64), 1024, 0, s>>>(
-        (const float*)ws, groups, H, w_f32 ? 1 : 0, dgamma, dbeta);
+    ln_dw_reduce_kernel<<<(unsigned)(2 * H / 16), 1024, 0, s>>>(
+        (const float*)ws, ln_parts(T, H), H, w_f32 ? 1 : 0, dgamma, dbeta);
     return hipGetLastError();
 }
 

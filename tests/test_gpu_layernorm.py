@@ -93,7 +93,7 @@ def _fwd_case(T, H, xt, wt, ckpt, seed=0, eps=1e-5, affine=True):
 
 
 SIZES = [(1, 8), (1, 4096), (3, 40), (5, 64), (257, 96), (130, 512), (66, 520), (1001, 1416), (37, 2048),
-         (9, 2056), (300, 4096), (33, 4104), (17, 8192), (5, 8200), (3, 16384), (2, 16392), (2, 32768)]
+         (9, 2056), (301, 128), (67, 136), (33, 256), (7, 264), (300, 4096), (33, 4104), (17, 8192), (5, 8200), (3, 16384), (2, 16392), (2, 32768)]
 
 
 @pytest.mark.parametrize("T,H", SIZES)
@@ -111,6 +111,7 @@ def test_forward_without_weights():
 def test_forward_many_rows():
     say("layernorm fwd, more rows than workgroups at once")
     _fwd_case(9001, 256, F32, F32, True, seed=5)
+    _fwd_case(20003, 128, BF, F32, True, seed=6)
 
 
 def _xh32(x, mean, rstd):
@@ -186,6 +187,7 @@ def test_backward_wanted_gradients(want):
 def test_backward_many_rows():
     say("layernorm bwd, many rows")
     _bwd_case(20011, 128, BF, F32, False, False, seed=9)
+    _bwd_case(20011, 256, BF, F32, True, False, seed=9)
 
 
 def test_constant_rows_and_zero_rows():
