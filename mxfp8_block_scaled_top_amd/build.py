@@ -24,9 +24,9 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libmoe_mi355x.so")
 ARCH = "gfx950"
 
-SOURCES = ["route.hip", "router.hip", "permute.hip", "mxfp8.hip", "gemm.hip", "check.hip",
-           "layernorm.hip", "swiglu.hip", "capi.cpp", "mlp.cpp", "linear.cpp", "sublayer.cpp",
-           "trace.cpp"]
+SOURCES = ["route.hip", "router.hip", "permute.hip", "mxfp8.hip", "gemm.hip", "gemm_few.hip",
+           "check.hip", "layernorm.hip", "swiglu.hip", "capi.cpp", "mlp.cpp", "linear.cpp",
+           "sublayer.cpp", "trace.cpp"]
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17",

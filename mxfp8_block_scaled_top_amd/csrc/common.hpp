@@ -161,6 +161,17 @@ __device__ __forceinline__ void mx_store8(const float (&x)[8], uint8_t* codes, u
     if ((threadIdx.x & 3) == 0) *scale = (uint8_t)S;
 }
 
+// The values of 4 codes of one block.
+__device__ __forceinline__ void mx_decode4(uint32_t w, uint32_t S, float (&x)[4]) {
+    const float scale = __builtin_ldexpf(1.f, (int)S - 127);
+    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, false);
+    const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, true);
+    x[0] = a[0];
+    x[1] = a[1];
+    x[2] = b[0];
+    x[3] = b[1];
+}
+
 // The values of 8 neighbouring codes of one block.
 __device__ __forceinline__ void mx_decode8(u32x2 w, uint32_t S, float (&x)[8]) {
     const float scale = __builtin_ldexpf(1.f, (int)S - 127);

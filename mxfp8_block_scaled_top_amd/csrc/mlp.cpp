@@ -105,6 +105,7 @@ BwdWs carve_bwd(void* base, int64_t rows, int H, int I, int E, int precision) {
     Carve c(base);
     BwdWs w{};
     int ntn = gemm_n_tiles(EPI_SWIGLU_BWD, I, I);
+    if (precision == MOE_BF16 && use_few_rows(rows, E)) ntn = few_tiles(I);   // narrower tiles
     w.part = (float*)c.take((size_t)rows * ntn * sizeof(float));
     if (precision == MOE_BF16) {
         w.da1 = c.take((size_t)rows * 2 * I * 2);
@@ -359,7 +360,9 @@ int mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp
         set_a1(g, saved, ck);
         g.act = saved->a2;
         g.name = "gemm_bf16_gateup_fwd_swiglu";
-        MOE_TRY(launch_gemm(DT_BF16, U_GATEUP_FWD, g, stream));
+        const bool few = ck.used && use_few_rows(rows, E);
+        MOE_TRY(few ? launch_few(U_GATEUP_FWD, g, stream)
+                    : launch_gemm(DT_BF16, U_GATEUP_FWD, g, stream));
         GemmArgs d = g;
         d.a = saved->a2;
         d.lda = I;
@@ -370,7 +373,8 @@ int mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp
         d.c = yp;
         d.ldc = H;
         d.name = "gemm_bf16_down_fwd";
-        MOE_TRY(launch_gemm(DT_BF16, U_DOWN_FWD, d, stream));
+        MOE_TRY(few ? launch_few(U_DOWN_FWD, d, stream)
+                    : launch_gemm(DT_BF16, U_DOWN_FWD, d, stream));
         return MOE_OK;
     }
     // MXFP8: quantize operands along their contraction axis.  xp: rowwise for
@@ -532,6 +536,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
     // weight-gradient GEMMs run for every expert (empty experts get zeros),
     // even when there are no rows at all
     if (precision == MOE_BF16) {
+        const bool few = ck.used && use_few_rows(rows, E);
         GemmArgs g{};
         g.split = split_sizes;
         g.E = E;
@@ -551,8 +556,13 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             g.act = (bf16_t*)w.da1;
             g.dprob_part = w.part;
             g.name = "gemm_bf16_down_dgrad_swiglu_bwd";
-            MOE_TRY(launch_gemm(DT_BF16, U_DOWN_DGRAD, g, stream));
-            MOE_TRY(launch_dprob_reduce(w.part, rows, ntn, dprob_perm, stream));
+            if (few) {
+                MOE_TRY(launch_few(U_DOWN_DGRAD, g, stream));
+                MOE_TRY(launch_few_dprob(w.part, rows, few_tiles(I), dprob_perm, stream));
+            } else {
+                MOE_TRY(launch_gemm(DT_BF16, U_DOWN_DGRAD, g, stream));
+                MOE_TRY(launch_dprob_reduce(w.part, rows, ntn, dprob_perm, stream));
+            }
         }
         // down wgrad: dW2 [H, I] = dYp^T A2
         GemmArgs wg{};
@@ -586,7 +596,8 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             dg.c = dxp;
             dg.ldc = H;
             dg.name = "gemm_bf16_gateup_dgrad";
-            MOE_TRY(launch_gemm(DT_BF16, U_GATEUP_DGRAD, dg, stream));
+            MOE_TRY(few ? launch_few(U_GATEUP_DGRAD, dg, stream)
+                        : launch_gemm(DT_BF16, U_GATEUP_DGRAD, dg, stream));
         }
         // gate_up wgrad: dW1 [2I, H] = dA1^T Xp
         GemmArgs wg1{};

@@ -4,7 +4,9 @@ the pre-norm sublayer built on it.
 The forward's other outputs are those of grouped_mlp_fwd bit for bit, and the
 backward's are those of grouped_mlp_bwd on the decoded A1 bit for bit, so what
 the tests of those calls show carries over; the codes themselves are held
-against A1 in float64."""
+against A1 in float64.  In BF16 with at most 64 rows per expert on average
+other kernels run (the fp32 sums in another order): those are held against
+float64 throughout."""
 import numpy as np
 import pytest
 import torch
@@ -43,11 +45,14 @@ def _cuda(inp):
 
 
 SIZES = [([300, 0, 1, 399], 384, 640), ([1], 128, 128), ([0, 0, 5], 256, 384), ([257, 31, 513], 128, 1408),
-         ([64] * 16, 256, 256)]
+         ([64] * 16, 256, 256), ([65, 65], 128, 128)]
 
 
-@pytest.mark.parametrize("sizes,H,I", SIZES)
-@pytest.mark.parametrize("precision", ALL, ids=IDS)
+def _few(precision, sizes):
+    return precision == moe.MOE_BF16 and sum(sizes) <= 64 * len(sizes)
+
+
+@pytest.mark.parametrize("precision,sizes,H,I", [(p, *s) for p in ALL for s in SIZES if not _few(p, s[0])])
 def test_against_the_bf16_form(precision, sizes, H, I):
     say(f"mlp ckpt {NAME[precision]} sizes={sizes} H={H} I={I}")
     d = _cuda(_inputs(sizes, H, I, seed=len(sizes) + I))
@@ -105,6 +110,74 @@ def test_codes_against_float64(precision):
     top = a1.abs().reshape(*scales.shape, 32).amax(2)
     slack = err.reshape(*scales.shape, 32).amax(2)
     assert (top <= 448 * Xb + slack).all() and (top >= 224 * Xb - slack).all()
+
+
+FEW = [([1], 128, 128), ([0, 0, 5], 256, 384), ([64] * 16, 256, 256), ([3, 0, 1, 2], 384, 640),
+       ([0, 200, 0, 1, 0, 0, 0, 50], 256, 128), ([16, 17, 15, 64], 128, 1408), ([65, 63], 640, 256),
+       ([2, 2], 128, 4096), ([1, 1, 0, 1], 2048, 128), ([1] * 64, 128, 256), ([0, 0], 128, 128)]
+
+
+@pytest.mark.parametrize("sizes,H,I", FEW)
+def test_few_rows_against_float64(sizes, H, I):
+    """Element by element, u = 2^-24, h = 2^-8 (half a bf16 step): a product of
+    K terms in any order is off by at most K u sum|terms|; SiLU's slope is at
+    most 1.1, its fp32 form off by (2 |g| + 16) u; dA1 enters its products
+    rounded to bf16.  The 2-norm sees two independent roundings of at most
+    h / sqrt(3) each: 0.004 with room."""
+    say(f"mlp ckpt few rows sizes={sizes} H={H} I={I}")
+    inp = _inputs(sizes, H, I, seed=H + I, wstd=0.06)
+    d = _cuda(inp)
+    rows, E, h = sum(sizes), len(sizes), 2.0 ** -8
+    args = (d["split"], d["w1"], d["w2"], d["pp"])
+    yp, s = moe.grouped_mlp_fwd_ckpt(d["xp"], *args, moe.MOE_BF16)
+    dxp, dw1, dw2, dpp = moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s, moe.MOE_BF16)
+    torch.cuda.synchronize()
+    scales = np_(s["a1_scales"]).astype(np.float64)
+    v = torch.from_numpy(omx.dequantize_rows(np_(s["a1_codes"]), np_(s["a1_scales"]))).double().reshape(rows, 2 * I)
+    a2s = s["a2"].double().cpu()
+    got = {"yp": yp, "dxp": dxp, "dpp": dpp}
+    ref = {k: [] for k in got}
+    at = 0
+    for e, n in enumerate(sizes):
+        w1, w2 = inp["w1"][e].double(), inp["w2"][e].double()
+        sl = slice(at, at + n)
+        at += n
+        x, dy, p = inp["xp"][sl].double(), inp["dyp"][sl].double(), inp["pp"][sl].double()[:, None]
+        a1 = x @ w1.T
+        ea = H * U * (x.abs() @ w1.abs().T)
+        if n:
+            X = torch.from_numpy(2.0 ** (scales[sl] - 127)).repeat_interleave(32, 1)
+            assert ((v[sl] - a1).abs() <= torch.maximum(2.0 ** -4 * a1.abs(), 2.0 ** -10 * X) + 1.0625 * ea).all(), e
+            top = a1.abs().reshape(n, -1, 32).amax(2)
+            slack = ea.reshape(n, -1, 32).amax(2)
+            Xb = torch.from_numpy(2.0 ** (scales[sl] - 127))
+            assert (top <= 448 * Xb + slack).all() and (top >= 224 * Xb - slack).all(), e
+        g, u = a1[:, :I], a1[:, I:]
+        a2 = p * torch.nn.functional.silu(g) * u
+        e2 = p * (1.1 * ea[:, :I] * (u.abs() + ea[:, I:]) + torch.nn.functional.silu(g).abs() * ea[:, I:]) \
+            + a2.abs() * (2 * g.abs() + 16) * U
+        assert ((a2s[sl] - a2).abs() <= e2 * 1.01 + h * (a2.abs() + e2) + 1e-37).all(), e
+        ref["yp"].append((a2s[sl] @ w2.T, I * U * (a2s[sl].abs() @ w2.abs().T)))
+        da2 = dy @ w2
+        ed = H * U * (dy.abs() @ w2.abs())
+        g, u = v[sl, :I], v[sl, I:]
+        da1, dp = S.swiglu_bwd(da2, v[sl], inp["pp"][sl])
+        sig = torch.sigmoid(g)
+        rel = (4 * g.abs() + 30) * U
+        es = torch.cat([p * u.abs() * sig * (1 + g.abs()) * (ed + da2.abs() * rel),
+                        p * (g * sig).abs() * (ed + da2.abs() * rel)], 1)
+        eb = es + h * (da1.abs() + es)                       # dA1 as bf16
+        ref["dpp"].append((dp, ((g * sig * u).abs() * (ed + da2.abs() * (rel + (I + 20) * U))).sum(1)))
+        ref["dxp"].append((da1 @ w1, eb @ w1.abs() + 2 * I * U * ((da1.abs() + eb) @ w1.abs())))
+        # the weight gradients: dW2 from the saved bf16 A2, dW1 from the rounded dA1
+        for w, r, err in ((dw2[e], dy.T @ a2s[sl], n * U * (dy.abs().T @ a2s[sl].abs())),
+                          (dw1[e], da1.T @ x, (eb + n * U * (da1.abs() + eb)).T @ x.abs())):
+            assert ((w.double().cpu() - r).abs() <= err * 1.01 + h * (r.abs() + err) + 1e-37).all(), e
+    for k, t in got.items():
+        r, err = (torch.cat(z) for z in zip(*ref[k]))
+        half = h if t.dtype == BF else U
+        assert ((t.double().cpu() - r).abs() <= err * 1.01 + half * (r.abs() + err) + 1e-37).all(), k
+        assert rows == 0 or rel_frob(t, r) <= (0.004 if t.dtype == BF else 1e-4), (k, rel_frob(t, r))
 
 
 @pytest.mark.parametrize("precision", ALL, ids=IDS)
