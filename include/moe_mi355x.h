@@ -543,7 +543,9 @@ int grouped_mlp_bwd_gather(int precision, int E, int H, int I, int64_t rows, con
  *              33/32 bytes a value in place of saved->a1's 2.
  * saved        as in grouped_mlp_fwd; saved->a1 is neither read nor written
  *              and may be NULL.
- * yp and the other saved tensors are bit for bit those of grouped_mlp_fwd.
+ * yp and the other saved tensors are those of grouped_mlp_fwd: bit for bit,
+ * except in MOE_BF16 with few rows per expert (rows <= 64 E, or rows <= 256 E
+ * and rows * I <= 2^21), where the fp32 sums are taken in another order.
  */
 int grouped_mlp_fwd_ckpt(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp,
                          const int32_t* src_token, const int32_t* split_sizes,
@@ -559,8 +561,9 @@ int grouped_mlp_fwd_ckpt(int precision, int E, int H, int I, int64_t rows, const
  * [The same passage.]
  *
  * a1_codes, a1_scales   as grouped_mlp_fwd_ckpt wrote them.
- * Results are bit for bit those of grouped_mlp_bwd on a saved->a1 that holds
- * the decoded values (which bf16 represents).  A2 is not recomputed: dW_down
+ * Results are those of grouped_mlp_bwd on a saved->a1 that holds the decoded
+ * values (which bf16 represents): bit for bit, with the same exception as in
+ * the forward.  A2 is not recomputed: dW_down
  * does not depend on the 8-bit A1.
  */
 int grouped_mlp_bwd_ckpt(int precision, int E, int H, int I, int64_t rows, const uint16_t* dyp,

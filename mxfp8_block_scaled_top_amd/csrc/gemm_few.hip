@@ -4,13 +4,14 @@
 //   gate_up   A1 = x W1^T, then A2 = p silu(g) u and A1's MXFP8 rows
 //   down      y = A2 W2^T
 //   dgrads    dA2 = dy W2 with the SwiGLU backward,  dx = dA1 W1
+//   wgrads    dW2 = dy^T A2,  dW1 = dA1^T x
 //
-// With few rows the weights' bytes bound them: each weight should be read
-// once, by as many compute units as there are.  The 256 x 256 tiles of the
-// large products do neither: a tile spends its whole matrix time on a few
-// rows, and a narrow weight gives few tiles (N = 2816 and 5 experts: 55).
+// With few rows the weights' bytes bound them: each weight should be read (or
+// written) once, by as many compute units as there are.  The 256 x 256 tiles
+// of the large products do neither: a tile spends its whole matrix time on a
+// few rows, and a narrow weight gives few tiles (N = 2816 and 5 experts: 55).
 //   * A workgroup has 64 weight columns (32 gate and 32 up ones for gate_up)
-//     of one expert and up to 16 kMs of its rows; its 8 waves split K, so a
+//     of one expert and up to 16 kMs of its rows; its waves split K, so a
 //     narrow weight still has 64 x E workgroups at N = 4096.
 //   * Weights go from memory to registers to the matrix cores, with the next
 //     unit's loads in flight during this one's; nothing is shared by the waves
@@ -24,6 +25,13 @@
 //     rows and turns the 8 x 4 block in registers (16 byte permutes).
 //   * Tiles of the same weight columns go to the same XCD (round-robin
 //     dispatch), so an expert with several row tiles rereads weights from L2.
+//   * Weight gradients: a wave has a 64 x 64 piece of dW in registers, both
+//     operands turned as in the dgrads, and writes 128-byte lines straight
+//     from the accumulators: no LDS, several waves per SIMD whose reads, products and
+//     writes overlap, where a 256 x 256 tile has the CU to itself.
+// Measured, 8 experts of 2048 x 1408 with 4 rows each (138 MB of weights):
+// forward 33 us, backward 59 us (the weights' bytes alone, at a large copy's
+// rate: 27 and 53 us); 256 x 256 tiles 76 and 163 us.
 #include "common.hpp"
 #include "kernels.hpp"
 #include "mlp.hpp"
@@ -37,8 +45,6 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 constexpr int kFewN = 64;            // weight columns of a workgroup
-constexpr int kFewWaves = 8;
-constexpr int kFewThreads = 64 * kFewWaves;
 constexpr int kPitch = kFewN + 4;    // floats per row of a wave's partial sums in LDS
 
 struct FewTile {
@@ -77,11 +83,11 @@ __device__ __forceinline__ bool few_tile(const GemmArgs& g, int ntiles, int* lds
 
 // Adds the waves' partial sums: `part` holds [wave][row][kPitch]; the 4 columns
 // 4q.. of row m.
-template <int kMs>
+template <int kMs, int kWaves>
 __device__ __forceinline__ f32x4 few_sum(const float* part, int m, int q) {
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w)
+    for (int w = 0; w < kWaves; ++w)
         s += *(const f32x4*)(part + (w * 16 * kMs + m) * kPitch + 4 * q);
     return s;
 }
@@ -107,10 +113,10 @@ __device__ __forceinline__ void mx_store4(const f32x4& x, uint8_t* codes, uint8_
 
 // ---------------------------------------------------------------- K-contiguous weights
 // gate_up (kSwiglu) and down.
-template <int kMs, bool kSwiglu>
-__global__ __launch_bounds__(kFewThreads) void few_fwd_kernel(GemmArgs g, int ntiles) {
+template <int kMs, int kWaves, bool kSwiglu>
+__global__ __launch_bounds__(64 * kWaves) void few_fwd_kernel(GemmArgs g, int ntiles) {
     __shared__ int sched[192];
-    __shared__ __attribute__((aligned(16))) float part[kFewWaves * 16 * kMs * kPitch];
+    __shared__ __attribute__((aligned(16))) float part[kWaves * 16 * kMs * kPitch];
     FewTile t;
     if (!few_tile<kMs>(g, ntiles, sched, t)) return;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -148,7 +154,7 @@ __global__ __launch_bounds__(kFewThreads) void few_fwd_kernel(GemmArgs g, int nt
                 for (int h = 0; h < 2; ++h) x[i][h] = *(const u32x4*)(xp[i] + (int64_t)u * 64 + 8 * h);
     };
     if (wave < units) load(wave);
-    for (int u = wave; u < units; u += kFewWaves) {
+    for (int u = wave; u < units; u += kWaves) {
         u32x4 cw[4][2], cx[kMs][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -157,7 +163,7 @@ __global__ __launch_bounds__(kFewThreads) void few_fwd_kernel(GemmArgs g, int nt
 #pragma unroll
             for (int i = 0; i < kMs; ++i) cx[i][h] = x[i][h];
         }
-        if (u + kFewWaves < units) load(u + kFewWaves);
+        if (u + kWaves < units) load(u + kWaves);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -178,32 +184,34 @@ __global__ __launch_bounds__(kFewThreads) void few_fwd_kernel(GemmArgs g, int nt
                 *(f32x4*)(part + (wave * 16 * kMs + i * 16 + r) * kPitch + 16 * s + 4 * kg) = acc[s][i];
     __syncthreads();
     if constexpr (kSwiglu) {
-        const int m = threadIdx.x >> 3, q = threadIdx.x & 7;     // 8 threads per row, 4 j each
-        if (m >= t.valid) return;
-        const int64_t I = g.I, gr = t.row0 + m, j = t.nt * 32 + 4 * q;
-        const f32x4 gt = few_sum<kMs>(part, m, q), up = few_sum<kMs>(part, m, 8 + q);
-        const float p = g.prob[gr];
-        f32x4 a2;
+        const int q = threadIdx.x & 7;           // 8 threads per row, 4 j each
+        for (int m = threadIdx.x >> 3; m < t.valid; m += 8 * kWaves) {
+            const int64_t I = g.I, gr = t.row0 + m, j = t.nt * 32 + 4 * q;
+            const f32x4 gt = few_sum<kMs, kWaves>(part, m, q);
+            const f32x4 up = few_sum<kMs, kWaves>(part, m, 8 + q);
+            const float p = g.prob[gr];
+            f32x4 a2;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) a2[k] = p * (gt[k] * sigmoid_few(gt[k])) * up[k];
-        *(u32x2*)(g.act + gr * I + j) = pack4(a2);
-        const int64_t at = gr * 2 * I + j;
-        mx_store4(gt, g.a1_codes + at, g.a1_scales + at / 32, q == 0);
-        mx_store4(up, g.a1_codes + at + I, g.a1_scales + (at + I) / 32, q == 0);
+            for (int k = 0; k < 4; ++k) a2[k] = p * (gt[k] * sigmoid_few(gt[k])) * up[k];
+            *(u32x2*)(g.act + gr * I + j) = pack4(a2);
+            const int64_t at = gr * 2 * I + j;
+            mx_store4(gt, g.a1_codes + at, g.a1_scales + at / 32, q == 0);
+            mx_store4(up, g.a1_codes + at + I, g.a1_scales + (at + I) / 32, q == 0);
+        }
     } else {
         const int q = threadIdx.x & 15;
-        for (int m = threadIdx.x >> 4; m < t.valid; m += kFewThreads / 16)
+        for (int m = threadIdx.x >> 4; m < t.valid; m += 4 * kWaves)
             *(u32x2*)((bf16_t*)g.c + (t.row0 + m) * g.ldc + t.nt * 64 + 4 * q) =
-                pack4(few_sum<kMs>(part, m, q));
+                pack4(few_sum<kMs, kWaves>(part, m, q));
     }
 }
 
 // ---------------------------------------------------------------- N-contiguous weights
 // The down dgrad with the SwiGLU backward (kSwiglu) and the gate_up dgrad.
-template <int kMs, bool kSwiglu>
-__global__ __launch_bounds__(kFewThreads) void few_dgrad_kernel(GemmArgs g, int ntiles) {
+template <int kMs, int kWaves, bool kSwiglu>
+__global__ __launch_bounds__(64 * kWaves) void few_dgrad_kernel(GemmArgs g, int ntiles) {
     __shared__ int sched[192];
-    __shared__ __attribute__((aligned(16))) float part[kFewWaves * 16 * kMs * kPitch];
+    __shared__ __attribute__((aligned(16))) float part[kWaves * 16 * kMs * kPitch];
     FewTile t;
     if (!few_tile<kMs>(g, ntiles, sched, t)) return;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -233,7 +241,7 @@ __global__ __launch_bounds__(kFewThreads) void few_dgrad_kernel(GemmArgs g, int 
             if (i < ms) x[i] = *(const u32x4*)(xp[i] + (int64_t)u * 32);
     };
     if (wave < units) load(wave);
-    for (int u = wave; u < units; u += kFewWaves) {
+    for (int u = wave; u < units; u += kWaves) {
         u32x4 f[4], cx[kMs];        // f[s]: column 4 r + s, its 8 K values
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -243,7 +251,7 @@ __global__ __launch_bounds__(kFewThreads) void few_dgrad_kernel(GemmArgs g, int 
                                                 s & 1 ? 0x07060302u : 0x05040100u);
 #pragma unroll
         for (int i = 0; i < kMs; ++i) cx[i] = x[i];
-        if (u + kFewWaves < units) load(u + kFewWaves);
+        if (u + kWaves < units) load(u + kWaves);
 #pragma unroll
         for (int i = 0; i < kMs; ++i)
             if (i < ms)
@@ -263,8 +271,8 @@ __global__ __launch_bounds__(kFewThreads) void few_dgrad_kernel(GemmArgs g, int 
                     (f32x4){acc[0][i][q], acc[1][i][q], acc[2][i][q], acc[3][i][q]};
     __syncthreads();
     const int q = threadIdx.x & 15;
-    for (int m = threadIdx.x >> 4; m < t.valid; m += kFewThreads / 16) {
-        const f32x4 d = few_sum<kMs>(part, m, q);
+    for (int m = threadIdx.x >> 4; m < t.valid; m += 4 * kWaves) {
+        const f32x4 d = few_sum<kMs, kWaves>(part, m, q);
         const int64_t gr = t.row0 + m;
         const int64_t n = t.nt * 64 + 4 * q;
         if constexpr (kSwiglu) {
@@ -295,6 +303,65 @@ __global__ __launch_bounds__(kFewThreads) void few_dgrad_kernel(GemmArgs g, int 
     }
 }
 
+// ---------------------------------------------------------------- weight gradients
+// dW_e [M, N] = A_e^T B_e over the expert's rows.
+__global__ __launch_bounds__(256) void few_wgrad_kernel(GemmArgs g, int mt, int nt) {
+    const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int per = mt * nt;                    // 128 x 128 tiles of an expert
+    const int e = blockIdx.x / per, tile = blockIdx.x - e * per;
+    const int m0 = tile / nt * 128 + (wave >> 1) * 64, n0 = tile % nt * 128 + (wave & 1) * 64;
+    // the expert's rows (every wave for itself)
+    const int n = clamp_group_size(lane < g.E ? g.split[lane] : 0, g.rows);
+    const int incl = wave_incl_scan(n);
+    const int rows = __builtin_amdgcn_readlane(n, e);
+    const int64_t row0 = __builtin_amdgcn_readlane(incl, e) - rows;
+    const bf16_t* A = (const bf16_t*)g.a + row0 * g.lda + m0 + 4 * c;
+    const bf16_t* B = (const bf16_t*)g.b.p[0] + row0 * g.ldb + n0 + 4 * c;
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < rows; r0 += 32) {     // lane: 4 columns of rows r0 + 8 kg ..
+        u32x2 a[8], b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = r0 + 8 * kg + k;
+            a[k] = b[k] = (u32x2){0u, 0u};
+            if (r < rows) {
+                a[k] = *(const u32x2*)(A + (int64_t)r * g.lda);
+                b[k] = *(const u32x2*)(B + (int64_t)r * g.ldb);
+            }
+        }
+        u32x4 fa[4], fb[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t sel = s & 1 ? 0x07060302u : 0x05040100u;
+                fa[s][k] = __builtin_amdgcn_perm(a[2 * k + 1][s >> 1], a[2 * k][s >> 1], sel);
+                fb[s][k] = __builtin_amdgcn_perm(b[2 * k + 1][s >> 1], b[2 * k][s >> 1], sel);
+            }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8_t, fa[s]), __builtin_bit_cast(bf16x8_t, fb[t]),
+                    acc[s][t], 0, 0, 0);
+    }
+    // acc[s][t][q]: row 4 (4 kg + q) + s, column 4 c + t
+    bf16_t* C = (bf16_t*)g.c_tab.p[e] + (int64_t)(m0 + 16 * kg) * g.ldc + n0 + 4 * c;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            __builtin_nontemporal_store(
+                pack4((f32x4){acc[s][0][q], acc[s][1][q], acc[s][2][q], acc[s][3][q]}),
+                (u32x2*)(C + (int64_t)(4 * q + s) * g.ldc));
+}
+
 // dprob: the row's partial sums, one wave per row.
 __global__ __launch_bounds__(256) void few_dprob_kernel(const float* __restrict__ part, int64_t rows,
                                                         int ntiles, float* __restrict__ dprob) {
@@ -309,24 +376,43 @@ __global__ __launch_bounds__(256) void few_dprob_kernel(const float* __restrict_
 
 }  // namespace
 
-bool use_few_rows(int64_t rows, int E) { return rows <= 64 * (int64_t)E; }
+// The rule, from times of both forms (forward / backward, us, few against
+// 256 x 256 tiles).  Up to 64 rows per expert the weights' bytes lead:
+//   H, I, E           rows per expert
+//   4096, 14336, 8    64: 683 / 1521 against 892 / 1759;  128: 1257 / 2230 against 940 / 1924
+//   2048, 1408, 64    32: 275 / 550 against 380 / 741;  64: 347 / 706 against 390 / 789
+// Further up to 256 while the experts have so few 256-wide tiles that these
+// leave most compute units idle (rows I <= 2^21):
+//   2048, 1408, 8     128: 82 / 123 against 85 / 196;  256: 144 / 204 against 90 / 219
+//   1024, 4096, 2     256: 70 / 107 against 108 / 249
+//   512, 1024, 8      256: 37 / 60 against 50 / 121
+bool use_few_rows(int64_t rows, int E, int I) {
+    return rows <= 64 * (int64_t)E || (rows <= 256 * (int64_t)E && rows * I <= (1 << 21));
+}
 
 int few_tiles(int N) { return N / kFewN; }
 
 hipError_t launch_few(int use, const GemmArgs& g, hipStream_t s) {
+    TraceScope ts(g.name ? g.name : "gemm_few", s);
+    if (use == U_DOWN_WGRAD || use == U_GATEUP_WGRAD) {
+        const int mt = g.M / 128, nt = g.N / 128;
+        few_wgrad_kernel<<<(unsigned)(g.E * mt * nt), 256, 0, s>>>(g, mt, nt);
+        return hipGetLastError();
+    }
     const bool fwd = use == U_GATEUP_FWD || use == U_DOWN_FWD;
     const bool swiglu = use == U_GATEUP_FWD || use == U_DOWN_DGRAD;
     const int ntiles = use == U_GATEUP_FWD ? g.I / 32 : few_tiles(g.N);
-    // few rows on average: 16-row tiles (an expert with more has several)
+    // up to 16 rows on average: 16-row tiles of 8 waves (an expert with more
+    // rows has several); above, 64-row tiles, of 4 waves so that two fit a CU
+    // (2048 x 1408, 64 experts of 32 rows: forward 277 us, with 8 waves 372)
     const bool wide = g.rows > 16 * (int64_t)g.E;
     const int64_t kM = wide ? 64 : 16;
     const int64_t slots = (g.rows + g.E * (kM - 1)) / kM;
     const unsigned grid = (unsigned)(slots * ((ntiles + 7) / 8 * 8));
-    TraceScope ts(g.name ? g.name : "gemm_few", s);
-#define FEW_CASE(KERNEL, SW)                                                  \
-    do {                                                                      \
-        if (wide) KERNEL<4, SW><<<grid, kFewThreads, 0, s>>>(g, ntiles);      \
-        else KERNEL<1, SW><<<grid, kFewThreads, 0, s>>>(g, ntiles);           \
+#define FEW_CASE(KERNEL, SW)                                         \
+    do {                                                             \
+        if (wide) KERNEL<4, 4, SW><<<grid, 256, 0, s>>>(g, ntiles);  \
+        else KERNEL<1, 8, SW><<<grid, 512, 0, s>>>(g, ntiles);       \
     } while (0)
     if (fwd && swiglu) FEW_CASE(few_fwd_kernel, true);
     else if (fwd) FEW_CASE(few_fwd_kernel, false);

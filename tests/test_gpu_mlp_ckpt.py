@@ -4,8 +4,8 @@ the pre-norm sublayer built on it.
 The forward's other outputs are those of grouped_mlp_fwd bit for bit, and the
 backward's are those of grouped_mlp_bwd on the decoded A1 bit for bit, so what
 the tests of those calls show carries over; the codes themselves are held
-against A1 in float64.  In BF16 with at most 64 rows per expert on average
-other kernels run (the fp32 sums in another order): those are held against
+against A1 in float64.  In BF16 with few rows per expert other
+kernels run (the fp32 sums in another order): those are held against
 float64 throughout."""
 import numpy as np
 import pytest
@@ -45,14 +45,16 @@ def _cuda(inp):
 
 
 SIZES = [([300, 0, 1, 399], 384, 640), ([1], 128, 128), ([0, 0, 5], 256, 384), ([257, 31, 513], 128, 1408),
-         ([64] * 16, 256, 256), ([65, 65], 128, 128)]
+         ([64] * 16, 256, 256), ([65, 65], 128, 128), ([300, 0, 2000], 128, 1408), ([700, 1, 700, 200], 256, 1536)]
 
 
-def _few(precision, sizes):
-    return precision == moe.MOE_BF16 and sum(sizes) <= 64 * len(sizes)
+def _few(precision, sizes, I):
+    """Sizes that the few-row kernels take."""
+    rows, E = sum(sizes), len(sizes)
+    return precision == moe.MOE_BF16 and (rows <= 64 * E or (rows <= 256 * E and rows * I <= 1 << 21))
 
 
-@pytest.mark.parametrize("precision,sizes,H,I", [(p, *s) for p in ALL for s in SIZES if not _few(p, s[0])])
+@pytest.mark.parametrize("precision,sizes,H,I", [(p, *s) for p in ALL for s in SIZES if not _few(p, s[0], s[2])])
 def test_against_the_bf16_form(precision, sizes, H, I):
     say(f"mlp ckpt {NAME[precision]} sizes={sizes} H={H} I={I}")
     d = _cuda(_inputs(sizes, H, I, seed=len(sizes) + I))
@@ -114,7 +116,8 @@ def test_codes_against_float64(precision):
 
 FEW = [([1], 128, 128), ([0, 0, 5], 256, 384), ([64] * 16, 256, 256), ([3, 0, 1, 2], 384, 640),
        ([0, 200, 0, 1, 0, 0, 0, 50], 256, 128), ([16, 17, 15, 64], 128, 1408), ([65, 63], 640, 256),
-       ([2, 2], 128, 4096), ([1, 1, 0, 1], 2048, 128), ([1] * 64, 128, 256), ([0, 0], 128, 128)]
+       ([2, 2], 128, 4096), ([1, 1, 0, 1], 2048, 128), ([1] * 64, 128, 256), ([0, 0], 128, 128),
+       ([300, 0, 1, 399], 384, 640), ([257, 31, 480], 128, 1408), ([256], 256, 512), ([129, 127], 384, 8192)]
 
 
 @pytest.mark.parametrize("sizes,H,I", FEW)
