@@ -364,6 +364,54 @@ __device__ __forceinline__ bf16x8_t mn_frag(const uint8_t* lds, int s, int colba
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// A lane's side of the bf16 loops' DMA: offsets that do not change with the K
+// step, so that a DMA costs one or two vector instructions.
+template <int L>
+struct Lane;
+template <>
+struct Lane<L_KMAJ> {
+    uint32_t o[4];
+    int kbytes;
+    __device__ __forceinline__ void init(const KOp& op, int lane, int wave) {
+        const int lc16 = ((lane & 3) ^ ((lane >> 4) & 3)) << 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int gr = kop_row(op, (wave * 4 + j) * 16 + (lane >> 2));
+            o[j] = (uint32_t)((int64_t)gr * op.stride) + (uint32_t)lc16;
+        }
+        kbytes = op.kbytes;          // a multiple of the step's 64 bytes
+    }
+    __device__ __forceinline__ uint32_t off(int kt, int j) const {
+        return o[j] + (kt * kRowB < kbytes ? (uint32_t)(kt * kRowB) : kOob);
+    }
+};
+template <>
+struct Lane<L_MNMAJ> {
+    uint32_t o[4];
+    const uint8_t* base;
+    int64_t stride;
+    int k_valid, hi, w2;
+    __device__ __forceinline__ void init(const MNOp& op, int lane, int wave) {
+        base = op.base;
+        stride = op.stride;
+        k_valid = op.k_valid;
+        hi = lane >> 5;
+        w2 = wave * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = w2 + j * 2 + hi;
+            const int c = (lane & 31) ^ ((k & 3) << 2);
+            o[j] = c * 8 < op.mn_valid ? (uint32_t)(k * op.stride) + (uint32_t)(c * 16) : kOob;
+        }
+    }
+    __device__ __forceinline__ i32x4 rsrc(int kt) const {
+        return make_rsrc(base + (int64_t)kt * 32 * stride);
+    }
+    __device__ __forceinline__ uint32_t off(int kt, int j) const {
+        return hi < k_valid - kt * 32 - w2 - j * 2 ? o[j] : kOob;
+    }
+};
+
 // MXFP8 scales of one K step.  GEMM operands keep their E8M0 scales
 // block-major ([block][row]), so the scales of one K block for the 256 tile
 // rows are 256 bytes: one dword per lane covers 4 consecutive tile rows.
@@ -1231,6 +1279,94 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
+    if constexpr (DT == DT_BF16) {
+        // bf16: the barrier stands at the start of a step and publishes the
+        // next step's stage, so that everything the step issues, 8 DMAs, the
+        // next step's fragment reads and 32 MFMAs, is spread evenly over it:
+        // one wave per SIMD has nothing but its own instructions to keep the
+        // matrix pipe busy with while the LDS serves 64 KiB of reads.  Step kt
+        // loads batch kt+4 into its own stage: every wave had finished that
+        // stage's reads before the barrier.
+        Lane<LA> da;
+        Lane<LB> db;
+        if constexpr (LA == L_KMAJ) da.init(ka, lane, wave); else da.init(ma, lane, wave);
+        if constexpr (LB == L_KMAJ) db.init(kb, lane, wave); else db.init(mb, lane, wave);
+        auto dma = [&](auto S, int kt, int j) {       // instruction j of 8 of batch kt
+            uint8_t* base = stage_ptr(S);
+            const uint32_t l0 = lds_u32(base + wave * 4096) + (j & 3) * 1024;
+            if (j < 4) {
+                if constexpr (LA == L_KMAJ) dma16(rs_a, da.off(kt, j), l0);
+                else dma16(da.rsrc(kt), da.off(kt, j), l0);
+            } else {
+                if constexpr (LB == L_KMAJ) dma16(rs_b, db.off(kt, j - 4), l0 + kTileB);
+                else dma16(db.rsrc(kt), db.off(kt, j - 4), l0 + kTileB);
+            }
+        };
+        auto read_a = [&](const uint8_t* A, Frags& F, int s, int f) {
+            if constexpr (LA == L_KMAJ)
+                F.a[s][f] = *(const bf16x8_t*)(A + (s ? oA2 : oA0) + f * kFragB);
+            else
+                F.a[s][f] = mn_frag(A, s, wm * 128 + f * 32);
+        };
+        auto read_b = [&](const uint8_t* B, Frags& F, int s, int f) {
+            if constexpr (LB == L_KMAJ)
+                F.b[s][f] = *(const bf16x8_t*)(B + (s ? oB2 : oB0) + f * kFragB);
+            else
+                F.b[s][f] = mn_frag(B, s, wn * 128 + f * 32);
+        };
+        // fragment read n of 16, in the order in which the step uses them
+        auto read = [&](auto S, Frags& F, int n) {
+            const uint8_t* A = stage_ptr(S);
+            const uint8_t* B = A + kTileB;
+            if (n < 4) read_b(B, F, 0, n);
+            else if (n == 4) read_a(A, F, 0, 0);
+            else if (n < 9) read_b(B, F, 1, n - 5);
+            else read_a(A, F, n == 9 || ((n & 1) && n > 10), (n - 8) / 2);
+        };
+        auto bstep = [&](auto S, int kt, Frags& Fc, Frags& Fn) {
+            constexpr int st = decltype(S)::value;
+            using Next = std::integral_constant<int, (st + 1) % kStages>;
+            __builtin_amdgcn_sched_barrier(0);
+            pipe_barrier<kWait2>();                   // batch kt+1 has landed
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {             // block i: 4 MFMAs
+                const int fi = i >> 1, s = i & 1;
+                const int r0 = i < 2 ? 3 * i : 2 * i + 2, r1 = i < 2 ? r0 + 3 : r0 + 2;
+#pragma unroll
+                for (int fj = 0; fj < 4; ++fj) {
+                    acc[fi][fj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        Fc.a[s][fi], Fc.b[s][fj], acc[fi][fj], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (fj == 0) dma(S, kt + 4, i);
+                    if (fj > 0 && r0 + fj - 1 < r1 && r0 + fj - 1 < 16) read(Next{}, Fn, r0 + fj - 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dma(I0{}, 0, j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dma(I1{}, 1, j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dma(I2{}, 2, j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dma(I3{}, 3, j);
+        pipe_barrier<3 * kBatch>();                   // batch 0 has landed
+#pragma unroll
+        for (int n = 0; n < 16; ++n) read(I0{}, F0, n);
+        int kt = 0;
+        for (; kt + kStages <= nk; kt += kStages) {
+            bstep(I0{}, kt, F0, F1);
+            bstep(I1{}, kt + 1, F1, F0);
+            bstep(I2{}, kt + 2, F0, F1);
+            bstep(I3{}, kt + 3, F1, F0);
+        }
+        if (kt < nk) bstep(I0{}, kt, F0, F1);
+        if (kt + 1 < nk) bstep(I1{}, kt + 1, F1, F0);
+        if (kt + 2 < nk) bstep(I2{}, kt + 2, F0, F1);
+        __builtin_amdgcn_sched_barrier(0);
+    } else {
     if (nk > 0) {
         issue(I0{}, 0);
         issue(I1{}, 1);
@@ -1252,6 +1388,7 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     if (kt < nk) step(I0{}, kt, F0, F1);
     if (kt + 1 < nk) step(I1{}, kt + 1, F1, F0);
     if (kt + 2 < nk) step(I2{}, kt + 2, F0, F1);
+    }
     // the look-ahead batches past the end still write LDS: drain them before
     // the epilogue reuses it
     pipe_barrier<0>();
