@@ -540,7 +540,8 @@ int grouped_mlp_bwd_gather(int precision, int E, int H, int I, int64_t rows, con
  * a1_codes     uint8 [rows, 2I] out and
  * a1_scales    uint8 [rows, 2I/32] out (both 16-byte aligned): MXFP8 of the
  *              fp32 A1 in the layout and by the rule of mxfp8_quantize axis=1,
- *              33/32 bytes a value in place of saved->a1's 2.
+ *              33/32 bytes a value in place of saved->a1's 2.  (NaN and
+ *              infinities in A1 are outside the contract, as there.)
  * saved        as in grouped_mlp_fwd; saved->a1 is neither read nor written
  *              and may be NULL.
  * yp and the other saved tensors are those of grouped_mlp_fwd: bit for bit,

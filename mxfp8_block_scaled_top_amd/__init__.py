@@ -416,6 +416,14 @@ def _saved_struct(s: dict) -> _Saved:
     return _Saved(*[_ptr(s.get(n)) for n, _ in _Saved._fields_])
 
 
+def _mlp_args(E: int, rows: int, device, split_sizes, w_down, prob_perm, *outputs) -> None:
+    """One matrix per expert in every table; sizes and probabilities of the rows."""
+    if any(t is not None and len(t) != E for t in (w_down, *outputs)):
+        raise MoEError(f"every weight table must have one matrix per expert ({E})")
+    _arg(split_sizes, "split_sizes", torch.int32, (E,), device)
+    _arg(prob_perm, "prob_perm", torch.float32, (rows,), device)
+
+
 def grouped_mlp_fwd_ckpt(xp, split_sizes, w_gate_up, w_down, prob_perm, precision=MOE_MXFP8,
                          saved=None, workspace=None, src_token=None):
     """grouped_mlp_fwd (with src_token: grouped_mlp_fwd_gather) that keeps A1
@@ -431,6 +439,7 @@ def grouped_mlp_fwd_ckpt(xp, split_sizes, w_gate_up, w_down, prob_perm, precisio
     dev = xp.device
     if saved is None:
         saved = alloc_saved(rows, H, I, E, precision, dev, checkpoint=True)
+    _mlp_args(E, rows, dev, split_sizes, w_down, prob_perm)
     codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
     if codes is None:
         raise MoEError("saved has no a1_codes: use alloc_saved(..., checkpoint=True)")
@@ -459,6 +468,7 @@ def grouped_mlp_bwd_ckpt(dyp, xp, split_sizes, w_gate_up, w_down, prob_perm, sav
     E = len(w_gate_up)
     I = w_down[0].shape[1]
     dev = dyp.device
+    _mlp_args(E, rows, dev, split_sizes, w_down, prob_perm, dw_gate_up, dw_down)
     codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
     if codes is None:
         raise MoEError("saved has no a1_codes (grouped_mlp_fwd_ckpt)")
@@ -623,6 +633,7 @@ def grouped_linear_bwd(dy, x, split_sizes, w, precision=MOE_BF16, want_dx=True, 
 
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}      # moe_type
+_EITHER = (torch.bfloat16, torch.float32)
 
 
 def _arg(t, name: str, dtype, shape, device) -> None:
@@ -643,12 +654,14 @@ def _arg(t, name: str, dtype, shape, device) -> None:
 
 
 def _first(t, name: str, dtype) -> tuple:
-    """The first tensor argument, a matrix: (rows, columns, device)."""
+    """The first tensor argument, a dense matrix: (rows, columns, device)."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.is_contiguous()
+            and (t.dtype in dtype if dtype.__class__ is tuple else t.dtype is dtype)):
+        return *t.shape, t.device
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise MoEError(f"{name} must be a matrix")
-    device = t.device
-    _arg(t, name, dtype, t.shape, device)
-    return *t.shape, device
+    _arg(t, name, dtype, t.shape, t.device)
+    return *t.shape, t.device
 
 
 def _checkpoint(rows: int, cols: int, device):
@@ -672,14 +685,14 @@ def moe_layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, checkpoint: b
     or fp32 [H], or None.  Returns (y bf16 [T, H], saved): saved holds mean and
     rstd (fp32 [T]) and, with checkpoint, the normalized rows in 8 bits
     (xhat_codes, xhat_scales); without it the backward needs x."""
-    T, H, dev = _first(x, "x", tuple(_TYPES))
+    T, H, dev = _first(x, "x", _EITHER)
     for t, n in ((gamma, "gamma"), (beta, "beta")):
         if t is not None:
-            _arg(t, n, tuple(_TYPES), (H,), dev)
+            _arg(t, n, _EITHER, (H,), dev)
     if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
         raise MoEError("gamma and beta must have one type")
     w = gamma if gamma is not None else beta
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    y = torch.empty_like(x, dtype=torch.bfloat16)
     mean = torch.empty(T, dtype=torch.float32, device=dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
     saved = {"mean": mean, "rstd": rstd}
@@ -703,25 +716,26 @@ def moe_layernorm_bwd(dy, saved: dict, gamma=None, x=None, dres=None, dx_dtype=N
     T, H, dev = _first(dy, "dy", torch.bfloat16)
     codes, scales = _saved_pair(saved, "xhat", T, H, dev)
     _arg(saved.get("rstd"), "rstd", torch.float32, (T,), dev)
-    mean = None
-    if codes is None:
-        if x is None:
-            raise MoEError("without a checkpoint x is needed")
-        _arg(x, "x", tuple(_TYPES), (T, H), dev)
-        mean = saved.get("mean")
-        _arg(mean, "mean", torch.float32, (T,), dev)
-    else:
-        x = None        # the checkpoint takes its place
+    if x is not None:
+        _arg(x, "x", _EITHER, (T, H), dev)
     if dx_dtype is None:
         dx_dtype = next((t.dtype for t in (x, dres) if t is not None), torch.bfloat16)
     if dx_dtype not in _TYPES or (x is not None and x.dtype != dx_dtype):
         raise MoEError(f"dx_dtype must be x's, torch.bfloat16 or torch.float32, got {dx_dtype}")
+    mean = None
+    if codes is not None:
+        x = None        # the checkpoint takes its place
+    else:
+        if x is None:
+            raise MoEError("without a checkpoint x is needed")
+        mean = saved.get("mean")
+        _arg(mean, "mean", torch.float32, (T,), dev)
     if dres is not None:
         _arg(dres, "dres", dx_dtype, (T, H), dev)
     if gamma is not None:
-        _arg(gamma, "gamma", tuple(_TYPES), (H,), dev)
+        _arg(gamma, "gamma", _EITHER, (H,), dev)
     wt = gamma.dtype if gamma is not None else torch.float32
-    dx = torch.empty((T, H), dtype=dx_dtype, device=dev)
+    dx = torch.empty_like(dy, dtype=dx_dtype)
     dgamma = torch.empty(H, dtype=wt, device=dev) if want_dgamma else None
     dbeta = torch.empty(H, dtype=wt, device=dev) if want_dbeta else None
     if workspace is None and (want_dgamma or want_dbeta):

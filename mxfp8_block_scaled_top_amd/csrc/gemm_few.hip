@@ -386,7 +386,10 @@ __global__ __launch_bounds__(256) void few_dprob_kernel(const float* __restrict_
 //   2048, 1408, 8     128: 82 / 123 against 85 / 196;  256: 144 / 204 against 90 / 219
 //   1024, 4096, 2     256: 70 / 107 against 108 / 249
 //   512, 1024, 8      256: 37 / 60 against 50 / 121
-bool use_few_rows(int64_t rows, int E, int I) {
+// Wider weights than 65536 stay with the tiles (the grids here are bounded for
+// those that are not).
+bool use_few_rows(int64_t rows, int E, int H, int I) {
+    if (H > (1 << 16) || I > (1 << 16)) return false;
     return rows <= 64 * (int64_t)E || (rows <= 256 * (int64_t)E && rows * I <= (1 << 21));
 }
 

@@ -105,7 +105,7 @@ BwdWs carve_bwd(void* base, int64_t rows, int H, int I, int E, int precision) {
     Carve c(base);
     BwdWs w{};
     int ntn = gemm_n_tiles(EPI_SWIGLU_BWD, I, I);
-    if (precision == MOE_BF16 && use_few_rows(rows, E, I)) ntn = few_tiles(I);   // narrower tiles
+    if (precision == MOE_BF16 && use_few_rows(rows, E, H, I)) ntn = few_tiles(I);   // narrower tiles
     w.part = (float*)c.take((size_t)rows * ntn * sizeof(float));
     if (precision == MOE_BF16) {
         w.da1 = c.take((size_t)rows * 2 * I * 2);
@@ -360,7 +360,7 @@ int mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp
         set_a1(g, saved, ck);
         g.act = saved->a2;
         g.name = "gemm_bf16_gateup_fwd_swiglu";
-        const bool few = ck.used && use_few_rows(rows, E, I);
+        const bool few = ck.used && use_few_rows(rows, E, H, I);
         MOE_TRY(few ? launch_few(U_GATEUP_FWD, g, stream)
                     : launch_gemm(DT_BF16, U_GATEUP_FWD, g, stream));
         GemmArgs d = g;
@@ -536,7 +536,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
     // weight-gradient GEMMs run for every expert (empty experts get zeros),
     // even when there are no rows at all
     if (precision == MOE_BF16) {
-        const bool few = ck.used && use_few_rows(rows, E, I);
+        const bool few = ck.used && use_few_rows(rows, E, H, I);
         GemmArgs g{};
         g.split = split_sizes;
         g.E = E;

@@ -89,7 +89,7 @@ hipError_t launch_dprob_reduce(const float* part, int64_t rows, int ntiles, floa
 // bf16 products for few rows per expert (gemm_few.hip): the six uses, with A1
 // as MXFP8 rows; whether the sizes take them, their dprob partial sums per row
 // (dgrad of N = I columns) and the sum of those.
-bool use_few_rows(int64_t rows, int E, int I);
+bool use_few_rows(int64_t rows, int E, int H, int I);
 int few_tiles(int N);
 hipError_t launch_few(int use, const GemmArgs& g, hipStream_t s);
 hipError_t launch_few_dprob(const float* part, int64_t rows, int ntiles, float* dprob,

@@ -356,6 +356,18 @@ def test_in_a_graph_and_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_checkpoint_takes_the_place_of_x():
+    """With a checkpoint x only gives dx its type."""
+    say("layernorm bwd with both")
+    x = _randn(20, 96, seed=1).cuda()
+    dy = _randn(20, 96, seed=2, dtype=BF).cuda()
+    _, saved = moe.moe_layernorm_fwd(x, checkpoint=True)
+    a = moe.moe_layernorm_bwd(dy, saved, x=x)
+    b = moe.moe_layernorm_bwd(dy, saved, dx_dtype=F32)
+    torch.cuda.synchronize()
+    assert a[0].dtype == F32 and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_binding_refusals():
     say("layernorm binding refusals")
     x = torch.zeros((4, 64), dtype=BF, device="cuda")

@@ -411,6 +411,10 @@ def test_binding_refusals():
                  lambda: moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s | {"a1_codes": s["a1_codes"][:4]},
                                                   moe.MOE_BF16),
                  lambda: moe.grouped_mlp_fwd_ckpt(d["xp"], *args, moe.MOE_BF16, src_token=src),
-                 lambda: moe.grouped_mlp_bwd_ckpt(d["dyp"], None, *args, s, moe.MOE_BF16)):
+                 lambda: moe.grouped_mlp_bwd_ckpt(d["dyp"], None, *args, s, moe.MOE_BF16),
+                 lambda: moe.grouped_mlp_fwd_ckpt(d["xp"], d["split"].long(), *args[1:], moe.MOE_BF16),
+                 lambda: moe.grouped_mlp_fwd_ckpt(d["xp"], args[0], d["w1"], d["w2"][:1], d["pp"], moe.MOE_BF16),
+                 lambda: moe.grouped_mlp_fwd_ckpt(d["xp"], *args[:3], d["pp"][:4], moe.MOE_BF16),
+                 lambda: moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s, moe.MOE_BF16, None, d["w1"][:1])):
         with pytest.raises(moe.MoEError):
             call()
