@@ -17,15 +17,15 @@
 //     v_mfma_scale_f32_32x32x64_f8f6f4, the E8M0 scale of every 32 K-values
 //     and row fed straight to the instruction, so nothing is dequantized).
 //   * LDS holds four stages of both operand tiles (4 x 32 KiB); the loads of
-//     steps k+1..k+3 are in flight while step k feeds the MFMAs, one barrier
+//     steps k+2..k+4 are in flight while step k feeds the MFMAs, one barrier
 //     per step.  Operands go from memory to LDS without passing through
 //     registers (buffer_load_dwordx4 ... lds: lane l's 16 bytes land at the
 //     wave's LDS base + 16 l, so the lane picks the global chunk that fills
 //     its slot); 16-byte chunks of a 64-byte tile row are XOR-swizzled by
 //     (row >> 2) & 3 so fragment reads of 16 consecutive rows hit distinct
 //     banks.  Offsets past a row's valid K read zeros.  The fragments of
-//     step k+1 are read from LDS into a second register set right after the
-//     barrier that publishes them, under the last MFMAs of step k.
+//     step k+1 are read from LDS into a second register set during step k,
+//     spread between its MFMAs like the DMAs of step k+4.
 //   * Epilogues: each wave stages its 128 x 128 result through its own LDS
 //     region, 32 rows at a time (last slice first), and syncs only on its
 //     own LDS accesses.  Outputs that a wave owns whole lines of (the plain
@@ -293,32 +293,6 @@ __device__ __forceinline__ void pipe_barrier() {
     __builtin_amdgcn_s_waitcnt(0xC07F);   // vmcnt(63) expcnt(7) lgkmcnt(0)
 }
 
-// LDS-DMA of one K step of a K-contiguous tile: the wave's 4 instructions
-// cover tile rows (wave*4 + j)*16 .. +15; slot i of instruction j is tile row
-// (wave*4 + j)*16 + i/4 and physical chunk i%4, whose logical chunk is
-// (i%4) ^ ((row>>2)&3) = (i%4) ^ ((i>>4)&3).
-template <bool P2>
-__device__ __forceinline__ void dma_kop(const KOp& op, const i32x4& rs, int k0b, uint8_t* lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int lc16 = ((lane & 3) ^ ((lane >> 4) & 3)) << 4;    // logical 16-byte chunk
-    const int kc16 = lc16 + k0b;
-    const uint32_t l0 = lds_u32(lds + wave * 4 * 1024);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        int r = (wave * 4 + j) * 16 + (lane >> 2);
-        const int gr = kop_row(op, r);
-        uint32_t o = kOob;
-        if (kc16 < op.kbytes) {
-            if (P2)   // K step k0b / 64 of row pair gr / 2: line k0b / 64, half gr & 1
-                o = (uint32_t)(gr >> 1) * (uint32_t)op.stride + (uint32_t)(2 * k0b) +
-                    (uint32_t)((gr & 1) * 64 + lc16);
-            else
-                o = (uint32_t)((int64_t)gr * op.stride) + (uint32_t)kc16;
-        }
-        dma16(rs, o, l0 + j * 1024);
-    }
-}
-
 // M/N-contiguous bf16 operand: element (k, mn) at base + k*stride + mn*2.
 struct MNOp {
     const uint8_t* base;
@@ -326,26 +300,6 @@ struct MNOp {
     int k_valid;
     int mn_valid;
 };
-
-// LDS-DMA of one K step (32 K rows x 256 columns) of an M/N-contiguous tile
-// into its natural order: instruction j of the wave covers K rows
-// (wave*4 + j)*2 .. +1; slot i is K row (wave*4+j)*2 + i/32, physical chunk
-// i%32, logical chunk (i%32) ^ ((k&3)<<2).  Rows past k_valid and columns
-// past mn_valid read zeros.  The buffer resource is rebuilt at the step's
-// first K row, so offsets stay below 32 rows whatever the K extent.
-__device__ __forceinline__ void dma_mnop(const MNOp& op, int k0, uint8_t* lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const i32x4 rs = make_rsrc(op.base + (int64_t)k0 * op.stride);
-    const uint32_t l0 = lds_u32(lds + wave * 4 * 1024);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        int k = (wave * 4 + j) * 2 + (lane >> 5);
-        int c = (lane & 31) ^ ((k & 3) << 2);
-        bool ok = k0 + k < op.k_valid && c * 8 < op.mn_valid;
-        uint32_t o = ok ? (uint32_t)(k * op.stride) + (uint32_t)(c * 16) : kOob;
-        dma16(rs, o, l0 + j * 1024);
-    }
-}
 
 // K-packed bf16 fragment (8 K-values, K sub-step s, columns colbase..+31) of
 // an M/N-contiguous LDS tile, via two transposing reads: in each 16-lane
@@ -364,8 +318,14 @@ __device__ __forceinline__ bf16x8_t mn_frag(const uint8_t* lds, int s, int colba
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// A lane's side of the bf16 loops' DMA: offsets that do not change with the K
-// step, so that a DMA costs one or two vector instructions.
+// A lane's side of the operands' LDS-DMA: offsets that do not change with the
+// K step, so that a DMA costs one or two vector instructions.  An operand's K
+// step takes 4 instructions of each wave.
+//
+// K-contiguous tiles: instruction j covers tile rows (wave*4 + j)*16 .. +15;
+// slot i of it is tile row (wave*4 + j)*16 + i/4 and physical chunk i%4, whose
+// logical chunk is (i%4) ^ ((row>>2)&3) = (i%4) ^ ((i>>4)&3).  Steps past the
+// K extent read zeros.
 template <int L>
 struct Lane;
 template <>
@@ -385,6 +345,30 @@ struct Lane<L_KMAJ> {
         return o[j] + (kt * kRowB < kbytes ? (uint32_t)(kt * kRowB) : kOob);
     }
 };
+// The same for the 8-bit operands (row-pair layout; K extents of whole blocks
+// of 32, so the last step may be half a step).
+struct LaneP2 {
+    uint32_t o[4];
+    int lc16, kbytes;
+    __device__ __forceinline__ void init(const KOp& op, int lane, int wave) {
+        lc16 = ((lane & 3) ^ ((lane >> 4) & 3)) << 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int gr = kop_row(op, (wave * 4 + j) * 16 + (lane >> 2));
+            o[j] = (uint32_t)(gr >> 1) * (uint32_t)op.stride + (uint32_t)((gr & 1) * 64 + lc16);
+        }
+        kbytes = op.kbytes;
+    }
+    __device__ __forceinline__ uint32_t off(int kt, int j) const {
+        return lc16 < kbytes - kt * kRowB ? o[j] + (uint32_t)(2 * kt * kRowB) : kOob;
+    }
+};
+// M/N-contiguous tiles (32 K rows x 256 columns in their natural order):
+// instruction j covers K rows (wave*4 + j)*2 .. +1; slot i is K row
+// (wave*4+j)*2 + i/32, physical chunk i%32, logical chunk (i%32) ^ ((k&3)<<2).
+// Rows past k_valid and columns past mn_valid read zeros.  The buffer resource
+// is rebuilt at the step's first K row, so offsets stay below 32 rows whatever
+// the K extent.
 template <>
 struct Lane<L_MNMAJ> {
     uint32_t o[4];
@@ -1113,10 +1097,10 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
-    // One batch of loads per K step, always issued in the same order and
-    // number (DMA A: 4, DMA B: 4, MXFP8 scales: 1) so that "wait until at
-    // most two batches are outstanding" is a fixed vmcnt.  Steps past the end
-    // read zeros into stages that are never consumed.
+    // One batch of loads per K step, always the same number (DMA A: 4, DMA B:
+    // 4, MXFP8 scales: 1) so that "wait until at most two batches are
+    // outstanding" is a fixed vmcnt.  Steps past the end read zeros into
+    // stages that are never consumed.
     constexpr int kBatch = 8 + (DT != DT_BF16 ? 1 : 0);
     constexpr int kWait2 = 2 * kBatch;                           // vmcnt(2 batches)
     // (M/N-contiguous operands build their buffer resource per K step)
@@ -1127,17 +1111,6 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     auto stage_ptr = [&](auto S) -> uint8_t* {
         constexpr int st = decltype(S)::value % kStages;
         return st == 0 ? lds0 : st == 1 ? lds1 : st == 2 ? lds2 : lds3;
-    };
-    // issue the loads of K step kt into stage S
-    auto issue = [&](auto S, int kt) {
-        constexpr int st = decltype(S)::value % kStages;
-        uint8_t* base = stage_ptr(S);
-        if (LA == L_KMAJ) dma_kop<kP2>(ka, rs_a, kt * kRowB, base);
-        else dma_mnop(ma, kt * 32, base);
-        if (LB == L_KMAJ) dma_kop<kP2>(kb, rs_b, kt * kRowB, base + kTileB);
-        else dma_mnop(mb, kt * 32, base + kTileB);
-        if (DT != DT_BF16)
-            dma_scales(rs_sa, rs_sb, soff_a, soff_b, sld_a, sld_b, kt, nblk, ssc[st]);
     };
 
     const int fr = lane & 31, hi = lane >> 5;
@@ -1157,136 +1130,23 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     struct FragsBF { bf16x8_t a[2][4]; bf16x8_t b[2][4]; };
     using Frags = std::conditional_t<DT == DT_BF16, FragsBF, FragsMX>;
 
-    // LDS -> registers: every fragment of the K step held in stage S
-    auto load = [&](auto S, Frags& F) {
-        constexpr int st = decltype(S)::value % kStages;
-        const uint8_t* A = stage_ptr(S);
-        const uint8_t* B = A + kTileB;
-        if constexpr (DT == DT_BF16) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-#pragma unroll
-                for (int fj = 0; fj < 4; ++fj) {
-                    if (LB == L_KMAJ)
-                        F.b[s][fj] = *(const bf16x8_t*)(B + (s ? oB2 : oB0) + fj * kFragB);
-                    else
-                        F.b[s][fj] = mn_frag(B, s, wn * 128 + fj * 32);
-                }
-#pragma unroll
-                for (int fi = 0; fi < 4; ++fi) {
-                    if (LA == L_KMAJ)
-                        F.a[s][fi] = *(const bf16x8_t*)(A + (s ? oA2 : oA0) + fi * kFragB);
-                    else
-                        F.a[s][fi] = mn_frag(A, s, wm * 128 + fi * 32);
-                }
-            }
-        } else {
-            // Operand layout of the scaled 32x32x64 MFMA: lane (row r, half h)
-            // holds K [16h, 16h+16) and [32+16h, 32+16h+16) of the 64-K step;
-            // the E8M0 scale of K-block 0 of row r is taken from lane r, that
-            // of block 1 from lane r+32 (byte h of the staged scale pair).
-#pragma unroll
-            for (int fj = 0; fj < 4; ++fj) {
-                int row = wn * 128 + fj * 32 + fr;
-                u32x4 lo = *(const u32x4*)(B + oB0 + fj * kFragB);
-                u32x4 up = *(const u32x4*)(B + oB2 + fj * kFragB);
-                F.b[fj] = (i32x8){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                                  (int)up[0], (int)up[1], (int)up[2], (int)up[3]};
-                F.sb[fj] = ssc[st][1][hi][row];          // byte -> low 8 bits
-            }
-#pragma unroll
-            for (int fi = 0; fi < 4; ++fi) {
-                int row = wm * 128 + fi * 32 + fr;
-                u32x4 lo = *(const u32x4*)(A + oA0 + fi * kFragB);
-                u32x4 up = *(const u32x4*)(A + oA2 + fi * kFragB);
-                F.a[fi] = (i32x8){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                                  (int)up[0], (int)up[1], (int)up[2], (int)up[3]};
-                F.sa[fi] = ssc[st][0][hi][row];
-            }
-        }
-    };
-    // the MFMAs of fragment rows [FI0, FI1) of one K step; each accumulator
-    // takes the step's K values in increasing order whatever the split
-    auto mma = [&](auto FI0, auto FI1, const Frags& F) {
-        constexpr int f0 = decltype(FI0)::value, f1 = decltype(FI1)::value;
-#pragma unroll
-        for (int fi = f0; fi < f1; ++fi) {
-            if constexpr (DT == DT_BF16) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int fj = 0; fj < 4; ++fj)
-                        acc[fi][fj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            F.a[s][fi], F.b[s][fj], acc[fi][fj], 0, 0, 0);
-            } else {
-#pragma unroll
-                for (int fj = 0; fj < 4; ++fj)
-                    acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        F.a[fi], F.b[fj], acc[fi][fj], 0, 0, 0, (int)F.sa[fi], 0, (int)F.sb[fj]);
-            }
-        }
-    };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
     using I3 = std::integral_constant<int, 3>;
-    using I4 = std::integral_constant<int, 4>;
-    // fragment rows whose MFMAs run after the barrier, under the next step's
-    // LDS reads: 8 of the 16 scaled MFMAs, 8 of the 32 bf16 ones (measured
-    // best; the bf16 step has 16 fragment reads against the 8-bit step's 24)
-    constexpr int kTailRows = DT == DT_BF16 ? 1 : 2;
-    using ISplit = std::integral_constant<int, 4 - kTailRows>;
-    // One K step kt whose fragments are in Fc (read from stage S): prefetch
-    // step kt+3 into stage S+3 (whose reads all finished before the previous
-    // barrier), run most MFMAs, wait until batch kt+1 has landed in every
-    // wave, read its fragments into Fn, and run the remaining MFMAs.
     Frags F0, F1;
-    auto step = [&](auto S, int kt, Frags& Fc, Frags& Fn) {
-        constexpr int st = decltype(S)::value;
-        // (scheduling barriers keep the compiler from sinking the reads of Fn
-        // to their first use, which would stall the next step's MFMAs on LDS)
-        issue(std::integral_constant<int, (st + 3) % kStages>{}, kt + 3);
-        mma(I0{}, ISplit{}, Fc);
-        __builtin_amdgcn_sched_barrier(0);
-        pipe_barrier<kWait2>();                                  // batch kt+1 has landed
-        __builtin_amdgcn_sched_barrier(0);
-        load(std::integral_constant<int, (st + 1) % kStages>{}, Fn);
-        mma(ISplit{}, I4{}, Fc);
-        // The next step's LDS reads spread between the MFMAs after the
-        // barrier, the first MFMA ahead of them: the matrix pipe stays busy
-        // while the reads trickle into LDS, and every read has several MFMAs
-        // to land behind.  (Left to itself the compiler put all reads after
-        // the sixth MFMA, two MFMAs before their first use; all 24 reads up
-        // front, ahead of the MFMAs, was slower still.)
-        if constexpr (DT == DT_BF16) {
-            // reads per step: 8 per K-contiguous operand, 16 (transposing
-            // 8-byte reads) per M/N-contiguous one
-            constexpr int kReads = (LA == L_KMAJ ? 8 : 16) + (LB == L_KMAJ ? 8 : 16);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x100, kReads / 8, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // 1 MFMA
-            }
-        } else {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-#pragma unroll
-            for (int i = 0; i < 6; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            }
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-
+    // The K loop.  The barrier stands at the start of a step and publishes the
+    // next step's stage, so that everything the step issues (its DMAs, the
+    // next step's fragment reads and its MFMAs) is spread evenly over it: one
+    // wave per SIMD has nothing but its own instructions to keep the matrix
+    // pipe busy with while the LDS serves 64 KiB of reads.  Step kt loads batch
+    // kt+4 into its own stage: every wave has finished that stage's reads
+    // (lgkmcnt(0)) before the barrier.  Against the barrier after three
+    // quarters of the step's MFMAs, with the reads behind it and the DMAs in
+    // front (Mixtral shape, ms): bf16 forward 5.18 -> 5.08, backward 10.05 ->
+    // 9.61; MXFP8 5.38 -> 5.30 backward, and 196 -> 184 us for 5105 rows of
+    // 1024 x 1536 experts.
     if constexpr (DT == DT_BF16) {
-        // bf16: the barrier stands at the start of a step and publishes the
-        // next step's stage, so that everything the step issues, 8 DMAs, the
-        // next step's fragment reads and 32 MFMAs, is spread evenly over it:
-        // one wave per SIMD has nothing but its own instructions to keep the
-        // matrix pipe busy with while the LDS serves 64 KiB of reads.  Step kt
-        // loads batch kt+4 into its own stage: every wave had finished that
-        // stage's reads before the barrier.
         Lane<LA> da;
         Lane<LB> db;
         if constexpr (LA == L_KMAJ) da.init(ka, lane, wave); else da.init(ma, lane, wave);
@@ -1367,27 +1227,96 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
         if (kt + 2 < nk) bstep(I2{}, kt + 2, F0, F1);
         __builtin_amdgcn_sched_barrier(0);
     } else {
-    if (nk > 0) {
-        issue(I0{}, 0);
-        issue(I1{}, 1);
-        issue(I2{}, 2);
-    }
-    pipe_barrier<kWait2>();                                      // batch 0 has landed
-    load(I0{}, F0);
-    __builtin_amdgcn_sched_barrier(0);
-    // whole groups of four steps, then the rest: a conditional step inside
-    // the loop body makes the register allocator shuttle accumulators
-    // between register files on every iteration
-    int kt = 0;
-    for (; kt + kStages <= nk; kt += kStages) {
-        step(I0{}, kt, F0, F1);
-        step(I1{}, kt + 1, F1, F0);
-        step(I2{}, kt + 2, F0, F1);
-        step(I3{}, kt + 3, F1, F0);
-    }
-    if (kt < nk) step(I0{}, kt, F0, F1);
-    if (kt + 1 < nk) step(I1{}, kt + 1, F1, F0);
-    if (kt + 2 < nk) step(I2{}, kt + 2, F0, F1);
+        // 8-bit: a block of the step is 2 MFMAs, one DMA and the
+        // three reads of one fragment (two of codes, one of scales)
+        LaneP2 da, db;
+        da.init(ka, lane, wave);
+        db.init(kb, lane, wave);
+        auto dma = [&](auto S, int kt, int j) {       // instruction j of 8 of batch kt
+            uint8_t* base = stage_ptr(S);
+            const uint32_t l0 = lds_u32(base + wave * 4096) + (j & 3) * 1024;
+            if (j < 4) dma16(rs_a, da.off(kt, j), l0);
+            else dma16(rs_b, db.off(kt, j - 4), l0 + kTileB);
+        };
+        auto scales = [&](auto S, int kt) {
+            dma_scales(rs_sa, rs_sb, soff_a, soff_b, sld_a, sld_b, kt, nblk,
+                       ssc[decltype(S)::value % kStages]);
+        };
+        // Operand layout of the scaled 32x32x64 MFMA: lane (row r, half h)
+        // holds K [16h, 16h+16) and [32+16h, 32+16h+16) of the 64-K step; the
+        // E8M0 scale of K-block 0 of row r is taken from lane r, that of block
+        // 1 from lane r+32 (byte h of the staged scale pair).
+        auto read_b = [&](auto S, Frags& F, int f) {
+            constexpr int st = decltype(S)::value % kStages;
+            const uint8_t* B = stage_ptr(S) + kTileB;
+            const u32x4 lo = *(const u32x4*)(B + oB0 + f * kFragB);
+            const u32x4 up = *(const u32x4*)(B + oB2 + f * kFragB);
+            F.b[f] = (i32x8){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                             (int)up[0], (int)up[1], (int)up[2], (int)up[3]};
+            F.sb[f] = ssc[st][1][hi][wn * 128 + f * 32 + fr];    // byte -> low 8 bits
+        };
+        auto read_a = [&](auto S, Frags& F, int f) {
+            constexpr int st = decltype(S)::value % kStages;
+            const uint8_t* A = stage_ptr(S);
+            const u32x4 lo = *(const u32x4*)(A + oA0 + f * kFragB);
+            const u32x4 up = *(const u32x4*)(A + oA2 + f * kFragB);
+            F.a[f] = (i32x8){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                             (int)up[0], (int)up[1], (int)up[2], (int)up[3]};
+            F.sa[f] = ssc[st][0][hi][wm * 128 + f * 32 + fr];
+        };
+        // fragment n of 8, in the order in which the step uses them
+        auto read = [&](auto S, Frags& F, int n) {
+            if (n == 0) read_b(S, F, 0);
+            else if (n == 1) read_a(S, F, 0);
+            else if (n < 5) read_b(S, F, n - 1);
+            else read_a(S, F, n - 4);
+        };
+        auto qstep = [&](auto S, int kt, Frags& Fc, Frags& Fn) {
+            constexpr int st = decltype(S)::value;
+            using Next = std::integral_constant<int, (st + 1) % kStages>;
+            __builtin_amdgcn_sched_barrier(0);
+            pipe_barrier<kWait2>();                   // batch kt+1 has landed
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {             // block i: 2 MFMAs
+                const int fi = i >> 1, f0 = 2 * (i & 1);
+                acc[fi][f0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    Fc.a[fi], Fc.b[f0], acc[fi][f0], 0, 0, 0, (int)Fc.sa[fi], 0, (int)Fc.sb[f0]);
+                __builtin_amdgcn_sched_barrier(0);
+                dma(S, kt + 4, i);
+                if (i == 0) scales(S, kt + 4);
+                __builtin_amdgcn_sched_barrier(0);
+                acc[fi][f0 + 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    Fc.a[fi], Fc.b[f0 + 1], acc[fi][f0 + 1], 0, 0, 0, (int)Fc.sa[fi], 0,
+                    (int)Fc.sb[f0 + 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                read(Next{}, Fn, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        auto whole = [&](auto S, int kt) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dma(S, kt, j);
+            scales(S, kt);
+        };
+        whole(I0{}, 0);
+        whole(I1{}, 1);
+        whole(I2{}, 2);
+        whole(I3{}, 3);
+        pipe_barrier<3 * kBatch>();                   // batch 0 has landed
+#pragma unroll
+        for (int n = 0; n < 8; ++n) read(I0{}, F0, n);
+        int kt = 0;
+        for (; kt + kStages <= nk; kt += kStages) {
+            qstep(I0{}, kt, F0, F1);
+            qstep(I1{}, kt + 1, F1, F0);
+            qstep(I2{}, kt + 2, F0, F1);
+            qstep(I3{}, kt + 3, F1, F0);
+        }
+        if (kt < nk) qstep(I0{}, kt, F0, F1);
+        if (kt + 1 < nk) qstep(I1{}, kt + 1, F1, F0);
+        if (kt + 2 < nk) qstep(I2{}, kt + 2, F0, F1);
+        __builtin_amdgcn_sched_barrier(0);
     }
     // the look-ahead batches past the end still write LDS: drain them before
     // the epilogue reuses it
