@@ -33,7 +33,7 @@
 //     streaming stores.
 //   * M/N-contiguous bf16 operands (the dgrad weights and both weight-gradient
 //     operands) are staged in LDS in their natural [k][m] order (16-byte
-//     chunks of a 512-byte row XOR-ed with 4*(k&3)) and turned into K-packed
+//     chunks of a 512-byte row XOR-ed by K row) and turned into K-packed
 //     MFMA fragments by ds_read_b64_tr_b16, which transposes 4 K-rows x 16
 //     columns across each 16-lane group, so no transposed copy is written.
 //   * MXFP8 operands carry block-major scales ([K/32][rows]); one dword per
@@ -77,9 +77,19 @@ constexpr uint32_t kOob = 0x80000000u;        // buffer offset that reads zeros
 __device__ __forceinline__ int lds_off(int row, int chunk) {
     return row * kRowB + ((chunk ^ ((row >> 2) & 3)) << 4);
 }
-// M/N-contiguous tile: K row k (32 per stage), 16-byte chunk c (32 per row)
+// The same tile as the 16-row bf16 fragments read it (16 rows x 4 chunks): an
+// LDS read of 16 bytes per lane takes its lanes in groups that mix two chunks
+// of different rows, which XOR with 2 in every other 8 rows keeps apart.
+__device__ __forceinline__ int lds_off16(int row, int chunk) {
+    return row * kRowB + ((chunk ^ (((row >> 3) & 1) << 1)) << 4);
+}
+// M/N-contiguous tile: K row k (32 per stage), 16-byte chunk c (32 per row).
+// A transposing read takes 32 bytes of rows k..k+3 and of rows 8 below in one
+// go: the XOR puts the four rows in different quarters of 256 bytes and the
+// two sets in different halves of a quarter.
+__device__ __forceinline__ int mn_swizzle(int k) { return ((k & 3) << 2) ^ ((k >> 2) & 2); }
 __device__ __forceinline__ int mn_off(int k, int c) {
-    return k * kMNRowB + ((c ^ ((k & 3) << 2)) << 4);
+    return k * kMNRowB + ((c ^ mn_swizzle(k)) << 4);
 }
 
 // Per-workgroup tile descriptor.
@@ -301,15 +311,15 @@ struct MNOp {
     int mn_valid;
 };
 
-// K-packed bf16 fragment (8 K-values, K sub-step s, columns colbase..+31) of
-// an M/N-contiguous LDS tile, via two transposing reads: in each 16-lane
-// group g, lane q supplies (K row kb + q/4, columns n..n+3) and receives
-// column n0 + q for 4 consecutive K rows.
-__device__ __forceinline__ bf16x8_t mn_frag(const uint8_t* lds, int s, int colbase) {
+// K-packed bf16 fragment (16 columns from colbase, the 32 K-values of a step,
+// 8 per 16-lane group) of an M/N-contiguous LDS tile, via two transposing
+// reads: in each 16-lane group g, lane q supplies (K row kb + q/4, columns
+// n..n+3) and receives column colbase + q for 4 consecutive K rows.
+__device__ __forceinline__ bf16x8_t mn_frag(const uint8_t* lds, int colbase) {
     const int lane = threadIdx.x & 63;
     const int g = lane >> 4, q = lane & 15;
-    const int kb = 16 * s + 8 * (g >> 1) + (q >> 2);
-    const int n = colbase + 16 * (g & 1) + 4 * (q & 3);       // element column
+    const int kb = 8 * g + (q >> 2);
+    const int n = colbase + 4 * (q & 3);                       // element column
     const int c = n >> 3, sub = (n & 7) * 2;                   // 16-byte chunk, byte in chunk
     i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds + mn_off(kb, c) + sub));
     i16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -324,8 +334,9 @@ __device__ __forceinline__ bf16x8_t mn_frag(const uint8_t* lds, int s, int colba
 //
 // K-contiguous tiles: instruction j covers tile rows (wave*4 + j)*16 .. +15;
 // slot i of it is tile row (wave*4 + j)*16 + i/4 and physical chunk i%4, whose
-// logical chunk is (i%4) ^ ((row>>2)&3) = (i%4) ^ ((i>>4)&3).  Steps past the
-// K extent read zeros.
+// logical chunk is (i%4) ^ 2 ((row>>3)&1) = (i%4) ^ 2 (i>>5) (bf16, lds_off16)
+// or (i%4) ^ ((row>>2)&3) = (i%4) ^ ((i>>4)&3) (8-bit, lds_off).  Steps past
+// the K extent read zeros.
 template <int L>
 struct Lane;
 template <>
@@ -333,7 +344,7 @@ struct Lane<L_KMAJ> {
     uint32_t o[4];
     int kbytes;
     __device__ __forceinline__ void init(const KOp& op, int lane, int wave) {
-        const int lc16 = ((lane & 3) ^ ((lane >> 4) & 3)) << 4;
+        const int lc16 = ((lane & 3) ^ ((lane >> 5) << 1)) << 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int gr = kop_row(op, (wave * 4 + j) * 16 + (lane >> 2));
@@ -365,7 +376,7 @@ struct LaneP2 {
 };
 // M/N-contiguous tiles (32 K rows x 256 columns in their natural order):
 // instruction j covers K rows (wave*4 + j)*2 .. +1; slot i is K row
-// (wave*4+j)*2 + i/32, physical chunk i%32, logical chunk (i%32) ^ ((k&3)<<2).
+// (wave*4+j)*2 + i/32, physical chunk i%32, logical chunk (i%32) ^ mn_swizzle(k).
 // Rows past k_valid and columns past mn_valid read zeros.  The buffer resource
 // is rebuilt at the step's first K row, so offsets stay below 32 rows whatever
 // the K extent.
@@ -384,7 +395,7 @@ struct Lane<L_MNMAJ> {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int k = w2 + j * 2 + hi;
-            const int c = (lane & 31) ^ ((k & 3) << 2);
+            const int c = (lane & 31) ^ mn_swizzle(k);
             o[j] = c * 8 < op.mn_valid ? (uint32_t)(k * op.stride) + (uint32_t)(c * 16) : kOob;
         }
     }
@@ -494,6 +505,107 @@ __device__ __forceinline__ void stage_pairs_bf16(uint32_t* P, const f32x16& f0, 
         }
 }
 
+// The same two stagings from 16 x 16 fragments (bf16): value v of fragment
+// (h, n) of a 32-row slice is row 16 h + 4 g + v, column 16 n + c (lane = 16 g
+// + c).  In the pair staging columns are XOR-ed with 16 in every other pair of
+// row pairs, so that the four row groups of a write meet two at a time in the
+// banks, which the write takes two cycles for anyway.
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+
+__device__ __forceinline__ void stage_fragments16(float* R, const f32x4 (&r0)[8],
+                                                  const f32x4 (&r1)[8], int lane) {
+    const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        float* even = R + st_idx(4 * g + v, c);           // fragments 0, 2, .. of the row
+        float* odd = R + st_idx(4 * g + v, 16 + c);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            even[32 * p] = r0[2 * p][v];
+            odd[32 * p] = r0[2 * p + 1][v];
+            even[16 * 128 + 32 * p] = r1[2 * p][v];
+            odd[16 * 128 + 32 * p] = r1[2 * p + 1][v];
+        }
+    }
+}
+
+__device__ __forceinline__ void stage_pairs16(uint32_t* P, const f32x4 (&r0)[8],
+                                              const f32x4 (&r1)[8], int lane) {
+    const int c = lane & 15, g = lane >> 4, x = 16 * (g & 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const f32x4& f = h ? r1[n] : r0[n];
+                P[(8 * h + 2 * g + w) * 128 + ((16 * n + c) ^ x)] =
+                    pack_bf16x2(f[2 * w], f[2 * w + 1]);
+            }
+}
+
+// The accumulators of a wave's 128 x 128 result and their way into LDS, 32 rows
+// (slice fi) at a time.  bf16: 16 x 16 x 32 products, which sum the same K
+// values in the same order as two 32 x 32 x 16 ones (the same bits) and draw
+// less power: with nothing but products, 1.99 against 1.76 PFLOP/s.
+template <int DT>
+struct Acc {
+    f32x16 v[4][4];
+    static constexpr int kPairXor = 0;
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[i][j][k] = 0.f;
+    }
+    __device__ __forceinline__ void stage(float* R, int fi, int lane) const {
+        stage_fragments(R, v[fi][0], v[fi][1], v[fi][2], v[fi][3], lane);
+    }
+    __device__ __forceinline__ void pairs(uint32_t* P, int fi, int lane) const {
+        stage_pairs_bf16(P, v[fi][0], v[fi][1], v[fi][2], v[fi][3], lane);
+    }
+};
+template <>
+struct Acc<DT_BF16> {
+    f32x4 v[8][8];
+    static constexpr int kPairXor = 16;
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        settle();
+    }
+    // Written as assembly to keep the accumulator in place: the builtin's
+    // result may go to other registers than its third operand, and the
+    // register allocator made use of it, rotating the accumulators through
+    // about 75 moves per K step.  The compiler does not see a matrix
+    // instruction here, so the waits it would insert are kept by hand: the
+    // operands come from LDS (whose waits it does insert) and the zeros, and
+    // the results leave, through settle().
+    __device__ __forceinline__ void mma(int i, int j, const bf16x8_t& a, const bf16x8_t& b) {
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
+                     : "+a"(v[i][j]) : "v"(a), "v"(b));
+    }
+    // Ordinary instructions and products on either side: 20 wait states, more
+    // than any matrix instruction's result needs before it is read.
+    __device__ __forceinline__ void settle() {
+        asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(v[i][j]));
+    }
+    __device__ __forceinline__ void stage(float* R, int fi, int lane) const {
+        stage_fragments16(R, v[2 * fi], v[2 * fi + 1], lane);
+    }
+    __device__ __forceinline__ void pairs(uint32_t* P, int fi, int lane) const {
+        stage_pairs16(P, v[2 * fi], v[2 * fi + 1], lane);
+    }
+};
+
 __device__ __forceinline__ void load_row8(const float* R, int row, int col, float (&x)[8]) {
     float4 a = *(const float4*)(R + st_idx(row, col));
     float4 b = *(const float4*)(R + st_idx(row, col + 4));
@@ -570,14 +682,13 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {
 // a value instead of 2, and no second read of the staged values; ordinary
 // stores, since a wave's 64-byte row pieces meet their neighbours' in L2.
 template <int DT, bool kCk>
-__device__ __forceinline__ void swiglu_fwd_rows(const EpiCtx& c, float* R, const f32x16& f0,
-                                                const f32x16& f1, const f32x16& f2,
-                                                const f32x16& f3, int fi, uint32_t& amx) {
+__device__ __forceinline__ void swiglu_fwd_rows(const EpiCtx& c, float* R, const Acc<DT>& acc,
+                                                int fi, uint32_t& amx) {
     const GemmArgs& g = c.g;
     const Tile& tl = c.tl;
     const int lane = c.lane;
     const int64_t I = g.I;
-    stage_fragments(R, f0, f1, f2, f3, lane);
+    acc.stage(R, fi, lane);
     wave_lds_sync();
     const int frow0 = tl.m0 + c.wm * 128 + fi * 32;      // row inside the expert
     const int valid = min(32, tl.rows_e - frow0);          // rows of this slice that exist
@@ -816,14 +927,13 @@ __device__ __forceinline__ float pair_up(float x) { return hi_bf16(__float_as_ui
 // The saved A1 comes as bf16 (A1Words) or as MXFP8 codes (A1Codes).
 template <int DT, class Saved>
 __device__ __forceinline__ void swiglu_bwd_rows(const EpiCtx& c, float* R, float* R2,
-                                                float* red, const f32x16& f0, const f32x16& f1,
-                                                const f32x16& f2, const f32x16& f3, int fi,
+                                                float* red, const Acc<DT>& acc, int fi,
                                                 uint32_t& amx, Saved& w) {
     const GemmArgs& g = c.g;
     const Tile& tl = c.tl;
     const int lane = c.lane;
     const int64_t I = g.I;
-    stage_fragments(R, f0, f1, f2, f3, lane);
+    acc.stage(R, fi, lane);
     wave_lds_sync();
     const int frow0 = tl.m0 + c.wm * 128 + fi * 32;
     const int valid = min(32, tl.rows_e - frow0);
@@ -1089,13 +1199,8 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     constexpr int kStepElems = DT == DT_BF16 ? 32 : 64;   // K per stage (64 bytes per row)
     const int nk = (kext + kStepElems - 1) / kStepElems;
 
-    f32x16 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    Acc<DT> acc;
+    acc.zero();
 
     // One batch of loads per K step, always the same number (DMA A: 4, DMA B:
     // 4, MXFP8 scales: 1) so that "wait until at most two batches are
@@ -1127,7 +1232,7 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     // k+1 fill the other, so LDS latency is hidden behind matrix work instead
     // of stalling the wave before each group of MFMAs.
     struct FragsMX { i32x8 a[4]; i32x8 b[4]; uint32_t sa[4]; uint32_t sb[4]; };
-    struct FragsBF { bf16x8_t a[2][4]; bf16x8_t b[2][4]; };
+    struct FragsBF { bf16x8_t a[8]; bf16x8_t b[8]; };
     using Frags = std::conditional_t<DT == DT_BF16, FragsBF, FragsMX>;
 
     using I0 = std::integral_constant<int, 0>;
@@ -1162,26 +1267,24 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
                 else dma16(db.rsrc(kt), db.off(kt, j - 4), l0 + kTileB);
             }
         };
-        auto read_a = [&](const uint8_t* A, Frags& F, int s, int f) {
-            if constexpr (LA == L_KMAJ)
-                F.a[s][f] = *(const bf16x8_t*)(A + (s ? oA2 : oA0) + f * kFragB);
-            else
-                F.a[s][f] = mn_frag(A, s, wm * 128 + f * 32);
+        // K-contiguous fragments: lane (row r of 16, 16-byte chunk of the step's
+        // 64 bytes); 16 f rows leave the chunk swizzle unchanged
+        const int oA = lds_off16(wm * 128 + (lane & 15), lane >> 4);
+        const int oB = lds_off16(wn * 128 + (lane & 15), lane >> 4);
+        auto read_a = [&](const uint8_t* A, Frags& F, int f) {
+            if constexpr (LA == L_KMAJ) F.a[f] = *(const bf16x8_t*)(A + oA + f * 16 * kRowB);
+            else F.a[f] = mn_frag(A, wm * 128 + f * 16);
         };
-        auto read_b = [&](const uint8_t* B, Frags& F, int s, int f) {
-            if constexpr (LB == L_KMAJ)
-                F.b[s][f] = *(const bf16x8_t*)(B + (s ? oB2 : oB0) + f * kFragB);
-            else
-                F.b[s][f] = mn_frag(B, s, wn * 128 + f * 32);
+        auto read_b = [&](const uint8_t* B, Frags& F, int f) {
+            if constexpr (LB == L_KMAJ) F.b[f] = *(const bf16x8_t*)(B + oB + f * 16 * kRowB);
+            else F.b[f] = mn_frag(B, wn * 128 + f * 16);
         };
         // fragment read n of 16, in the order in which the step uses them
         auto read = [&](auto S, Frags& F, int n) {
             const uint8_t* A = stage_ptr(S);
-            const uint8_t* B = A + kTileB;
-            if (n < 4) read_b(B, F, 0, n);
-            else if (n == 4) read_a(A, F, 0, 0);
-            else if (n < 9) read_b(B, F, 1, n - 5);
-            else read_a(A, F, n == 9 || ((n & 1) && n > 10), (n - 8) / 2);
+            if (n == 0) read_a(A, F, 0);
+            else if (n < 9) read_b(A + kTileB, F, n - 1);
+            else read_a(A, F, n - 8);
         };
         auto bstep = [&](auto S, int kt, Frags& Fc, Frags& Fn) {
             constexpr int st = decltype(S)::value;
@@ -1190,16 +1293,14 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
             pipe_barrier<kWait2>();                   // batch kt+1 has landed
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {             // block i: 4 MFMAs
-                const int fi = i >> 1, s = i & 1;
-                const int r0 = i < 2 ? 3 * i : 2 * i + 2, r1 = i < 2 ? r0 + 3 : r0 + 2;
+            for (int i = 0; i < 8; ++i) {             // block i: 8 MFMAs, one DMA, 2 or 3 reads
+                const int r0 = i < 2 ? 3 * i : 2 * i + 2, nr = i < 2 ? 3 : i < 7 ? 2 : 0;
 #pragma unroll
-                for (int fj = 0; fj < 4; ++fj) {
-                    acc[fi][fj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        Fc.a[s][fi], Fc.b[s][fj], acc[fi][fj], 0, 0, 0);
+                for (int j = 0; j < 8; ++j) {
+                    acc.mma(i, j, Fc.a[i], Fc.b[j]);
                     __builtin_amdgcn_sched_barrier(0);
-                    if (fj == 0) dma(S, kt + 4, i);
-                    if (fj > 0 && r0 + fj - 1 < r1 && r0 + fj - 1 < 16) read(Next{}, Fn, r0 + fj - 1);
+                    if (j == 1) dma(S, kt + 4, i);
+                    if (j >= 3 && (j & 1) && (j - 3) / 2 < nr) read(Next{}, Fn, r0 + (j - 3) / 2);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -1226,6 +1327,7 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
         if (kt + 1 < nk) bstep(I1{}, kt + 1, F1, F0);
         if (kt + 2 < nk) bstep(I2{}, kt + 2, F0, F1);
         __builtin_amdgcn_sched_barrier(0);
+        acc.settle();
     } else {
         // 8-bit: a block of the step is 2 MFMAs, one DMA and the
         // three reads of one fragment (two of codes, one of scales)
@@ -1280,14 +1382,14 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {             // block i: 2 MFMAs
                 const int fi = i >> 1, f0 = 2 * (i & 1);
-                acc[fi][f0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    Fc.a[fi], Fc.b[f0], acc[fi][f0], 0, 0, 0, (int)Fc.sa[fi], 0, (int)Fc.sb[f0]);
+                acc.v[fi][f0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    Fc.a[fi], Fc.b[f0], acc.v[fi][f0], 0, 0, 0, (int)Fc.sa[fi], 0, (int)Fc.sb[f0]);
                 __builtin_amdgcn_sched_barrier(0);
                 dma(S, kt + 4, i);
                 if (i == 0) scales(S, kt + 4);
                 __builtin_amdgcn_sched_barrier(0);
-                acc[fi][f0 + 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    Fc.a[fi], Fc.b[f0 + 1], acc[fi][f0 + 1], 0, 0, 0, (int)Fc.sa[fi], 0,
+                acc.v[fi][f0 + 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    Fc.a[fi], Fc.b[f0 + 1], acc.v[fi][f0 + 1], 0, 0, 0, (int)Fc.sa[fi], 0,
                     (int)Fc.sb[f0 + 1]);
                 __builtin_amdgcn_sched_barrier(0);
                 read(Next{}, Fn, i);
@@ -1364,14 +1466,15 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
 #pragma unroll
         for (int fr = 0; fr < 4; ++fr) {
             const int fi = 3 - fr;
-            stage_pairs_bf16(P, acc[fi][0], acc[fi][1], acc[fi][2], acc[fi][3], ln);
+            acc.pairs(P, fi, ln);
             wave_lds_sync();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int p = r0 + 4 * i;                          // row pair of the slice
                 const int urow = wm * 128 + fi * 32 + 8 * i;       // uniform
-                const u32x4 d0 = *(const u32x4*)(P + p * 128 + c8);
-                const u32x4 d1 = *(const u32x4*)(P + p * 128 + c8 + 4);
+                const uint32_t* d = P + p * 128 + (c8 ^ ((p >> 1) & 1) * Acc<DT>::kPairXor);
+                const u32x4 d0 = ((const u32x4*)d)[0];
+                const u32x4 d1 = ((const u32x4*)d)[1];
                 u32x4 lo, hi2;
                 lo[0] = __builtin_amdgcn_perm(d0[1], d0[0], 0x05040100u);
                 lo[1] = __builtin_amdgcn_perm(d0[3], d0[2], 0x05040100u);
@@ -1414,10 +1517,10 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
         uint32_t amx = 0;
         // (slices in reverse order, as in the plain-store epilogue: no
         // accumulator fragment is parked in scratch memory)
-        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc[3][0], acc[3][1], acc[3][2], acc[3][3], 3, amx);
-        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc[2][0], acc[2][1], acc[2][2], acc[2][3], 2, amx);
-        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc[1][0], acc[1][1], acc[1][2], acc[1][3], 1, amx);
-        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc[0][0], acc[0][1], acc[0][2], acc[0][3], 0, amx);
+        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc, 3, amx);
+        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc, 2, amx);
+        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc, 1, amx);
+        swiglu_fwd_rows<DT, epi_ck(EPI)>(c, R, acc, 0, amx);
         if (kAmax) amax_to_part(amx, (uint32_t*)sched, g.amax_part);
         return;
     }
@@ -1428,10 +1531,10 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
         float* R2 = R + 32 * 128;
         uint32_t amx = 0;
         // (slices in reverse order: no accumulator fragment parked in scratch)
-        swiglu_bwd_rows<DT>(c, R, R2, red, acc[3][0], acc[3][1], acc[3][2], acc[3][3], 3, amx, a1w);
-        swiglu_bwd_rows<DT>(c, R, R2, red, acc[2][0], acc[2][1], acc[2][2], acc[2][3], 2, amx, a1w);
-        swiglu_bwd_rows<DT>(c, R, R2, red, acc[1][0], acc[1][1], acc[1][2], acc[1][3], 1, amx, a1w);
-        swiglu_bwd_rows<DT>(c, R, R2, red, acc[0][0], acc[0][1], acc[0][2], acc[0][3], 0, amx, a1w);
+        swiglu_bwd_rows<DT>(c, R, R2, red, acc, 3, amx, a1w);
+        swiglu_bwd_rows<DT>(c, R, R2, red, acc, 2, amx, a1w);
+        swiglu_bwd_rows<DT>(c, R, R2, red, acc, 1, amx, a1w);
+        swiglu_bwd_rows<DT>(c, R, R2, red, acc, 0, amx, a1w);
         if (kAmax) amax_to_part(amx, (uint32_t*)sched, g.amax_part);
         __syncthreads();                    // red holds both column halves' partials
         const int t = wave * 64 + ln;
