@@ -9,11 +9,11 @@
 //
 // Work decomposition
 //   * 256 x 256 output tile per workgroup of 256 threads (4 waves, 2 x 2);
-//     every wave owns a 128 x 128 sub-tile = 4 x 4 MFMA 32x32 fragments whose
-//     256 fp32 accumulators live in the accumulation registers (one wave per
-//     SIMD, 512 registers per lane).
-//   * K steps of 64 bytes per operand row: 32 bf16 (2 x
-//     v_mfma_f32_32x32x16_bf16) or 64 E4M3 (one
+//     every wave owns a 128 x 128 sub-tile (bf16: 8 x 8 MFMA fragments of
+//     16 x 16, 8 bits: 4 x 4 of 32 x 32) whose 256 fp32 accumulators live in
+//     the accumulation registers (one wave per SIMD, 512 registers per lane).
+//   * K steps of 64 bytes per operand row: 32 bf16 (one
+//     v_mfma_f32_16x16x32_bf16 per fragment) or 64 E4M3 (one
 //     v_mfma_scale_f32_32x32x64_f8f6f4, the E8M0 scale of every 32 K-values
 //     and row fed straight to the instruction, so nothing is dequantized).
 //   * LDS holds four stages of both operand tiles (4 x 32 KiB); the loads of
@@ -21,9 +21,8 @@
 //     per step.  Operands go from memory to LDS without passing through
 //     registers (buffer_load_dwordx4 ... lds: lane l's 16 bytes land at the
 //     wave's LDS base + 16 l, so the lane picks the global chunk that fills
-//     its slot); 16-byte chunks of a 64-byte tile row are XOR-swizzled by
-//     (row >> 2) & 3 so fragment reads of 16 consecutive rows hit distinct
-//     banks.  Offsets past a row's valid K read zeros.  The fragments of
+//     its slot); 16-byte chunks of a 64-byte tile row are XOR-swizzled by row
+//     bits so that a fragment's read hits distinct banks.  Offsets past a row's valid K read zeros.  The fragments of
 //     step k+1 are read from LDS into a second register set during step k,
 //     spread between its MFMAs like the DMAs of step k+4.
 //   * Epilogues: each wave stages its 128 x 128 result through its own LDS
@@ -328,21 +327,35 @@ __device__ __forceinline__ bf16x8_t mn_frag(const uint8_t* lds, int colbase) {
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// A lane's side of the operands' LDS-DMA: offsets that do not change with the
-// K step, so that a DMA costs one or two vector instructions.  An operand's K
-// step takes 4 instructions of each wave.
+// An operand's LDS-DMA, K step after K step: 4 instructions of each wave per
+// step.
 //
 // K-contiguous tiles: instruction j covers tile rows (wave*4 + j)*16 .. +15;
 // slot i of it is tile row (wave*4 + j)*16 + i/4 and physical chunk i%4, whose
 // logical chunk is (i%4) ^ 2 ((row>>3)&1) = (i%4) ^ 2 (i>>5) (bf16, lds_off16)
-// or (i%4) ^ ((row>>2)&3) = (i%4) ^ ((i>>4)&3) (8-bit, lds_off).  Steps past
-// the K extent read zeros.
+// or (i%4) ^ ((row>>2)&3) = (i%4) ^ ((i>>4)&3) (8-bit, lds_off).
+//
+// bf16: a lane's offsets do not change with the step, which moves uniform
+// values alone (the scalar offset, the resource): no vector instruction per
+// DMA.  Steps past the K extent read zeros (a resource without records).
+struct Dma { i32x4 rs; uint32_t soff; };
+
+__device__ __forceinline__ i32x4 rsrc_at(uint64_t base, int nrec) {
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32));
+    r[2] = __builtin_amdgcn_readfirstlane(nrec);
+    r[3] = 0x00020000;
+    return r;
+}
+
 template <int L>
-struct Lane;
+struct Feed;
 template <>
-struct Lane<L_KMAJ> {
+struct Feed<L_KMAJ> {
     uint32_t o[4];
-    int kbytes;
+    uint64_t base;
+    int k, kbytes;                   // kbytes: a multiple of the step's 64 bytes
     __device__ __forceinline__ void init(const KOp& op, int lane, int wave) {
         const int lc16 = ((lane & 3) ^ ((lane >> 5) << 1)) << 4;
 #pragma unroll
@@ -350,14 +363,58 @@ struct Lane<L_KMAJ> {
             const int gr = kop_row(op, (wave * 4 + j) * 16 + (lane >> 2));
             o[j] = (uint32_t)((int64_t)gr * op.stride) + (uint32_t)lc16;
         }
-        kbytes = op.kbytes;          // a multiple of the step's 64 bytes
+        base = (uint64_t)op.base;
+        k = 0;
+        kbytes = op.kbytes;
     }
-    __device__ __forceinline__ uint32_t off(int kt, int j) const {
-        return o[j] + (kt * kRowB < kbytes ? (uint32_t)(kt * kRowB) : kOob);
+    __device__ __forceinline__ Dma next() {
+        const bool live = k < kbytes;
+        const Dma d = {rsrc_at(base, live ? 0x7fffffff : 0),
+                       (uint32_t)__builtin_amdgcn_readfirstlane(live ? k : 0)};
+        k += kRowB;
+        return d;
     }
 };
-// The same for the 8-bit operands (row-pair layout; K extents of whole blocks
-// of 32, so the last step may be half a step).
+// M/N-contiguous tiles (32 K rows x 256 columns in their natural order):
+// instruction j covers K rows (wave*4 + j)*2 .. +1; slot i is K row
+// (wave*4+j)*2 + i/32, physical chunk i%32, logical chunk (i%32) ^ mn_swizzle(k).
+// Columns past mn_valid read zeros by their offset, rows past k_valid by the
+// resource's size; it starts at the step's first K row, so offsets stay below
+// 32 rows whatever the K extent.
+template <>
+struct Feed<L_MNMAJ> {
+    uint32_t o[4];
+    uint64_t base;
+    int64_t stride;
+    int left;
+    __device__ __forceinline__ void init(const MNOp& op, int lane, int wave) {
+        base = (uint64_t)op.base;
+        stride = op.stride;
+        left = op.k_valid;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = (wave * 4 + j) * 2 + (lane >> 5);
+            const int c = (lane & 31) ^ mn_swizzle(k);
+            o[j] = c * 8 < op.mn_valid ? (uint32_t)(k * op.stride) + (uint32_t)(c * 16) : kOob;
+        }
+    }
+    __device__ __forceinline__ Dma next() {
+        const int rows = left < 0 ? 0 : left > 32 ? 32 : left;
+        const Dma d = {rsrc_at(base, rows * (int)stride), 0};
+        base += (uint64_t)(32 * stride);
+        left -= 32;
+        return d;
+    }
+};
+
+__device__ __forceinline__ void dma16(const Dma& d, uint32_t voff, uint32_t lds) {
+    // (5 wait states from a vector write of the resource's registers)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 ::"s"(lds), "v"(voff), "s"(d.rs), "s"(d.soff) : "memory");
+}
+
+// 8-bit operands (row-pair layout; K extents of whole blocks of 32, so the last
+// step may be half a step).
 struct LaneP2 {
     uint32_t o[4];
     int lc16, kbytes;
@@ -374,39 +431,6 @@ struct LaneP2 {
         return lc16 < kbytes - kt * kRowB ? o[j] + (uint32_t)(2 * kt * kRowB) : kOob;
     }
 };
-// M/N-contiguous tiles (32 K rows x 256 columns in their natural order):
-// instruction j covers K rows (wave*4 + j)*2 .. +1; slot i is K row
-// (wave*4+j)*2 + i/32, physical chunk i%32, logical chunk (i%32) ^ mn_swizzle(k).
-// Rows past k_valid and columns past mn_valid read zeros.  The buffer resource
-// is rebuilt at the step's first K row, so offsets stay below 32 rows whatever
-// the K extent.
-template <>
-struct Lane<L_MNMAJ> {
-    uint32_t o[4];
-    const uint8_t* base;
-    int64_t stride;
-    int k_valid, hi, w2;
-    __device__ __forceinline__ void init(const MNOp& op, int lane, int wave) {
-        base = op.base;
-        stride = op.stride;
-        k_valid = op.k_valid;
-        hi = lane >> 5;
-        w2 = wave * 8;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = w2 + j * 2 + hi;
-            const int c = (lane & 31) ^ mn_swizzle(k);
-            o[j] = c * 8 < op.mn_valid ? (uint32_t)(k * op.stride) + (uint32_t)(c * 16) : kOob;
-        }
-    }
-    __device__ __forceinline__ i32x4 rsrc(int kt) const {
-        return make_rsrc(base + (int64_t)kt * 32 * stride);
-    }
-    __device__ __forceinline__ uint32_t off(int kt, int j) const {
-        return hi < k_valid - kt * 32 - w2 - j * 2 ? o[j] : kOob;
-    }
-};
-
 // MXFP8 scales of one K step.  GEMM operands keep their E8M0 scales
 // block-major ([block][row]), so the scales of one K block for the 256 tile
 // rows are 256 bytes: one dword per lane covers 4 consecutive tile rows.
@@ -588,6 +612,19 @@ struct Acc<DT_BF16> {
     __device__ __forceinline__ void mma(int i, int j, const bf16x8_t& a, const bf16x8_t& b) {
         asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
                      : "+a"(v[i][j]) : "v"(a), "v"(b));
+    }
+    // A product with a DMA to LDS address lds + kOff around it: the address goes
+    // to M0 before the product, which gives it the wait state that the DMA
+    // needs, so that the two cost one issue slot each.
+    template <int kOff>
+    __device__ __forceinline__ void mma_dma(int i, int j, const bf16x8_t& a, const bf16x8_t& b,
+                                            const Dma& d, uint32_t voff, uint32_t lds) {
+        asm volatile("s_add_u32 m0, %3, %4\n\t"
+                     "v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\t"
+                     "buffer_load_dwordx4 %5, %6, %7 offen lds"
+                     : "+a"(v[i][j])
+                     : "v"(a), "v"(b), "s"(lds), "n"(kOff), "v"(voff), "s"(d.rs), "s"(d.soff)
+                     : "memory", "scc");
     }
     // Ordinary instructions and products on either side: 20 wait states, more
     // than any matrix instruction's result needs before it is read.
@@ -1078,6 +1115,19 @@ __device__ __forceinline__ void amax_to_part(uint32_t v, uint32_t* scratch, uint
         part[blockIdx.x] = max(max(scratch[0], scratch[1]), max(scratch[2], scratch[3]));
 }
 
+// f(0) .. f(7), each with its number as a constant
+template <class F>
+__device__ __forceinline__ void unroll8(F&& f) {
+    f(std::integral_constant<int, 0>{});
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
+    f(std::integral_constant<int, 4>{});
+    f(std::integral_constant<int, 5>{});
+    f(std::integral_constant<int, 6>{});
+    f(std::integral_constant<int, 7>{});
+}
+
 // ---------------------------------------------------------------- the kernel
 template <int DT, int LA, int LB, int GRP, int EPI, int USE>
 __global__ __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
@@ -1208,9 +1258,6 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     // stages that are never consumed.
     constexpr int kBatch = 8 + (DT != DT_BF16 ? 1 : 0);
     constexpr int kWait2 = 2 * kBatch;                           // vmcnt(2 batches)
-    // (M/N-contiguous operands build their buffer resource per K step)
-    const i32x4 rs_a = make_rsrc(LA == L_KMAJ ? (const void*)ka.base : nullptr);
-    const i32x4 rs_b = make_rsrc(LB == L_KMAJ ? (const void*)kb.base : nullptr);
     const i32x4 rs_sa = make_rsrc(sbase_a), rs_sb = make_rsrc(sbase_b);
 
     auto stage_ptr = [&](auto S) -> uint8_t* {
@@ -1248,23 +1295,27 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     // kt+4 into its own stage: every wave has finished that stage's reads
     // (lgkmcnt(0)) before the barrier.  Against the barrier after three
     // quarters of the step's MFMAs, with the reads behind it and the DMAs in
-    // front (Mixtral shape, ms): bf16 forward 5.18 -> 5.08, backward 10.05 ->
-    // 9.61; MXFP8 5.38 -> 5.30 backward, and 196 -> 184 us for 5105 rows of
-    // 1024 x 1536 experts.
+    // front (MXFP8): 5.38 -> 5.30 ms for the Mixtral shape's backward, 196 ->
+    // 184 us for 5105 rows of 1024 x 1536 experts.
+    //
+    // bf16: 64 MFMAs of 16 cycles each leave 4 issue slots per MFMA, which the
+    // preparation of 8 DMAs (the offset's sum and bounds, M0, a wait state)
+    // overran.  With offsets that stay, uniform values that move and the DMA's
+    // M0 write around an MFMA (Acc::mma_dma), a step of the weight gradient is
+    // 135 instructions (105 with K-contiguous operands): backward 9.35 -> 9.02
+    // ms for the Mixtral shape, 263 -> 245 us for 5105 rows of 1024 x 1536.
     if constexpr (DT == DT_BF16) {
-        Lane<LA> da;
-        Lane<LB> db;
-        if constexpr (LA == L_KMAJ) da.init(ka, lane, wave); else da.init(ma, lane, wave);
-        if constexpr (LB == L_KMAJ) db.init(kb, lane, wave); else db.init(mb, lane, wave);
-        auto dma = [&](auto S, int kt, int j) {       // instruction j of 8 of batch kt
-            uint8_t* base = stage_ptr(S);
-            const uint32_t l0 = lds_u32(base + wave * 4096) + (j & 3) * 1024;
-            if (j < 4) {
-                if constexpr (LA == L_KMAJ) dma16(rs_a, da.off(kt, j), l0);
-                else dma16(da.rsrc(kt), da.off(kt, j), l0);
-            } else {
-                if constexpr (LB == L_KMAJ) dma16(rs_b, db.off(kt, j - 4), l0 + kTileB);
-                else dma16(db.rsrc(kt), db.off(kt, j - 4), l0 + kTileB);
+        Feed<LA> fa;
+        Feed<LB> fb;
+        if constexpr (LA == L_KMAJ) fa.init(ka, lane, wave); else fa.init(ma, lane, wave);
+        if constexpr (LB == L_KMAJ) fb.init(kb, lane, wave); else fb.init(mb, lane, wave);
+        auto whole = [&](auto S) {                    // the next batch, into stage S
+            const Dma a = fa.next(), b = fb.next();
+            const uint32_t l0 = lds_u32(stage_ptr(S) + wave * 4096);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dma16(a, fa.o[j], l0 + j * 1024);
+                dma16(b, fb.o[j], l0 + kTileB + j * 1024);
             }
         };
         // K-contiguous fragments: lane (row r of 16, 16-byte chunk of the step's
@@ -1286,46 +1337,50 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
             else if (n < 9) read_b(A + kTileB, F, n - 1);
             else read_a(A, F, n - 8);
         };
-        auto bstep = [&](auto S, int kt, Frags& Fc, Frags& Fn) {
+        auto bstep = [&](auto S, Frags& Fc, Frags& Fn) {
             constexpr int st = decltype(S)::value;
             using Next = std::integral_constant<int, (st + 1) % kStages>;
+            const Dma da = fa.next(), db = fb.next();     // batch kt+4
+            const uint32_t l0 = lds_u32(stage_ptr(S) + wave * 4096);
             __builtin_amdgcn_sched_barrier(0);
-            pipe_barrier<kWait2>();                   // batch kt+1 has landed
+            pipe_barrier<kWait2>();                       // batch kt+1 has landed
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {             // block i: 8 MFMAs, one DMA, 2 or 3 reads
-                const int r0 = i < 2 ? 3 * i : 2 * i + 2, nr = i < 2 ? 3 : i < 7 ? 2 : 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    acc.mma(i, j, Fc.a[i], Fc.b[j]);
+            // block i: 8 MFMAs, one of them with a DMA, 2 or 3 reads
+            unroll8([&](auto Bi) {
+                constexpr int i = decltype(Bi)::value;
+                constexpr int r0 = i < 2 ? 3 * i : 2 * i + 2, nr = i < 2 ? 3 : i < 7 ? 2 : 0;
+                unroll8([&](auto Bj) {
+                    constexpr int j = decltype(Bj)::value;
+                    if constexpr (j != 1) acc.mma(i, j, Fc.a[i], Fc.b[j]);
+                    else if constexpr (i < 4)
+                        acc.template mma_dma<i * 1024>(i, j, Fc.a[i], Fc.b[j], da, fa.o[i & 3], l0);
+                    else
+                        acc.template mma_dma<kTileB + (i - 4) * 1024>(i, j, Fc.a[i], Fc.b[j], db,
+                                                                      fb.o[i & 3], l0);
                     __builtin_amdgcn_sched_barrier(0);
-                    if (j == 1) dma(S, kt + 4, i);
-                    if (j >= 3 && (j & 1) && (j - 3) / 2 < nr) read(Next{}, Fn, r0 + (j - 3) / 2);
+                    if constexpr (j >= 3 && (j & 1) && (j - 3) / 2 < nr)
+                        read(Next{}, Fn, r0 + (j - 3) / 2);
                     __builtin_amdgcn_sched_barrier(0);
-                }
-            }
+                });
+            });
         };
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dma(I0{}, 0, j);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dma(I1{}, 1, j);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dma(I2{}, 2, j);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dma(I3{}, 3, j);
+        whole(I0{});
+        whole(I1{});
+        whole(I2{});
+        whole(I3{});
         pipe_barrier<3 * kBatch>();                   // batch 0 has landed
 #pragma unroll
         for (int n = 0; n < 16; ++n) read(I0{}, F0, n);
         int kt = 0;
         for (; kt + kStages <= nk; kt += kStages) {
-            bstep(I0{}, kt, F0, F1);
-            bstep(I1{}, kt + 1, F1, F0);
-            bstep(I2{}, kt + 2, F0, F1);
-            bstep(I3{}, kt + 3, F1, F0);
+            bstep(I0{}, F0, F1);
+            bstep(I1{}, F1, F0);
+            bstep(I2{}, F0, F1);
+            bstep(I3{}, F1, F0);
         }
-        if (kt < nk) bstep(I0{}, kt, F0, F1);
-        if (kt + 1 < nk) bstep(I1{}, kt + 1, F1, F0);
-        if (kt + 2 < nk) bstep(I2{}, kt + 2, F0, F1);
+        if (kt < nk) bstep(I0{}, F0, F1);
+        if (kt + 1 < nk) bstep(I1{}, F1, F0);
+        if (kt + 2 < nk) bstep(I2{}, F0, F1);
         __builtin_amdgcn_sched_barrier(0);
         acc.settle();
     } else {
@@ -1334,6 +1389,7 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
         LaneP2 da, db;
         da.init(ka, lane, wave);
         db.init(kb, lane, wave);
+        const i32x4 rs_a = make_rsrc(ka.base), rs_b = make_rsrc(kb.base);
         auto dma = [&](auto S, int kt, int j) {       // instruction j of 8 of batch kt
             uint8_t* base = stage_ptr(S);
             const uint32_t l0 = lds_u32(base + wave * 4096) + (j & 3) * 1024;
