@@ -65,6 +65,7 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4_t;
 
 constexpr int kStages = 4;                    // LDS pipeline depth (loads run 3 steps ahead)
 constexpr int kRowB = 64;                     // K-contiguous LDS tile row (bytes per K step)
+constexpr int kRow2B = 2 * kRowB;             // the same for bf16 (two K steps, a whole line)
 constexpr int kTileB = kGemmBM * kRowB;       // 16 KiB per operand per stage
 constexpr int kStageB = 2 * kTileB;           // A + B
 constexpr int kLdsB = kStages * kStageB;      // 128 KiB
@@ -76,11 +77,12 @@ constexpr uint32_t kOob = 0x80000000u;        // buffer offset that reads zeros
 __device__ __forceinline__ int lds_off(int row, int chunk) {
     return row * kRowB + ((chunk ^ ((row >> 2) & 3)) << 4);
 }
-// The same tile as the 16-row bf16 fragments read it (16 rows x 4 chunks): an
-// LDS read of 16 bytes per lane takes its lanes in groups that mix two chunks
-// of different rows, which XOR with 2 in every other 8 rows keeps apart.
+// K-contiguous bf16 tile: rows of 128 bytes (two K steps), 8 chunks each.  An
+// LDS read of 16 bytes per lane takes its lanes in groups of 16 that mix two
+// chunks of different rows of the fragment's 16; XOR with (row>>1)&7 puts the
+// 8 even rows of a group, and its 8 odd ones, in 8 different bank groups.
 __device__ __forceinline__ int lds_off16(int row, int chunk) {
-    return row * kRowB + ((chunk ^ (((row >> 3) & 1) << 1)) << 4);
+    return row * kRow2B + ((chunk ^ ((row >> 1) & 7)) << 4);
 }
 // M/N-contiguous tile: K row k (32 per stage), 16-byte chunk c (32 per row).
 // A transposing read takes 32 bytes of rows k..k+3 and of rows 8 below in one
@@ -327,17 +329,10 @@ __device__ __forceinline__ bf16x8_t mn_frag(const uint8_t* lds, int colbase) {
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// An operand's LDS-DMA, K step after K step: 4 instructions of each wave per
-// step.
-//
-// K-contiguous tiles: instruction j covers tile rows (wave*4 + j)*16 .. +15;
-// slot i of it is tile row (wave*4 + j)*16 + i/4 and physical chunk i%4, whose
-// logical chunk is (i%4) ^ 2 ((row>>3)&1) = (i%4) ^ 2 (i>>5) (bf16, lds_off16)
-// or (i%4) ^ ((row>>2)&3) = (i%4) ^ ((i>>4)&3) (8-bit, lds_off).
-//
-// bf16: a lane's offsets do not change with the step, which moves uniform
-// values alone (the scalar offset, the resource): no vector instruction per
-// DMA.  Steps past the K extent read zeros (a resource without records).
+// bf16 operands' LDS-DMA.  A lane's offsets do not change with the K step, which
+// moves uniform values alone (the scalar offset, the resource): no vector
+// instruction per DMA.  Steps past the K extent read zeros (a resource without
+// records).
 struct Dma { i32x4 rs; uint32_t soff; };
 
 __device__ __forceinline__ i32x4 rsrc_at(uint64_t base, int nrec) {
@@ -351,27 +346,39 @@ __device__ __forceinline__ i32x4 rsrc_at(uint64_t base, int nrec) {
 
 template <int L>
 struct Feed;
+// K-contiguous tiles, two K steps at a time: 128 bytes per row are whole lines.
+// (With 64 bytes per row and step the L1 fetched every line twice, the 64 KiB
+// of lines that a step touches being more than it holds: 491 against 246 million
+// line reads for 16384 x 28672 x 4096.)  Instruction j of 8 covers tile rows
+// (wave*8 + j)*8 .. +7; slot i is row (wave*8 + j)*8 + i/8 and physical chunk
+// i%8, whose logical chunk is (i%8) ^ ((row>>1)&7) = (i%8) ^ (i>>4) ^ 4 (j&1).
 template <>
 struct Feed<L_KMAJ> {
-    uint32_t o[4];
+    uint32_t o[8];
     uint64_t base;
-    int k, kbytes;                   // kbytes: a multiple of the step's 64 bytes
-    __device__ __forceinline__ void init(const KOp& op, int lane, int wave) {
-        const int lc16 = ((lane & 3) ^ ((lane >> 5) << 1)) << 4;
+    int k, kbytes, lane;             // kbytes: a multiple of 64
+    __device__ __forceinline__ void init(const KOp& op, int lane_, int wave) {
+        lane = lane_;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int gr = kop_row(op, (wave * 4 + j) * 16 + (lane >> 2));
-            o[j] = (uint32_t)((int64_t)gr * op.stride) + (uint32_t)lc16;
+        for (int j = 0; j < 8; ++j) {
+            const int gr = kop_row(op, (wave * 8 + j) * 8 + (lane >> 3));
+            const int c = (lane & 7) ^ (lane >> 4) ^ ((j & 1) << 2);
+            o[j] = (uint32_t)((int64_t)gr * op.stride) + (uint32_t)(c << 4);
         }
         base = (uint64_t)op.base;
         k = 0;
         kbytes = op.kbytes;
     }
     __device__ __forceinline__ Dma next() {
+        if (kbytes - k == kRowB) {       // one step left: chunks 4..7 are past the row
+            const uint32_t up = (uint32_t)(lane & 4) << 29;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] |= j & 1 ? up ^ kOob : up;
+        }
         const bool live = k < kbytes;
         const Dma d = {rsrc_at(base, live ? 0x7fffffff : 0),
                        (uint32_t)__builtin_amdgcn_readfirstlane(live ? k : 0)};
-        k += kRowB;
+        k += kRow2B;
         return d;
     }
 };
@@ -1304,11 +1311,135 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     // M0 write around an MFMA (Acc::mma_dma), a step of the weight gradient is
     // 135 instructions (105 with K-contiguous operands): backward 9.35 -> 9.02
     // ms for the Mixtral shape, 263 -> 245 us for 5105 rows of 1024 x 1536.
-    if constexpr (DT == DT_BF16) {
-        Feed<LA> fa;
+    if constexpr (DT == DT_BF16 && LA == L_KMAJ) {
+        // Pairs of steps: pair p's A tile of two steps lies in lds0 / lds1 (p
+        // even / odd), a K-contiguous B tile in lds2 / lds3, an M/N-contiguous
+        // one step by step in their halves.  The odd step 2p - 1 reads A of
+        // steps 2p and 2p + 1 and B of step 2p, the even step 2p B of step
+        // 2p + 1: pair p's A tile is free from step 2p on, its B tile from
+        // 2p + 1 on, and each step loads the next pair but one into what is.
+        Feed<L_KMAJ> fa;
         Feed<LB> fb;
-        if constexpr (LA == L_KMAJ) fa.init(ka, lane, wave); else fa.init(ma, lane, wave);
+        fa.init(ka, lane, wave);
         if constexpr (LB == L_KMAJ) fb.init(kb, lane, wave); else fb.init(mb, lane, wave);
+        constexpr bool kPB = LB == L_KMAJ;
+        using Frag8 = bf16x8_t[8];
+        bf16x8_t X[8], Y[8], Z[8], B0[8], B1[8];
+        const int oA = lds_off16(wm * 128 + (lane & 15), lane >> 4);
+        const int oB = lds_off16(wn * 128 + (lane & 15), lane >> 4);
+        auto a_ptr = [&](auto St) -> uint8_t* { return decltype(St)::value & 2 ? lds1 : lds0; };
+        auto b_ptr = [&](auto St) -> uint8_t* {
+            constexpr int st = decltype(St)::value & 3;
+            return (st & 2 ? lds3 : lds2) + (kPB ? 0 : (st & 1) * kTileB);
+        };
+        // fragment f of step St (mod 4); 16 f rows leave the swizzle unchanged
+        auto read_a = [&](auto St, Frag8& F, int f) {
+            F[f] = *(const bf16x8_t*)(a_ptr(St) + (oA ^ ((decltype(St)::value & 1) * 64)) +
+                                      f * 16 * kRow2B);
+        };
+        auto read_b = [&](auto St, Frag8& F, int f) {
+            if constexpr (kPB)
+                F[f] = *(const bf16x8_t*)(b_ptr(St) + (oB ^ ((decltype(St)::value & 1) * 64)) +
+                                          f * 16 * kRow2B);
+            else
+                F[f] = mn_frag(b_ptr(St), wn * 128 + f * 16);
+        };
+        auto load_a = [&](auto St) {
+            const Dma d = fa.next();
+            const uint32_t l0 = lds_u32(a_ptr(St) + wave * 8192);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dma16(d, fa.o[j], l0 + j * 1024);
+        };
+        auto load_b = [&](auto St) {
+            const Dma d = fb.next();
+            const uint32_t l0 = lds_u32(b_ptr(St) + wave * (kPB ? 8192 : 4096));
+#pragma unroll
+            for (int j = 0; j < (kPB ? 8 : 4); ++j) dma16(d, fb.o[j], l0 + j * 1024);
+        };
+        Dma da{}, db{};
+        uint32_t la = 0, lb = 0;
+        // Step St (mod 4) on Ac and Bc: reads the next step's B into Bn and, odd,
+        // the next pair's A into An (even step) and Af (odd step).
+        auto step = [&](auto St, Frag8& Ac, Frag8& Bc, Frag8& Bn, Frag8& An, Frag8& Af) {
+            constexpr int st = decltype(St)::value;
+            constexpr bool odd = st & 1;
+            using N1 = std::integral_constant<int, (st + 1) & 3>;
+            using N2 = std::integral_constant<int, (st + 2) & 3>;
+            if constexpr (!odd) {
+                da = fa.next();
+                la = lds_u32(a_ptr(St) + wave * 8192);
+            }
+            if constexpr (odd || !kPB) {
+                db = fb.next();
+                lb = lds_u32(b_ptr(St) + wave * (kPB ? 8192 : 4096));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // What has landed.  Odd: the next pair's A and the next step's B; the
+            // loads behind them are the last step's 8 and, with B step by step,
+            // the last 4 of the step before.  Even: nothing new, or the next
+            // step's B with the last two steps' loads behind it.
+            pipe_barrier<odd ? (kPB ? 8 : 12) : (kPB ? 63 : 16)>();
+            __builtin_amdgcn_sched_barrier(0);
+            // block i: 8 MFMAs, its DMAs with MFMAs, its reads between them
+            unroll8([&](auto Bi) {
+                constexpr int i = decltype(Bi)::value;
+                unroll8([&](auto Bj) {
+                    constexpr int j = decltype(Bj)::value;
+                    constexpr int jd = kPB ? (i < 4 && (j & 3) == 0 ? 2 * i + j / 4 : -1)
+                                           : (j == 0 ? i : -1);
+                    if constexpr (jd < 0)
+                        acc.mma(i, j, Ac[i], Bc[j]);
+                    else if constexpr (kPB ? !odd : jd < 4)
+                        acc.template mma_dma<(kPB ? jd : jd + 4 * odd) * 1024>(
+                            i, j, Ac[i], Bc[j], da, fa.o[kPB ? jd : jd + 4 * odd], la);
+                    else
+                        acc.template mma_dma<(kPB ? jd : jd - 4) * 1024>(
+                            i, j, Ac[i], Bc[j], db, fb.o[kPB ? jd : jd - 4], lb);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (j & 1) {
+                        constexpr int n = odd ? (j > 1 ? 3 * i + j / 2 - 1 : -1)
+                                              : (i < 4 && (j & 2) ? 2 * i + j / 4 : -1);
+                        if constexpr (!odd) {
+                            if constexpr (n >= 0) read_b(N1{}, Bn, n);
+                        } else if constexpr (n == 0) read_a(N1{}, An, 0);
+                        else if constexpr (n > 0 && n < 9) read_b(N1{}, Bn, n - 1);
+                        else if constexpr (n >= 9 && n < 16) read_a(N1{}, An, n - 8);
+                        else if constexpr (n >= 16) read_a(N2{}, Af, n - 16);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+            });
+        };
+        load_a(I0{});
+        load_b(I0{});
+        if constexpr (!kPB) load_b(I1{});
+        load_a(I2{});
+        load_b(I2{});
+        if constexpr (!kPB) load_b(I3{});
+        pipe_barrier<kPB ? 16 : 20>();                // what step 0 and A of step 1 need
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+            read_a(I0{}, X, f);
+            read_b(I0{}, B0, f);
+            read_a(I1{}, Y, f);
+        }
+        int kt = 0;
+        for (; kt + 4 <= nk; kt += 4) {
+            step(I0{}, X, B0, B1, X, X);
+            step(I1{}, Y, B1, B0, X, Z);
+            step(I2{}, X, B0, B1, X, X);
+            step(I3{}, Z, B1, B0, X, Y);
+        }
+        if (kt < nk) step(I0{}, X, B0, B1, X, X);
+        if (kt + 1 < nk) step(I1{}, Y, B1, B0, X, Z);
+        if (kt + 2 < nk) step(I2{}, X, B0, B1, X, X);
+        __builtin_amdgcn_sched_barrier(0);
+        acc.settle();
+    } else if constexpr (DT == DT_BF16) {
+        // both operands M/N-contiguous (weight gradients), step by step
+        Feed<L_MNMAJ> fa, fb;
+        fa.init(ma, lane, wave);
+        fb.init(mb, lane, wave);
         auto whole = [&](auto S) {                    // the next batch, into stage S
             const Dma a = fa.next(), b = fb.next();
             const uint32_t l0 = lds_u32(stage_ptr(S) + wave * 4096);
@@ -1318,18 +1449,8 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
                 dma16(b, fb.o[j], l0 + kTileB + j * 1024);
             }
         };
-        // K-contiguous fragments: lane (row r of 16, 16-byte chunk of the step's
-        // 64 bytes); 16 f rows leave the chunk swizzle unchanged
-        const int oA = lds_off16(wm * 128 + (lane & 15), lane >> 4);
-        const int oB = lds_off16(wn * 128 + (lane & 15), lane >> 4);
-        auto read_a = [&](const uint8_t* A, Frags& F, int f) {
-            if constexpr (LA == L_KMAJ) F.a[f] = *(const bf16x8_t*)(A + oA + f * 16 * kRowB);
-            else F.a[f] = mn_frag(A, wm * 128 + f * 16);
-        };
-        auto read_b = [&](const uint8_t* B, Frags& F, int f) {
-            if constexpr (LB == L_KMAJ) F.b[f] = *(const bf16x8_t*)(B + oB + f * 16 * kRowB);
-            else F.b[f] = mn_frag(B, wn * 128 + f * 16);
-        };
+        auto read_a = [&](const uint8_t* A, Frags& F, int f) { F.a[f] = mn_frag(A, wm * 128 + f * 16); };
+        auto read_b = [&](const uint8_t* B, Frags& F, int f) { F.b[f] = mn_frag(B, wn * 128 + f * 16); };
         // fragment read n of 16, in the order in which the step uses them
         auto read = [&](auto S, Frags& F, int n) {
             const uint8_t* A = stage_ptr(S);
