@@ -547,6 +547,9 @@ int grouped_mlp_bwd_gather(int precision, int E, int H, int I, int64_t rows, con
  * yp and the other saved tensors are those of grouped_mlp_fwd: bit for bit,
  * except in MOE_BF16 with few rows per expert (rows <= 64 E, or rows <= 256 E
  * and rows * I <= 2^21), where the fp32 sums are taken in another order.
+ * Rows behind the last expert's (buffers longer than the sizes' sum) are not
+ * written: not in yp, a1_codes and a1_scales here, nor in the backward's dxp
+ * and dprob_perm.
  */
 int grouped_mlp_fwd_ckpt(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp,
                          const int32_t* src_token, const int32_t* split_sizes,

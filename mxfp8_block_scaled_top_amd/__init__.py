@@ -416,12 +416,32 @@ def _saved_struct(s: dict) -> _Saved:
     return _Saved(*[_ptr(s.get(n)) for n, _ in _Saved._fields_])
 
 
-def _mlp_args(E: int, rows: int, device, split_sizes, w_down, prob_perm, *outputs) -> None:
-    """One matrix per expert in every table; sizes and probabilities of the rows."""
-    if any(t is not None and len(t) != E for t in (w_down, *outputs)):
-        raise MoEError(f"every weight table must have one matrix per expert ({E})")
+def _width(w_down) -> int:
+    """I, from the down projections."""
+    if not len(w_down) or not isinstance(w_down[0], torch.Tensor) or w_down[0].dim() != 2:
+        raise MoEError("w_down must be a list of matrices, one per expert")
+    return w_down[0].shape[1]
+
+
+def _mlp_args(H: int, I: int, rows: int, device, split_sizes, w_gate_up, w_down, prob_perm, workspace,
+              dw_gate_up=None, dw_down=None) -> int:
+    """One dense matrix per expert in every table; sizes and probabilities of
+    the rows; bytes of workspace.  Returns the number of experts."""
+    E = len(w_gate_up)
+    for ts, name, shape in ((w_gate_up, "w_gate_up", (2 * I, H)), (w_down, "w_down", (H, I)),
+                            (dw_gate_up, "dw_gate_up", (2 * I, H)), (dw_down, "dw_down", (H, I))):
+        if ts is None:
+            continue
+        if len(ts) != E:
+            raise MoEError(f"{name} must have one matrix per expert ({E})")
+        for t in ts:
+            if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is torch.bfloat16
+                    and t.device == device and t.is_contiguous()):
+                _arg(t, name, torch.bfloat16, shape, device)
     _arg(split_sizes, "split_sizes", torch.int32, (E,), device)
     _arg(prob_perm, "prob_perm", torch.float32, (rows,), device)
+    _work_arg(workspace, device)
+    return E
 
 
 def grouped_mlp_fwd_ckpt(xp, split_sizes, w_gate_up, w_down, prob_perm, precision=MOE_MXFP8,
@@ -432,14 +452,13 @@ def grouped_mlp_fwd_ckpt(xp, split_sizes, w_gate_up, w_down, prob_perm, precisio
     _dev(xp, torch.bfloat16, "xp")
     rows, H = xp.shape
     if src_token is not None:
-        _dev(src_token, torch.int32, "src_token")
         rows = src_token.numel()
-    E = len(w_gate_up)
-    I = w_down[0].shape[1]
+        _arg(src_token, "src_token", torch.int32, (rows,), xp.device)
+    I = _width(w_down)
     dev = xp.device
+    E = _mlp_args(H, I, rows, dev, split_sizes, w_gate_up, w_down, prob_perm, workspace)
     if saved is None:
         saved = alloc_saved(rows, H, I, E, precision, dev, checkpoint=True)
-    _mlp_args(E, rows, dev, split_sizes, w_down, prob_perm)
     codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
     if codes is None:
         raise MoEError("saved has no a1_codes: use alloc_saved(..., checkpoint=True)")
@@ -463,12 +482,14 @@ def grouped_mlp_bwd_ckpt(dyp, xp, split_sizes, w_gate_up, w_down, prob_perm, sav
     _dev(dyp, torch.bfloat16, "dyp")
     rows, H = dyp.shape
     if src_token is not None:
-        _dev(src_token, torch.int32, "src_token")
         rows = src_token.numel()
-    E = len(w_gate_up)
-    I = w_down[0].shape[1]
+        _arg(src_token, "src_token", torch.int32, (rows,), dyp.device)
+    elif xp is not None:
+        _arg(xp, "xp", torch.bfloat16, (rows, H), dyp.device)
+    I = _width(w_down)
     dev = dyp.device
-    _mlp_args(E, rows, dev, split_sizes, w_down, prob_perm, dw_gate_up, dw_down)
+    E = _mlp_args(H, I, rows, dev, split_sizes, w_gate_up, w_down, prob_perm, workspace, dw_gate_up,
+                  dw_down)
     codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
     if codes is None:
         raise MoEError("saved has no a1_codes (grouped_mlp_fwd_ckpt)")
@@ -653,6 +674,13 @@ def _arg(t, name: str, dtype, shape, device) -> None:
     raise MoEError(f"{name} must be contiguous")
 
 
+def _work_arg(workspace, device) -> None:
+    """A caller's workspace: bytes on the device."""
+    if workspace is not None:
+        _arg(workspace, "workspace", torch.uint8,
+             workspace.shape if isinstance(workspace, torch.Tensor) else (), device)
+
+
 def _first(t, name: str, dtype) -> tuple:
     """The first tensor argument, a dense matrix: (rows, columns, device)."""
     if (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.is_contiguous()
@@ -738,7 +766,9 @@ def moe_layernorm_bwd(dy, saved: dict, gamma=None, x=None, dres=None, dx_dtype=N
     dx = torch.empty_like(dy, dtype=dx_dtype)
     dgamma = torch.empty(H, dtype=wt, device=dev) if want_dgamma else None
     dbeta = torch.empty(H, dtype=wt, device=dev) if want_dbeta else None
-    if workspace is None and (want_dgamma or want_dbeta):
+    if workspace is not None:
+        _work_arg(workspace, dev)
+    elif want_dgamma or want_dbeta:
         workspace = _workspace(lib().moe_layernorm_workspace_bytes(T, H), dev)
     _call("moe_layernorm_bwd", dev, _TYPES[dx_dtype], _TYPES[wt], T, H, _ptr(dy), _ptr(x),
           _ptr(mean), _ptr(saved["rstd"]), _ptr(codes), _ptr(scales), _ptr(gamma), _ptr(dres),

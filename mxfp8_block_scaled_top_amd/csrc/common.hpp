@@ -238,6 +238,13 @@ __device__ __forceinline__ int clamp_group_size(int n, int64_t rows) {
     return (int)((incl < rows ? incl : rows) - (excl < rows ? excl : rows));
 }
 
+// Rows that the groups hold in all (every lane of a full wave gets it).
+__device__ __forceinline__ int grouped_rows(const int32_t* split, int E, int64_t rows) {
+    const int lane = threadIdx.x & 63;
+    const int n = clamp_group_size(lane < E ? split[lane] : 0, rows);
+    return __builtin_amdgcn_readlane(wave_incl_scan(n), 63);
+}
+
 __device__ __forceinline__ uint64_t lanemask_lt() {
     int lane = threadIdx.x & 63;
     return lane == 0 ? 0ull : (~0ull >> (64 - lane));

@@ -1728,10 +1728,11 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     }
 }
 
-__global__ void dprob_reduce_kernel(const float* __restrict__ part, int64_t rows, int ntiles,
-                                    float* __restrict__ dprob) {
+// (rows behind the last expert's have no partial sums and stay as they are)
+__global__ void dprob_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ split,
+                                    int E, int64_t rows, int ntiles, float* __restrict__ dprob) {
     int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (r >= rows) return;
+    if (r >= grouped_rows(split, E, rows)) return;
     float s = 0.f;
     for (int n = 0; n < ntiles; ++n) s += part[r * ntiles + n];
     dprob[r] = s;
@@ -1808,11 +1809,12 @@ hipError_t launch_gemm(int dtype, int use, const GemmArgs& g, hipStream_t s) {
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_dprob_reduce(const float* part, int64_t rows, int ntiles, float* dprob,
-                               hipStream_t s) {
+hipError_t launch_dprob_reduce(const float* part, const int32_t* split, int E, int64_t rows,
+                               int ntiles, float* dprob, hipStream_t s) {
     if (rows == 0) return hipSuccess;
     TraceScope ts("dprob_reduce", s);
-    dprob_reduce_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(part, rows, ntiles, dprob);
+    dprob_reduce_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(part, split, E, rows, ntiles,
+                                                                     dprob);
     return hipGetLastError();
 }
 

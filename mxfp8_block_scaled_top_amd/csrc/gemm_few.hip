@@ -362,12 +362,14 @@ __global__ __launch_bounds__(256) void few_wgrad_kernel(GemmArgs g, int mt, int 
                 (u32x2*)(C + (int64_t)(4 * q + s) * g.ldc));
 }
 
-// dprob: the row's partial sums, one wave per row.
-__global__ __launch_bounds__(256) void few_dprob_kernel(const float* __restrict__ part, int64_t rows,
-                                                        int ntiles, float* __restrict__ dprob) {
+// dprob: the row's partial sums, one wave per row of an expert.
+__global__ __launch_bounds__(256) void few_dprob_kernel(const float* __restrict__ part,
+                                                        const int32_t* __restrict__ split, int E,
+                                                        int64_t rows, int ntiles,
+                                                        float* __restrict__ dprob) {
     const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    if (r >= rows) return;
+    if (r >= grouped_rows(split, E, rows)) return;
     float s = 0.f;
     for (int n = lane; n < ntiles; n += 64) s += part[r * ntiles + n];
     s = wave_sum(s);
@@ -425,10 +427,10 @@ hipError_t launch_few(int use, const GemmArgs& g, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_few_dprob(const float* part, int64_t rows, int ntiles, float* dprob,
-                            hipStream_t s) {
+hipError_t launch_few_dprob(const float* part, const int32_t* split, int E, int64_t rows,
+                            int ntiles, float* dprob, hipStream_t s) {
     TraceScope ts("dprob_reduce_few", s);
-    few_dprob_kernel<<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(part, rows, ntiles, dprob);
+    few_dprob_kernel<<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(part, split, E, rows, ntiles, dprob);
     return hipGetLastError();
 }
 

@@ -558,10 +558,11 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             g.name = "gemm_bf16_down_dgrad_swiglu_bwd";
             if (few) {
                 MOE_TRY(launch_few(U_DOWN_DGRAD, g, stream));
-                MOE_TRY(launch_few_dprob(w.part, rows, few_tiles(I), dprob_perm, stream));
+                MOE_TRY(launch_few_dprob(w.part, split_sizes, E, rows, few_tiles(I), dprob_perm,
+                                         stream));
             } else {
                 MOE_TRY(launch_gemm(DT_BF16, U_DOWN_DGRAD, g, stream));
-                MOE_TRY(launch_dprob_reduce(w.part, rows, ntn, dprob_perm, stream));
+                MOE_TRY(launch_dprob_reduce(w.part, split_sizes, E, rows, ntn, dprob_perm, stream));
             }
         }
         // down wgrad: dW2 [H, I] = dYp^T A2
@@ -708,7 +709,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             g.name = "gemm_mx_down_dgrad_swiglu_bwd";
         }
         MOE_TRY(launch_gemm(dt8, U_DOWN_DGRAD, g, stream));
-        MOE_TRY(launch_dprob_reduce(w.part, rows, ntn, dprob_perm, stream));
+        MOE_TRY(launch_dprob_reduce(w.part, split_sizes, E, rows, ntn, dprob_perm, stream));
         if (fp8) {   // dA1: its amax, then rowwise (gate_up dgrad) and grouped columnwise
             MatTable ccd{}, csc{};
             src.p[0] = w.da1;

@@ -7,6 +7,8 @@ the tests of those calls show carries over; the codes themselves are held
 against A1 in float64.  In BF16 with few rows per expert other
 kernels run (the fp32 sums in another order): those are held against
 float64 throughout."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -418,3 +420,92 @@ def test_binding_refusals():
                  lambda: moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s, moe.MOE_BF16, None, d["w1"][:1])):
         with pytest.raises(moe.MoEError):
             call()
+
+
+def _table(ts):
+    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+@pytest.mark.parametrize("rows", [300, 1700], ids=["few", "tiles"])
+def test_outputs_behind_the_last_expert_stay(precision, rows):
+    """Through the C entry points, whose outputs the caller owns: rows that no
+    expert has keep what the buffers held."""
+    H, I, sizes = 128, 1408, [rows // 2, 0, rows // 4]
+    used = sum(sizes)
+    say(f"mlp ckpt outputs behind {NAME[precision]} rows={rows}")
+    d = _cuda(_inputs([*sizes, rows - used], H, I, seed=15))
+    split = torch.tensor(sizes, dtype=torch.int32).cuda()
+    w1, w2 = d["w1"][:3], d["w2"][:3]
+    L, s = moe.lib(), moe.alloc_saved(rows, H, I, 3, precision, "cuda", checkpoint=True)
+    ws = [torch.empty(max(256, moe.moe_workspace_bytes(op, rows, H, I, 3, 1, precision)),
+                      dtype=torch.uint8, device="cuda") for op in (moe.MOE_OP_MLP_FWD, moe.MOE_OP_MLP_BWD)]
+    yp, dxp = (torch.full((rows, H), 7.0, dtype=BF, device="cuda") for _ in range(2))
+    dpp = torch.full((rows,), 7.0, device="cuda")
+    dw1, dw2 = [torch.empty_like(w) for w in w1], [torch.empty_like(w) for w in w2]
+    st = moe._saved_struct(s)
+    p = lambda t: t.data_ptr()                                              # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    assert L.grouped_mlp_fwd_ckpt(precision, 3, H, I, rows, p(d["xp"]), None, p(split), _table(w1), _table(w2),
+                                  p(d["pp"]), p(yp), ctypes.byref(st), p(s["a1_codes"]), p(s["a1_scales"]),
+                                  p(ws[0]), ws[0].numel(), stream) == 0
+    assert L.grouped_mlp_bwd_ckpt(precision, 3, H, I, rows, p(d["dyp"]), None, p(d["xp"]), p(split), _table(w1),
+                                  _table(w2), p(d["pp"]), ctypes.byref(st), p(s["a1_codes"]), p(s["a1_scales"]),
+                                  p(dxp), _table(dw1), _table(dw2), p(dpp), p(ws[1]), ws[1].numel(), stream) == 0
+    torch.cuda.synchronize()
+    for t in (yp, dxp, dpp):
+        assert (t[used:] == 7).all() and not (t[:used] == 7).all()
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+@pytest.mark.parametrize("bad", [[200, -7, 150, 300], [600, 5, 0, 9], [-1, -1, 250, 250]],
+                         ids=["past_rows", "first_takes_all", "negatives"])
+@pytest.mark.parametrize("I", [256, 8448], ids=["few", "tiles"])
+def test_split_sizes_are_clamped(precision, bad, I):
+    """Sizes that are negative or sum past the rows: the run of the clamped sizes."""
+    rows, H, good, total = 500, 128, [], 0
+    for n in bad:
+        n = max(n, 0)
+        good.append(min(total + n, rows) - min(total, rows))
+        total += n
+    say(f"mlp ckpt clamped sizes {bad} -> {good} {NAME[precision]} I={I}")
+    d = _cuda(_inputs(good, H, I, seed=16))
+    out = []
+    for sizes in (bad, good):
+        args = (torch.tensor(sizes, dtype=torch.int32).cuda(), d["w1"], d["w2"], d["pp"])
+        yp, s = moe.grouped_mlp_fwd_ckpt(d["xp"], *args, precision)
+        dxp, dw1, dw2, dpp = moe.grouped_mlp_bwd_ckpt(d["dyp"], d["xp"], *args, s, precision)
+        torch.cuda.synchronize()
+        out.append([yp, s["a1_codes"], s["a1_scales"], dxp, dpp, *dw1, *dw2])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_binding_refusals_of_shapes():
+    say("mlp ckpt binding refusals of shapes")
+    d = _cuda(_inputs([3, 5], 128, 256, seed=17))
+    args = (d["split"], d["w1"], d["w2"], d["pp"])
+    _, s = moe.grouped_mlp_fwd_ckpt(d["xp"], *args, moe.MOE_BF16)
+    turned = [d["w2"][0].T.contiguous().T, d["w2"][1]]          # the shape, another order
+    small = torch.empty(4096, device="cuda")
+    f = lambda *a, **k: moe.grouped_mlp_fwd_ckpt(*a, moe.MOE_BF16, **k)     # noqa: E731
+    b = lambda *a, **k: moe.grouped_mlp_bwd_ckpt(*a, s, moe.MOE_BF16, **k)  # noqa: E731
+    for call in (lambda: f(d["xp"], d["split"], d["w1"], turned, d["pp"]),
+                 lambda: f(d["xp"], d["split"], d["w2"], d["w1"], d["pp"]),
+                 lambda: f(d["xp"], d["split"], [w.float() for w in d["w1"]], d["w2"], d["pp"]),
+                 lambda: f(d["xp"], d["split"], d["w1"], [w.cpu() for w in d["w2"]], d["pp"]),
+                 lambda: f(d["xp"], d["split"][:0], [], [], d["pp"]),
+                 lambda: f(d["xp"][:, :64].contiguous(), *args),
+                 lambda: f(d["xp"], *args, workspace=small),
+                 lambda: f(d["xp"], *args, workspace=torch.empty(1 << 20, dtype=torch.uint8)),
+                 lambda: f(d["xp"], *args, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")[::2]),
+                 lambda: b(d["dyp"], d["xp"][:4].contiguous(), *args),
+                 lambda: b(d["dyp"], d["xp"].float(), *args),
+                 lambda: b(d["dyp"], d["xp"], *args, dw_gate_up=[torch.empty_like(w) for w in d["w2"]]),
+                 lambda: b(d["dyp"], d["xp"], *args, dw_down=[w.float() for w in d["w2"]]),
+                 lambda: b(d["dyp"], d["xp"], *args, workspace=small)):
+        with pytest.raises(moe.MoEError):
+            call()
+    n, ns = moe.moe_layernorm_fwd(d["xp"])
+    for w in (small, torch.empty(1 << 20, dtype=torch.uint8)):
+        with pytest.raises(moe.MoEError):
+            moe.moe_layernorm_bwd(n, ns, x=d["xp"], workspace=w)
