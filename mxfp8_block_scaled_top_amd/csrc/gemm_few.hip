@@ -30,8 +30,8 @@
 //     from the accumulators: no LDS, several waves per SIMD whose reads, products and
 //     writes overlap, where a 256 x 256 tile has the CU to itself.
 // Measured, 8 experts of 2048 x 1408 with 4 rows each (138 MB of weights):
-// forward 33 us, backward 59 us (the weights' bytes alone, at a large copy's
-// rate: 27 and 53 us); 256 x 256 tiles 76 and 163 us.
+// forward 33 us, backward 52 us (the weights' bytes alone, at a large copy's
+// rate: 27 and 53 us); 256 x 256 tiles 76 and 160 us.
 #include "common.hpp"
 #include "kernels.hpp"
 #include "mlp.hpp"
@@ -304,34 +304,70 @@ __global__ __launch_bounds__(64 * kWaves) void few_dgrad_kernel(GemmArgs g, int 
 }
 
 // ---------------------------------------------------------------- weight gradients
-// dW_e [M, N] = A_e^T B_e over the expert's rows.
-__global__ __launch_bounds__(256) void few_wgrad_kernel(GemmArgs g, int mt, int nt) {
+// dW_e [128 mt, 128 nt] = A_e^T B_e over the expert's rows.
+struct FewWgrad {
+    const bf16_t* a;
+    const bf16_t* b;
+    int64_t lda, ldb;
+    int mt, nt;
+    MatTable dw;
+};
+// Both weight gradients and the sums of dprob in one launch: none of them fills
+// the chip to its end, and a launch costs about 2 us.  Workgroups: E x the
+// gate_up tiles, E x the down tiles, then those of dprob (a wave has a row).
+struct FewGrads {
+    FewWgrad gate_up, down;
+    const int32_t* split;
+    int E;
+    int64_t rows;
+    const float* part;      // [rows][ntiles]
+    int ntiles;
+    float* dprob;
+};
+
+__global__ __launch_bounds__(256) void few_grads_kernel(FewGrads g) {
     const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int per = mt * nt;                    // 128 x 128 tiles of an expert
-    const int e = blockIdx.x / per, tile = blockIdx.x - e * per;
-    const int m0 = tile / nt * 128 + (wave >> 1) * 64, n0 = tile % nt * 128 + (wave & 1) * 64;
-    // the expert's rows (every wave for itself)
+    // the experts' rows (every wave for itself)
     const int n = clamp_group_size(lane < g.E ? g.split[lane] : 0, g.rows);
     const int incl = wave_incl_scan(n);
+    int b = blockIdx.x;
+    const int n1 = g.E * g.gate_up.mt * g.gate_up.nt, n2 = g.E * g.down.mt * g.down.nt;
+    if (b >= n1 + n2) {
+        const int64_t r = (int64_t)(b - n1 - n2) * 4 + wave;
+        if (r >= __builtin_amdgcn_readlane(incl, 63)) return;    // rows of no expert
+        float s = 0.f;
+        for (int t = lane; t < g.ntiles; t += 64) s += g.part[r * g.ntiles + t];
+        s = wave_sum(s);
+        if (lane == 0) g.dprob[r] = s;
+        return;
+    }
+    const bool up = b < n1;
+    if (!up) b -= n1;
+    const FewWgrad& w = up ? g.gate_up : g.down;
+    const int64_t lda = w.lda, ldb = w.ldb, ldc = (int64_t)w.nt * 128;
+    const int per = w.mt * w.nt;                // 128 x 128 tiles of an expert
+    const int e = b / per, tile = b - e * per;
+    const int m0 = tile / w.nt * 128 + (wave >> 1) * 64, n0 = tile % w.nt * 128 + (wave & 1) * 64;
     const int rows = __builtin_amdgcn_readlane(n, e);
     const int64_t row0 = __builtin_amdgcn_readlane(incl, e) - rows;
-    const bf16_t* A = (const bf16_t*)g.a + row0 * g.lda + m0 + 4 * c;
-    const bf16_t* B = (const bf16_t*)g.b.p[0] + row0 * g.ldb + n0 + 4 * c;
+    const bf16_t* A = w.a + row0 * lda + m0 + 4 * c;
+    const bf16_t* B = w.b + row0 * ldb + n0 + 4 * c;
+    bf16_t* dw = (bf16_t*)w.dw.p[e];
     f32x4 acc[4][4];
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
     for (int r0 = 0; r0 < rows; r0 += 32) {     // lane: 4 columns of rows r0 + 8 kg ..
-        u32x2 a[8], b[8];
+        u32x2 a[8], bv[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int r = r0 + 8 * kg + k;
-            a[k] = b[k] = (u32x2){0u, 0u};
+            a[k] = bv[k] = (u32x2){0u, 0u};
             if (r < rows) {
-                a[k] = *(const u32x2*)(A + (int64_t)r * g.lda);
-                b[k] = *(const u32x2*)(B + (int64_t)r * g.ldb);
+                a[k] = *(const u32x2*)(A + (int64_t)r * lda);
+                bv[k] = *(const u32x2*)(B + (int64_t)r * ldb);
             }
         }
         u32x4 fa[4], fb[4];
@@ -341,7 +377,7 @@ __global__ __launch_bounds__(256) void few_wgrad_kernel(GemmArgs g, int mt, int 
             for (int s = 0; s < 4; ++s) {
                 const uint32_t sel = s & 1 ? 0x07060302u : 0x05040100u;
                 fa[s][k] = __builtin_amdgcn_perm(a[2 * k + 1][s >> 1], a[2 * k][s >> 1], sel);
-                fb[s][k] = __builtin_amdgcn_perm(b[2 * k + 1][s >> 1], b[2 * k][s >> 1], sel);
+                fb[s][k] = __builtin_amdgcn_perm(bv[2 * k + 1][s >> 1], bv[2 * k][s >> 1], sel);
             }
 #pragma unroll
         for (int s = 0; s < 4; ++s)
@@ -352,28 +388,14 @@ __global__ __launch_bounds__(256) void few_wgrad_kernel(GemmArgs g, int mt, int 
                     acc[s][t], 0, 0, 0);
     }
     // acc[s][t][q]: row 4 (4 kg + q) + s, column 4 c + t
-    bf16_t* C = (bf16_t*)g.c_tab.p[e] + (int64_t)(m0 + 16 * kg) * g.ldc + n0 + 4 * c;
+    bf16_t* C = dw + (int64_t)(m0 + 16 * kg) * ldc + n0 + 4 * c;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int s = 0; s < 4; ++s)
             __builtin_nontemporal_store(
                 pack4((f32x4){acc[s][0][q], acc[s][1][q], acc[s][2][q], acc[s][3][q]}),
-                (u32x2*)(C + (int64_t)(4 * q + s) * g.ldc));
-}
-
-// dprob: the row's partial sums, one wave per row of an expert.
-__global__ __launch_bounds__(256) void few_dprob_kernel(const float* __restrict__ part,
-                                                        const int32_t* __restrict__ split, int E,
-                                                        int64_t rows, int ntiles,
-                                                        float* __restrict__ dprob) {
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (r >= grouped_rows(split, E, rows)) return;
-    float s = 0.f;
-    for (int n = lane; n < ntiles; n += 64) s += part[r * ntiles + n];
-    s = wave_sum(s);
-    if (lane == 0) dprob[r] = s;
+                (u32x2*)(C + (int64_t)(4 * q + s) * ldc));
 }
 
 }  // namespace
@@ -381,13 +403,13 @@ __global__ __launch_bounds__(256) void few_dprob_kernel(const float* __restrict_
 // The rule, from times of both forms (forward / backward, us, few against
 // 256 x 256 tiles).  Up to 64 rows per expert the weights' bytes lead:
 //   H, I, E           rows per expert
-//   4096, 14336, 8    64: 683 / 1521 against 892 / 1759;  128: 1257 / 2230 against 940 / 1924
-//   2048, 1408, 64    32: 275 / 550 against 380 / 741;  64: 347 / 706 against 390 / 789
+//   4096, 14336, 8    64: 686 / 1486 against 725 / 1646;  128: 1257 / 2230 against 762 / 1800
+//   2048, 1408, 64    32: 280 / 544 against 344 / 766;  64: 353 / 697 against 336 / 800
 // Further up to 256 while the experts have so few 256-wide tiles that these
 // leave most compute units idle (rows I <= 2^21):
-//   2048, 1408, 8     128: 82 / 123 against 85 / 196;  256: 144 / 204 against 90 / 219
-//   1024, 4096, 2     256: 70 / 107 against 108 / 249
-//   512, 1024, 8      256: 37 / 60 against 50 / 121
+//   2048, 1408, 8     128: 83 / 121 against 80 / 179;  256: 144 / 204 against 84 / 201
+//   1024, 4096, 2     256: 70 / 101 against 102 / 218
+//   512, 1024, 8      256: 38 / 53 against 48 / 113
 // Wider weights than 65536 stay with the tiles (the grids here are bounded for
 // those that are not).
 bool use_few_rows(int64_t rows, int E, int H, int I) {
@@ -399,11 +421,6 @@ int few_tiles(int N) { return N / kFewN; }
 
 hipError_t launch_few(int use, const GemmArgs& g, hipStream_t s) {
     TraceScope ts(g.name ? g.name : "gemm_few", s);
-    if (use == U_DOWN_WGRAD || use == U_GATEUP_WGRAD) {
-        const int mt = g.M / 128, nt = g.N / 128;
-        few_wgrad_kernel<<<(unsigned)(g.E * mt * nt), 256, 0, s>>>(g, mt, nt);
-        return hipGetLastError();
-    }
     const bool fwd = use == U_GATEUP_FWD || use == U_DOWN_FWD;
     const bool swiglu = use == U_GATEUP_FWD || use == U_DOWN_DGRAD;
     const int ntiles = use == U_GATEUP_FWD ? g.I / 32 : few_tiles(g.N);
@@ -427,10 +444,18 @@ hipError_t launch_few(int use, const GemmArgs& g, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_few_dprob(const float* part, const int32_t* split, int E, int64_t rows,
+hipError_t launch_few_grads(const GemmArgs& gate_up, const GemmArgs& down, const float* part,
                             int ntiles, float* dprob, hipStream_t s) {
-    TraceScope ts("dprob_reduce_few", s);
-    few_dprob_kernel<<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(part, split, E, rows, ntiles, dprob);
+    auto wgrad = [](const GemmArgs& w) {
+        return FewWgrad{(const bf16_t*)w.a, (const bf16_t*)w.b.p[0], w.lda, w.ldb,
+                        w.M / 128, w.N / 128, w.c_tab};
+    };
+    const FewGrads g{wgrad(gate_up), wgrad(down), gate_up.split, gate_up.E, gate_up.rows,
+                     part, ntiles, dprob};
+    const int64_t grid = (int64_t)g.E * (g.gate_up.mt * g.gate_up.nt + g.down.mt * g.down.nt) +
+                         (g.rows + 3) / 4;
+    TraceScope ts("gemm_bf16_wgrads_dprob", s);
+    few_grads_kernel<<<(unsigned)grid, 256, 0, s>>>(g);
     return hipGetLastError();
 }
 

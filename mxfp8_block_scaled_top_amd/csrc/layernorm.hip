@@ -22,8 +22,9 @@
 //
 // Measured with bf16 rows, 168 MB a pass: forward with checkpoint 31 us at
 // 16384 x 2048 and 8192 x 4096 (5.4 TB/s; a large copy reaches 5.2); backward
-// from the checkpoint 43 us (3.9 TB/s), of which dx alone 35 us, the rest
-// the partial rows (4 us for the second kernel and its launch).
+// from the checkpoint 40 us (4.3 TB/s), of which the rows' kernel 36 us and
+// the second one 4 us.  One row of 4096: 3.1 us, the launch and two trips to
+// memory.
 #include "common.hpp"
 #include "kernels.hpp"
 #include "trace.hpp"

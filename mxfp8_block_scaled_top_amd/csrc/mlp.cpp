@@ -558,8 +558,6 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             g.name = "gemm_bf16_down_dgrad_swiglu_bwd";
             if (few) {
                 MOE_TRY(launch_few(U_DOWN_DGRAD, g, stream));
-                MOE_TRY(launch_few_dprob(w.part, split_sizes, E, rows, few_tiles(I), dprob_perm,
-                                         stream));
             } else {
                 MOE_TRY(launch_gemm(DT_BF16, U_DOWN_DGRAD, g, stream));
                 MOE_TRY(launch_dprob_reduce(w.part, split_sizes, E, rows, ntn, dprob_perm, stream));
@@ -580,8 +578,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         wg.c_tab = dw2;
         wg.ldc = I;
         wg.name = "gemm_bf16_down_wgrad";
-        MOE_TRY(few ? launch_few(U_DOWN_WGRAD, wg, stream)
-                    : launch_gemm(DT_BF16, U_DOWN_WGRAD, wg, stream));
+        if (!few) MOE_TRY(launch_gemm(DT_BF16, U_DOWN_WGRAD, wg, stream));
         if (rows > 0) {
             // gate_up dgrad: dXp = dA1 W1
             GemmArgs dg{};
@@ -616,7 +613,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         wg1.c_tab = dw1;
         wg1.ldc = H;
         wg1.name = "gemm_bf16_gateup_wgrad";
-        MOE_TRY(few ? launch_few(U_GATEUP_WGRAD, wg1, stream)
+        MOE_TRY(few ? launch_few_grads(wg1, wg, w.part, few_tiles(I), dprob_perm, stream)
                     : launch_gemm(DT_BF16, U_GATEUP_WGRAD, wg1, stream));
         return MOE_OK;
     }

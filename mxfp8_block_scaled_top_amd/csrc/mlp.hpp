@@ -86,13 +86,14 @@ struct GemmArgs {
 hipError_t launch_gemm(int dtype, int use, const GemmArgs& g, hipStream_t s);
 hipError_t launch_dprob_reduce(const float* part, const int32_t* split, int E, int64_t rows,
                                int ntiles, float* dprob, hipStream_t s);
-// bf16 products for few rows per expert (gemm_few.hip): the six uses, with A1
-// as MXFP8 rows; whether the sizes take them, their dprob partial sums per row
-// (dgrad of N = I columns) and the sum of those.
+// bf16 products for few rows per expert (gemm_few.hip), with A1 as MXFP8 rows:
+// whether the sizes take them, their dprob partial sums per row (dgrad of N = I
+// columns), the forward's and the dgrads' products, and in one launch both
+// weight gradients and the sums of dprob.
 bool use_few_rows(int64_t rows, int E, int H, int I);
 int few_tiles(int N);
 hipError_t launch_few(int use, const GemmArgs& g, hipStream_t s);
-hipError_t launch_few_dprob(const float* part, const int32_t* split, int E, int64_t rows,
+hipError_t launch_few_grads(const GemmArgs& gate_up, const GemmArgs& down, const float* part,
                             int ntiles, float* dprob, hipStream_t s);
 int gemm_n_tiles(int epi, int N, int I);
 // Workgroups (tile slots, a multiple of 8) of one grouped GEMM launch.

