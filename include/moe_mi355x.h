@@ -542,6 +542,10 @@ int grouped_mlp_bwd_gather(int precision, int E, int H, int I, int64_t rows, con
  *              fp32 A1 in the layout and by the rule of mxfp8_quantize axis=1,
  *              33/32 bytes a value in place of saved->a1's 2.  (NaN and
  *              infinities in A1 are outside the contract, as there.)
+ *              In the 8-bit precisions that A1 is the scaled matrix
+ *              instruction's: it adds its 64 products to about 2^-16 of their
+ *              root mean square (the running sum is fp32), so about one code
+ *              in a thousand is a step away from that of the exact A1.
  * saved        as in grouped_mlp_fwd; saved->a1 is neither read nor written
  *              and may be NULL.
  * yp and the other saved tensors are those of grouped_mlp_fwd: bit for bit,
