@@ -133,7 +133,8 @@ __device__ __forceinline__ void grouped_order(int t, int mt, int nt, int& m, int
 // [192, 256) and [256, 320) prefixes of the 32- and 64-padded sizes,
 // [320, 384) the weight gradients' expert order.
 template <int GRP>
-__device__ bool decode_tile(const GemmArgs& g, int ntn, int mtm, int t, int* sched, Tile& tl) {
+__device__ bool decode_tile(const GemmArgs& g, int ntn, int mtm, int block, int t, int* sched,
+                            Tile& tl) {
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
         const int n = clamp_group_size(lane < g.E ? g.split[lane] : 0, g.rows);
@@ -163,7 +164,7 @@ __device__ bool decode_tile(const GemmArgs& g, int ntn, int mtm, int t, int* sch
         // Xp: 2I rows against H): XCD x takes the row tiles m = 8m' + x of
         // every expert, so each XCD reads its own eighth of that operand once
         // and only the smaller one is read by all XCDs.
-        const int x = blockIdx.x & 7, i = blockIdx.x >> 3, mt8 = mtm >> 3;
+        const int x = block & 7, i = block >> 3, mt8 = mtm >> 3;
         const int per = mt8 * ntn;
         const int q = i / per;
         if (q >= g.E) return false;
@@ -179,7 +180,7 @@ __device__ bool decode_tile(const GemmArgs& g, int ntn, int mtm, int t, int* sch
         // all read are fetched from HBM once and served to the other XCDs by
         // the last-level cache, and every weight byte comes from HBM once.
         // Inside the XCD's share: bands of row-tiles (grouped_order).
-        const int x = blockIdx.x & 7, i = blockIdx.x >> 3, nt8 = ntn >> 3;
+        const int x = block & 7, i = block >> 3, nt8 = ntn >> 3;
         int mt;
         if (GRP == G_M) {
             e = 0;
@@ -1142,34 +1143,40 @@ __device__ __forceinline__ void unroll8(F&& f) {
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int DT, int LA, int LB, int GRP, int EPI, int USE>
-__global__ __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void gemm_kernel(GemmArgs g, int ntn, int mtm) {
-    // One LDS array per pipeline stage: with the K loop unrolled by the stage
-    // count every access names its stage statically, which lets the compiler
-    // see that the DMA into one stage does not alias the reads of another
-    // (otherwise it waits for all DMA before every LDS read).
-    __shared__ __attribute__((aligned(16))) uint8_t lds0[kStageB];
-    __shared__ __attribute__((aligned(16))) uint8_t lds1[kStageB];
-    __shared__ __attribute__((aligned(16))) uint8_t lds2[kStageB];
-    __shared__ __attribute__((aligned(16))) uint8_t lds3[kStageB];
-    __shared__ __attribute__((aligned(16))) uint8_t ssc[kStages][2][2][kGemmBM];   // MXFP8 scales
-    __shared__ float red[2 * kGemmBM];                  // probability-gradient row partials
+// A workgroup's LDS.  One array per pipeline stage: with the K loop unrolled by
+// the stage count every access names its stage statically, which lets the
+// compiler see that the DMA into one stage does not alias the reads of another
+// (otherwise it waits for all DMA before every LDS read).
+#define MOE_GEMM_LDS                                                                            \
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[kStageB];                              \
+    __shared__ __attribute__((aligned(16))) uint8_t lds1[kStageB];                              \
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[kStageB];                              \
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[kStageB];                              \
+    __shared__ __attribute__((aligned(16))) uint8_t ssc[kStages][2][2][kGemmBM]; /* scales */   \
+    __shared__ float red[2 * kGemmBM];   /* probability-gradient row partials */                \
     __shared__ int sched[384];
 
+// Workgroup `block` of a product's `grid`: its tile.
+template <int DT, int LA, int LB, int GRP, int EPI, int USE>
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, int ntn, int mtm, unsigned block,
+                                          unsigned grid, uint8_t (&lds0)[kStageB],
+                                          uint8_t (&lds1)[kStageB], uint8_t (&lds2)[kStageB],
+                                          uint8_t (&lds3)[kStageB],
+                                          uint8_t (&ssc)[kStages][2][2][kGemmBM],
+                                          float (&red)[2 * kGemmBM], int (&sched)[384]) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);      // uniform
     const int wm = wave >> 1, wn = wave & 1;
 
     // XCD-aware remap: dispatch is round-robin over 8 XCDs; hand XCD x the
     // contiguous logical range [x*G/8, (x+1)*G/8).
-    const int G8 = gridDim.x >> 3;
-    const int t = (blockIdx.x & 7) * G8 + (blockIdx.x >> 3);
+    const int G8 = grid >> 3;
+    const int t = (block & 7) * G8 + (block >> 3);
 
     constexpr bool kAmax = DT == DT_FP8 && (epi_fwd(EPI) || epi_bwd(EPI));
     Tile tl;
-    if (!decode_tile<GRP>(g, ntn, mtm, t, sched, tl)) {
-        if (kAmax && tid == 0) g.amax_part[blockIdx.x] = 0;
+    if (!decode_tile<GRP>(g, ntn, mtm, (int)block, t, sched, tl)) {
+        if (kAmax && tid == 0) g.amax_part[block] = 0;
         return;
     }
 
@@ -1733,6 +1740,31 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
     }
 }
 
+template <int DT, int LA, int LB, int GRP, int EPI, int USE>
+__global__ __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_kernel(GemmArgs g, int ntn, int mtm) {
+    MOE_GEMM_LDS
+    gemm_tile<DT, LA, LB, GRP, EPI, USE>(g, ntn, mtm, blockIdx.x, gridDim.x, lds0, lds1, lds2, lds3,
+                                         ssc, red, sched);
+}
+
+// The gate_up products of the backward in one launch: the dgrad's tiles (all of
+// K = 2I, few of them) come first and the weight gradient's (many, K the
+// expert's rows) fill the compute units that its last round leaves idle.
+template <int DT, int LB, int LW>
+__global__ __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_gateup_grads_kernel(GemmArgs d, GemmArgs w, unsigned n1, int ntn_d, int ntn_w, int mtm_w) {
+    MOE_GEMM_LDS
+    if (blockIdx.x < n1)
+        gemm_tile<DT, L_KMAJ, LB, G_M, EPI_STORE, U_GATEUP_DGRAD>(
+            d, ntn_d, 0, blockIdx.x, n1, lds0, lds1, lds2, lds3, ssc, red, sched);
+    else
+        gemm_tile<DT, LW, LW, G_K, EPI_STORE, U_GATEUP_WGRAD>(w, ntn_w, mtm_w, blockIdx.x - n1,
+                                                              gridDim.x - n1, lds0, lds1, lds2,
+                                                              lds3, ssc, red, sched);
+}
+#undef MOE_GEMM_LDS
+
 // (rows behind the last expert's have no partial sums and stay as they are)
 __global__ void dprob_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ split,
                                     int E, int64_t rows, int ntiles, float* __restrict__ dprob) {
@@ -1812,6 +1844,23 @@ hipError_t launch_gemm(int dtype, int use, const GemmArgs& g, hipStream_t s) {
     MOE_GEMM_CASE(DT_FP8, U_DOWN_DGRAD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_BWD)
 #undef MOE_GEMM_CASE
     return hipErrorInvalidValue;
+}
+
+hipError_t launch_gateup_grads(int dtype, const GemmArgs& dgrad, const GemmArgs& wgrad,
+                               hipStream_t s) {
+    const int64_t n1 = gemm_slots(G_M, EPI_STORE, dgrad.rows, dgrad.E, 0, dgrad.N, 0);
+    const int64_t n2 = gemm_slots(G_K, EPI_STORE, wgrad.rows, wgrad.E, wgrad.M, wgrad.N, 0);
+    const int ntn_d = gemm_n_tiles(EPI_STORE, dgrad.N, 0), ntn_w = gemm_n_tiles(EPI_STORE, wgrad.N, 0);
+    const int mtm_w = (wgrad.M + kGemmBM - 1) / kGemmBM;
+    const unsigned grid = (unsigned)(n1 + n2);
+    TraceScope ts(dtype == DT_BF16 ? "gemm_bf16_gateup_grads" : "gemm_mx_gateup_grads", s);
+    if (dtype == DT_BF16)
+        gemm_gateup_grads_kernel<DT_BF16, L_MNMAJ, L_MNMAJ><<<grid, kGemmThreads, 0, s>>>(
+            dgrad, wgrad, (unsigned)n1, ntn_d, ntn_w, mtm_w);
+    else
+        gemm_gateup_grads_kernel<DT_MX, L_KMAJ, L_KMAJ><<<grid, kGemmThreads, 0, s>>>(
+            dgrad, wgrad, (unsigned)n1, ntn_d, ntn_w, mtm_w);
+    return hipGetLastError();
 }
 
 hipError_t launch_dprob_reduce(const float* part, const int32_t* split, int E, int64_t rows,

@@ -579,9 +579,10 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         wg.ldc = I;
         wg.name = "gemm_bf16_down_wgrad";
         if (!few) MOE_TRY(launch_gemm(DT_BF16, U_DOWN_WGRAD, wg, stream));
+        const bool both = ck.used && rows > 0;  // the gate_up gradients in one launch
+        GemmArgs dg{};
         if (rows > 0) {
             // gate_up dgrad: dXp = dA1 W1
-            GemmArgs dg{};
             dg.split = split_sizes;
             dg.E = E;
             dg.rows = rows;
@@ -595,8 +596,8 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             dg.c = dxp;
             dg.ldc = H;
             dg.name = "gemm_bf16_gateup_dgrad";
-            MOE_TRY(few ? launch_few(U_GATEUP_DGRAD, dg, stream)
-                        : launch_gemm(DT_BF16, U_GATEUP_DGRAD, dg, stream));
+            if (few) MOE_TRY(launch_few(U_GATEUP_DGRAD, dg, stream));
+            else if (!both) MOE_TRY(launch_gemm(DT_BF16, U_GATEUP_DGRAD, dg, stream));
         }
         // gate_up wgrad: dW1 [2I, H] = dA1^T Xp
         GemmArgs wg1{};
@@ -613,8 +614,9 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         wg1.c_tab = dw1;
         wg1.ldc = H;
         wg1.name = "gemm_bf16_gateup_wgrad";
-        MOE_TRY(few ? launch_few_grads(wg1, wg, w.part, few_tiles(I), dprob_perm, stream)
-                    : launch_gemm(DT_BF16, U_GATEUP_WGRAD, wg1, stream));
+        MOE_TRY(few    ? launch_few_grads(wg1, wg, w.part, few_tiles(I), dprob_perm, stream)
+                : both ? launch_gateup_grads(DT_BF16, dg, wg1, stream)
+                       : launch_gemm(DT_BF16, U_GATEUP_WGRAD, wg1, stream));
         return MOE_OK;
     }
 
@@ -737,8 +739,9 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
     wg.ldc = I;
     wg.name = fp8 ? "gemm_fp8_down_wgrad" : "gemm_mx_down_wgrad";
     MOE_TRY(launch_gemm(dt8, U_DOWN_WGRAD, wg, stream));
+    const bool both = ck.used && rows > 0;      // the gate_up gradients in one launch
+    GemmArgs dg{};
     if (rows > 0) {
-        GemmArgs dg{};
         dg.split = split_sizes;
         dg.E = E;
         dg.rows = rows;
@@ -756,7 +759,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         dg.c = dxp;
         dg.ldc = H;
         dg.name = fp8 ? "gemm_fp8_gateup_dgrad" : "gemm_mx_gateup_dgrad";
-        MOE_TRY(launch_gemm(dt8, U_GATEUP_DGRAD, dg, stream));
+        if (!both) MOE_TRY(launch_gemm(dt8, U_GATEUP_DGRAD, dg, stream));
     }
     GemmArgs wg1{};
     wg1.split = split_sizes;
@@ -772,7 +775,8 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
     wg1.c_tab = dw1;
     wg1.ldc = H;
     wg1.name = fp8 ? "gemm_fp8_gateup_wgrad" : "gemm_mx_gateup_wgrad";
-    MOE_TRY(launch_gemm(dt8, U_GATEUP_WGRAD, wg1, stream));
+    MOE_TRY(both ? launch_gateup_grads(DT_MX, dg, wg1, stream)
+                 : launch_gemm(dt8, U_GATEUP_WGRAD, wg1, stream));
     return MOE_OK;
 }
 
