@@ -1748,20 +1748,25 @@ void gemm_kernel(GemmArgs g, int ntn, int mtm) {
                                          ssc, red, sched);
 }
 
-// The gate_up products of the backward in one launch: the dgrad's tiles (all of
-// K = 2I, few of them) come first and the weight gradient's (many, K the
-// expert's rows) fill the compute units that its last round leaves idle.
-template <int DT, int LB, int LW>
+// A dgrad and a weight gradient of the same weight in one launch: the dgrad's
+// tiles (K = H or 2I, few of them) come first and the weight gradient's (many,
+// K the expert's rows) fill the compute units that its last round leaves idle.
+// 4099 uneven rows over 8 experts of 4096 x 14336, gate_up: 328 dgrad tiles of
+// 0.5 ms on 256 compute units, 2.15 ms in two launches and 1.8 in one.  Both
+// pairs, whole backward: 2400 rows of 8 experts of 2048 x 1408 bf16 215 -> 166
+// us, MXFP8 181 -> 145; 16384 rows of 4096 x 14336: no change.
+template <int DTD, int DTW, int LB, int LW, int EPI, int USE>
 __global__ __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void gemm_gateup_grads_kernel(GemmArgs d, GemmArgs w, unsigned n1, int ntn_d, int ntn_w, int mtm_w) {
+void gemm_grads_kernel(GemmArgs d, GemmArgs w, unsigned n1, int ntn_d, int ntn_w, int mtm_w) {
     MOE_GEMM_LDS
     if (blockIdx.x < n1)
-        gemm_tile<DT, L_KMAJ, LB, G_M, EPI_STORE, U_GATEUP_DGRAD>(
-            d, ntn_d, 0, blockIdx.x, n1, lds0, lds1, lds2, lds3, ssc, red, sched);
+        gemm_tile<DTD, L_KMAJ, LB, G_M, EPI, USE>(d, ntn_d, 0, blockIdx.x, n1, lds0, lds1, lds2,
+                                                  lds3, ssc, red, sched);
     else
-        gemm_tile<DT, LW, LW, G_K, EPI_STORE, U_GATEUP_WGRAD>(w, ntn_w, mtm_w, blockIdx.x - n1,
-                                                              gridDim.x - n1, lds0, lds1, lds2,
-                                                              lds3, ssc, red, sched);
+        gemm_tile<DTW, LW, LW, G_K, EPI_STORE,
+                  USE == U_DOWN_DGRAD ? U_DOWN_WGRAD : U_GATEUP_WGRAD>(
+            w, ntn_w, mtm_w, blockIdx.x - n1, gridDim.x - n1, lds0, lds1, lds2, lds3, ssc, red,
+            sched);
 }
 #undef MOE_GEMM_LDS
 
@@ -1819,11 +1824,9 @@ hipError_t launch_gemm(int dtype, int use, const GemmArgs& g, hipStream_t s) {
     if (dtype == DT && use == USE) return run<DT, LA, LB, GRP, EPI, USE>(g, s);
     if (g.a1_codes) {   // A1 as MXFP8 rows
         MOE_GEMM_CASE(DT_BF16, U_GATEUP_FWD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_FWD_CK)
-        MOE_GEMM_CASE(DT_BF16, U_DOWN_DGRAD, L_KMAJ, L_MNMAJ, G_M, EPI_SWIGLU_BWD_CK)
         MOE_GEMM_CASE(DT_MX, U_GATEUP_FWD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_FWD_CK)
-        MOE_GEMM_CASE(DT_MX, U_DOWN_DGRAD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_BWD_CK)
         MOE_GEMM_CASE(DT_FP8, U_GATEUP_FWD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_FWD_CK)
-        MOE_GEMM_CASE(DT_FP8, U_DOWN_DGRAD, L_KMAJ, L_KMAJ, G_M, EPI_SWIGLU_BWD_CK)
+        if (use == U_DOWN_DGRAD) return hipErrorInvalidValue;      // launch_grads
     }
     // bf16: the backward reads W1, W2 and both weight-gradient operands in
     // their natural (M/N-contiguous) layout
@@ -1846,21 +1849,32 @@ hipError_t launch_gemm(int dtype, int use, const GemmArgs& g, hipStream_t s) {
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_gateup_grads(int dtype, const GemmArgs& dgrad, const GemmArgs& wgrad,
-                               hipStream_t s) {
-    const int64_t n1 = gemm_slots(G_M, EPI_STORE, dgrad.rows, dgrad.E, 0, dgrad.N, 0);
-    const int64_t n2 = gemm_slots(G_K, EPI_STORE, wgrad.rows, wgrad.E, wgrad.M, wgrad.N, 0);
-    const int ntn_d = gemm_n_tiles(EPI_STORE, dgrad.N, 0), ntn_w = gemm_n_tiles(EPI_STORE, wgrad.N, 0);
-    const int mtm_w = (wgrad.M + kGemmBM - 1) / kGemmBM;
-    const unsigned grid = (unsigned)(n1 + n2);
-    TraceScope ts(dtype == DT_BF16 ? "gemm_bf16_gateup_grads" : "gemm_mx_gateup_grads", s);
-    if (dtype == DT_BF16)
-        gemm_gateup_grads_kernel<DT_BF16, L_MNMAJ, L_MNMAJ><<<grid, kGemmThreads, 0, s>>>(
-            dgrad, wgrad, (unsigned)n1, ntn_d, ntn_w, mtm_w);
-    else
-        gemm_gateup_grads_kernel<DT_MX, L_KMAJ, L_KMAJ><<<grid, kGemmThreads, 0, s>>>(
-            dgrad, wgrad, (unsigned)n1, ntn_d, ntn_w, mtm_w);
+template <int DTD, int DTW, int LB, int LW, int EPI, int USE>
+static hipError_t run_grads(const GemmArgs& d, const GemmArgs& w, const char* name, hipStream_t s) {
+    const int64_t n1 = gemm_slots(G_M, EPI, d.rows, d.E, 0, d.N, d.I);
+    const int64_t n2 = gemm_slots(G_K, EPI_STORE, w.rows, w.E, w.M, w.N, 0);
+    TraceScope ts(name, s);
+    gemm_grads_kernel<DTD, DTW, LB, LW, EPI, USE><<<(unsigned)(n1 + n2), kGemmThreads, 0, s>>>(
+        d, w, (unsigned)n1, gemm_n_tiles(EPI, d.N, d.I), gemm_n_tiles(EPI_STORE, w.N, 0),
+        (w.M + kGemmBM - 1) / kGemmBM);
     return hipGetLastError();
+}
+
+hipError_t launch_grads(int dtype, int use, const GemmArgs& d, const GemmArgs& w, hipStream_t s) {
+    if (use == U_DOWN_DGRAD && dtype == DT_BF16)
+        return run_grads<DT_BF16, DT_BF16, L_MNMAJ, L_MNMAJ, EPI_SWIGLU_BWD_CK, U_DOWN_DGRAD>(
+            d, w, "gemm_bf16_down_grads", s);
+    if (use == U_DOWN_DGRAD && dtype == DT_MX)
+        return run_grads<DT_MX, DT_MX, L_KMAJ, L_KMAJ, EPI_SWIGLU_BWD_CK, U_DOWN_DGRAD>(
+            d, w, "gemm_mx_down_grads", s);
+    if (use == U_DOWN_DGRAD)
+        return run_grads<DT_FP8, DT_MX, L_KMAJ, L_KMAJ, EPI_SWIGLU_BWD_CK, U_DOWN_DGRAD>(
+            d, w, "gemm_fp8_down_grads", s);
+    if (dtype == DT_BF16)
+        return run_grads<DT_BF16, DT_BF16, L_MNMAJ, L_MNMAJ, EPI_STORE, U_GATEUP_DGRAD>(
+            d, w, "gemm_bf16_gateup_grads", s);
+    return run_grads<DT_MX, DT_MX, L_KMAJ, L_KMAJ, EPI_STORE, U_GATEUP_DGRAD>(
+        d, w, dtype == DT_FP8 ? "gemm_fp8_gateup_grads" : "gemm_mx_gateup_grads", s);
 }
 
 hipError_t launch_dprob_reduce(const float* part, const int32_t* split, int E, int64_t rows,

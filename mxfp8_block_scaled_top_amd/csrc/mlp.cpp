@@ -535,8 +535,26 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
     }
     // weight-gradient GEMMs run for every expert (empty experts get zeros),
     // even when there are no rows at all
+    // The checkpointed calls: each dgrad with the weight gradient of its weight
+    // in one launch.
+    const bool both = ck.used && rows > 0;
     if (precision == MOE_BF16) {
         const bool few = ck.used && use_few_rows(rows, E, H, I);
+        // down wgrad: dW2 [H, I] = dYp^T A2
+        GemmArgs wg{};
+        wg.split = split_sizes;
+        wg.E = E;
+        wg.rows = rows;
+        wg.rows_pad = padded_rows(rows, E);
+        wg.a = dyp;
+        wg.lda = H;
+        wg.b.p[0] = saved->a2;
+        wg.ldb = I;
+        wg.M = H;
+        wg.N = I;
+        wg.c_tab = dw2;
+        wg.ldc = I;
+        wg.name = "gemm_bf16_down_wgrad";
         GemmArgs g{};
         g.split = split_sizes;
         g.E = E;
@@ -559,27 +577,12 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             if (few) {
                 MOE_TRY(launch_few(U_DOWN_DGRAD, g, stream));
             } else {
-                MOE_TRY(launch_gemm(DT_BF16, U_DOWN_DGRAD, g, stream));
+                MOE_TRY(both ? launch_grads(DT_BF16, U_DOWN_DGRAD, g, wg, stream)
+                             : launch_gemm(DT_BF16, U_DOWN_DGRAD, g, stream));
                 MOE_TRY(launch_dprob_reduce(w.part, split_sizes, E, rows, ntn, dprob_perm, stream));
             }
         }
-        // down wgrad: dW2 [H, I] = dYp^T A2
-        GemmArgs wg{};
-        wg.split = split_sizes;
-        wg.E = E;
-        wg.rows = rows;
-        wg.rows_pad = padded_rows(rows, E);
-        wg.a = dyp;
-        wg.lda = H;
-        wg.b.p[0] = saved->a2;
-        wg.ldb = I;
-        wg.M = H;
-        wg.N = I;
-        wg.c_tab = dw2;
-        wg.ldc = I;
-        wg.name = "gemm_bf16_down_wgrad";
-        if (!few) MOE_TRY(launch_gemm(DT_BF16, U_DOWN_WGRAD, wg, stream));
-        const bool both = ck.used && rows > 0;  // the gate_up gradients in one launch
+        if (!few && !both) MOE_TRY(launch_gemm(DT_BF16, U_DOWN_WGRAD, wg, stream));
         GemmArgs dg{};
         if (rows > 0) {
             // gate_up dgrad: dXp = dA1 W1
@@ -615,7 +618,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         wg1.ldc = H;
         wg1.name = "gemm_bf16_gateup_wgrad";
         MOE_TRY(few    ? launch_few_grads(wg1, wg, w.part, few_tiles(I), dprob_perm, stream)
-                : both ? launch_gateup_grads(DT_BF16, dg, wg1, stream)
+                : both ? launch_grads(DT_BF16, U_GATEUP_DGRAD, dg, wg1, stream)
                        : launch_gemm(DT_BF16, U_GATEUP_WGRAD, wg1, stream));
         return MOE_OK;
     }
@@ -623,6 +626,21 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
     // ---- MXFP8 and FP8 (per-tensor scales from each tensor's amax)
     const bool fp8 = precision == MOE_FP8;
     const int dt8 = fp8 ? DT_FP8 : DT_MX;
+    // down wgrad: dW2 [H, I] = dYp^T A2 over grouped columnwise operands
+    GemmArgs wg{};
+    wg.split = split_sizes;
+    wg.E = E;
+    wg.rows = rows;
+    wg.rows_pad = padded_rows(rows, E);
+    wg.a = w.dyc;
+    wg.a_scale = w.dyc_s;
+    wg.b.p[0] = saved->a2_col_codes;
+    wg.b_scale.p[0] = saved->a2_col_scales;
+    wg.M = H;
+    wg.N = I;
+    wg.c_tab = dw2;
+    wg.ldc = I;
+    wg.name = fp8 ? "gemm_fp8_down_wgrad" : "gemm_mx_down_wgrad";
     const int64_t rpad = padded_rows(rows, E);
     MatTable src{}, cd{}, sc{};
     if (rows > 0) {
@@ -707,7 +725,8 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
             g.q_col_s = w.da1c_s;
             g.name = "gemm_mx_down_dgrad_swiglu_bwd";
         }
-        MOE_TRY(launch_gemm(dt8, U_DOWN_DGRAD, g, stream));
+        MOE_TRY(both ? launch_grads(dt8, U_DOWN_DGRAD, g, wg, stream)
+                     : launch_gemm(dt8, U_DOWN_DGRAD, g, stream));
         MOE_TRY(launch_dprob_reduce(w.part, split_sizes, E, rows, ntn, dprob_perm, stream));
         if (fp8) {   // dA1: its amax, then rowwise (gate_up dgrad) and grouped columnwise
             MatTable ccd{}, csc{};
@@ -723,23 +742,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
                                  &ccd, &csc, true, stream, "fp8_quant_da1", ad, rpad));
         }
     }
-    // down wgrad: dW2 [H, I] = dYp^T A2 over grouped columnwise operands
-    GemmArgs wg{};
-    wg.split = split_sizes;
-    wg.E = E;
-    wg.rows = rows;
-    wg.rows_pad = padded_rows(rows, E);
-    wg.a = w.dyc;
-    wg.a_scale = w.dyc_s;
-    wg.b.p[0] = saved->a2_col_codes;
-    wg.b_scale.p[0] = saved->a2_col_scales;
-    wg.M = H;
-    wg.N = I;
-    wg.c_tab = dw2;
-    wg.ldc = I;
-    wg.name = fp8 ? "gemm_fp8_down_wgrad" : "gemm_mx_down_wgrad";
-    MOE_TRY(launch_gemm(dt8, U_DOWN_WGRAD, wg, stream));
-    const bool both = ck.used && rows > 0;      // the gate_up gradients in one launch
+    if (!both) MOE_TRY(launch_gemm(dt8, U_DOWN_WGRAD, wg, stream));
     GemmArgs dg{};
     if (rows > 0) {
         dg.split = split_sizes;
@@ -775,7 +778,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
     wg1.c_tab = dw1;
     wg1.ldc = H;
     wg1.name = fp8 ? "gemm_fp8_gateup_wgrad" : "gemm_mx_gateup_wgrad";
-    MOE_TRY(both ? launch_gateup_grads(DT_MX, dg, wg1, stream)
+    MOE_TRY(both ? launch_grads(dt8, U_GATEUP_DGRAD, dg, wg1, stream)
                  : launch_gemm(dt8, U_GATEUP_WGRAD, wg1, stream));
     return MOE_OK;
 }

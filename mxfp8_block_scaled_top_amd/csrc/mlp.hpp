@@ -84,9 +84,10 @@ struct GemmArgs {
 };
 
 hipError_t launch_gemm(int dtype, int use, const GemmArgs& g, hipStream_t s);
-// U_GATEUP_DGRAD and U_GATEUP_WGRAD in one launch (DT_BF16 or DT_MX; rows > 0)
-hipError_t launch_gateup_grads(int dtype, const GemmArgs& dgrad, const GemmArgs& wgrad,
-                               hipStream_t s);
+// the dgrad `use` (U_DOWN_DGRAD, from an 8-bit A1, or U_GATEUP_DGRAD) and the
+// weight gradient of the same weight in one launch (rows > 0)
+hipError_t launch_grads(int dtype, int use, const GemmArgs& dgrad, const GemmArgs& wgrad,
+                        hipStream_t s);
 hipError_t launch_dprob_reduce(const float* part, const int32_t* split, int E, int64_t rows,
                                int ntiles, float* dprob, hipStream_t s);
 // bf16 products for few rows per expert (gemm_few.hip), with A1 as MXFP8 rows:
