@@ -101,11 +101,13 @@ struct BwdWs {
     size_t bytes;
 };
 
-BwdWs carve_bwd(void* base, int64_t rows, int H, int I, int E, int precision) {
+// (`few`: with the partial sums of the few-row kernels' narrower tiles, where
+// the sizes take them)
+BwdWs carve_bwd(void* base, int64_t rows, int H, int I, int E, int precision, bool few = true) {
     Carve c(base);
     BwdWs w{};
     int ntn = gemm_n_tiles(EPI_SWIGLU_BWD, I, I);
-    if (precision == MOE_BF16 && use_few_rows(rows, E, H, I)) ntn = few_tiles(I);   // narrower tiles
+    if (few && precision == MOE_BF16 && use_few_rows(rows, E, H, I)) ntn = few_tiles(I);
     w.part = (float*)c.take((size_t)rows * ntn * sizeof(float));
     if (precision == MOE_BF16) {
         w.da1 = c.take((size_t)rows * 2 * I * 2);
@@ -522,11 +524,11 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         if (!aligned16(w_gate_up[e]) || !aligned16(w_down[e]) || !aligned16(dw_gate_up[e]) ||
             !aligned16(dw_down[e]))
             return MOE_ERR_ALIGN;
-    if (workspace_bytes < mlp_bwd_workspace_bytes(rows, H, I, E, precision))
+    if (workspace_bytes < carve_bwd(nullptr, rows, H, I, E, precision, ck.used).bytes)
         return MOE_ERR_WORKSPACE;
     if ((st = device_check()) != MOE_OK) return st;
 
-    BwdWs w = carve_bwd(workspace, rows, H, I, E, precision);
+    BwdWs w = carve_bwd(workspace, rows, H, I, E, precision, ck.used);
     const int ntn = gemm_n_tiles(EPI_SWIGLU_BWD, I, I);
     MatTable dw1{}, dw2{};
     for (int e = 0; e < E; ++e) {
