@@ -509,3 +509,47 @@ def test_binding_refusals_of_shapes():
     for w in (small, torch.empty(1 << 20, dtype=torch.uint8)):
         with pytest.raises(moe.MoEError):
             moe.moe_layernorm_bwd(n, ns, x=d["xp"], workspace=w)
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+@pytest.mark.parametrize("sizes", [[700, 0, 901, 300], [3, 0, 17, 1]], ids=["tiles", "few"])
+def test_calls_in_a_graph_and_two_at_once(precision, sizes):
+    """A captured forward and backward, replayed between eager calls; then two
+    callers on two streams, each with its own buffers: the eager results."""
+    H, I = 256, 384
+    say(f"mlp ckpt graph and streams {NAME[precision]} {sizes}")
+    rows, E = sum(sizes), len(sizes)
+    ws = [[torch.empty(max(256, moe.moe_workspace_bytes(op, rows, H, I, E, 1, precision)), dtype=torch.uint8,
+                       device="cuda") for op in (moe.MOE_OP_MLP_FWD, moe.MOE_OP_MLP_BWD)] for _ in range(2)]
+    saved = [moe.alloc_saved(rows, H, I, E, precision, "cuda", checkpoint=True) for _ in range(2)]
+    d = [_cuda(_inputs(sizes, H, I, seed)) for seed in (18, 19)]
+
+    def call(i):
+        a = (d[i]["split"], d[i]["w1"], d[i]["w2"], d[i]["pp"])
+        yp, _ = moe.grouped_mlp_fwd_ckpt(d[i]["xp"], *a, precision, saved[i], ws[i][0])
+        dxp, dw1, dw2, dpp = moe.grouped_mlp_bwd_ckpt(d[i]["dyp"], d[i]["xp"], *a, saved[i], precision, ws[i][1])
+        return [yp, dxp, dpp, *dw1, *dw2]
+
+    ref = [[t.clone() for t in call(i)] for i in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(0)
+    for rep in range(3):
+        call(1)
+        torch.cuda.synchronize()
+        for t in out:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref[0])), rep
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for rep in range(3):
+        for i, s in enumerate(streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got[i] = call(i)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(got[i], ref[i])), i
