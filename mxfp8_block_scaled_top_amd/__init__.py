@@ -16,6 +16,7 @@ moe_workspace_bytes, moe_workspace_region.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -416,6 +417,31 @@ def _saved_struct(s: dict) -> _Saved:
     return _Saved(*[_ptr(s.get(n)) for n, _ in _Saved._fields_])
 
 
+@functools.lru_cache(maxsize=64)
+def _saved_needs(precision: int, rows: int, H: int, I: int, E: int) -> tuple:
+    """(name, bytes) of every saved tensor besides a1 that calls of these sizes touch."""
+    f = lib().moe_saved_bytes
+    need = [(name, int(f(precision, i, rows, H, I, E))) for i, (name, _) in enumerate(_Saved._fields_)]
+    return tuple((name, n) for name, n in need if n and name != "a1")
+
+
+def _saved_members(saved: dict, precision: int, rows: int, H: int, I: int, E: int, device) -> None:
+    """The saved tensors besides A1, which reach the kernels as bare addresses:
+    every one that is there is dense, on the device and as large as calls of
+    these sizes need.  (Which ones have to be there is the library's check.)"""
+    for name, need in _saved_needs(precision, rows, H, I, E):
+        t = saved.get(name)
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+            raise MoEError(f"saved {name} must be a contiguous tensor on {device}")
+        if name == "a2" and t.dtype != torch.bfloat16:
+            raise MoEError(f"saved a2 must be {torch.bfloat16}, got {t.dtype}")
+        if t.numel() * t.element_size() < need:
+            raise MoEError(f"saved {name} has {t.numel() * t.element_size()} bytes, these sizes need "
+                           f"{need} (alloc_saved)")
+
+
 def _width(w_down) -> int:
     """I, from the down projections."""
     if not len(w_down) or not isinstance(w_down[0], torch.Tensor) or w_down[0].dim() != 2:
@@ -462,6 +488,7 @@ def grouped_mlp_fwd_ckpt(xp, split_sizes, w_gate_up, w_down, prob_perm, precisio
     codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
     if codes is None:
         raise MoEError("saved has no a1_codes: use alloc_saved(..., checkpoint=True)")
+    _saved_members(saved, precision, rows, H, I, E, dev)
     if workspace is None:
         workspace = _workspace(moe_workspace_bytes(MOE_OP_MLP_FWD, rows, H, I, E, 1, precision), dev)
     yp = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
@@ -493,6 +520,7 @@ def grouped_mlp_bwd_ckpt(dyp, xp, split_sizes, w_gate_up, w_down, prob_perm, sav
     codes, scales = _saved_pair(saved, "a1", rows, 2 * I, dev)
     if codes is None:
         raise MoEError("saved has no a1_codes (grouped_mlp_fwd_ckpt)")
+    _saved_members(saved, precision, rows, H, I, E, dev)
     if workspace is None:
         workspace = _workspace(moe_workspace_bytes(MOE_OP_MLP_BWD, rows, H, I, E, 1, precision), dev)
     dxp = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
