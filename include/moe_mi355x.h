@@ -584,7 +584,8 @@ int grouped_mlp_bwd_ckpt(int precision, int E, int H, int I, int64_t rows, const
 
 /*
  * Workspace bytes for op (MOE_OP_ROUTE: T, E, k used; MLP ops: rows = T*k,
- * H, I, E, precision used).  Returns 0 for an invalid op.
+ * H, I, E, precision used).  The bytes for a batch serve every smaller one of
+ * the same H, I, E and precision (MLP ops).  Returns 0 for an invalid op.
  */
 size_t moe_workspace_bytes(int op, int64_t T, int H, int I, int E, int k, int precision);
 

@@ -411,11 +411,17 @@ __global__ __launch_bounds__(256) void few_grads_kernel(FewGrads g) {
 //   1024, 4096, 2     256: 70 / 101 against 102 / 218
 //   512, 1024, 8      256: 38 / 53 against 48 / 113
 // Wider weights than 65536 stay with the tiles (the grids here are bounded for
-// those that are not).
-bool use_few_rows(int64_t rows, int E, int H, int I) {
-    if (H > (1 << 16) || I > (1 << 16)) return false;
-    return rows <= 64 * (int64_t)E || (rows <= 256 * (int64_t)E && rows * I <= (1 << 21));
+// those that are not).  Both conditions hold up to some count of rows: the rule
+// is its larger one (-1: none).
+int64_t most_few_rows(int E, int H, int I) {
+    if (H > (1 << 16) || I > (1 << 16)) return -1;
+    const int64_t mean64 = 64 * (int64_t)E, mean256 = 256 * (int64_t)E;
+    const int64_t narrow = I > 0 ? (1 << 21) / I : mean256;
+    const int64_t few_tiled = narrow < mean256 ? narrow : mean256;
+    return mean64 > few_tiled ? mean64 : few_tiled;
 }
+
+bool use_few_rows(int64_t rows, int E, int H, int I) { return rows <= most_few_rows(E, H, I); }
 
 int few_tiles(int N) { return N / kFewN; }
 

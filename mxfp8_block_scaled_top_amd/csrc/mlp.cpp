@@ -265,8 +265,15 @@ size_t mlp_saved_bytes(int precision, int member, int64_t rows, int H, int I, in
 size_t mlp_fwd_workspace_bytes(int64_t rows, int H, int I, int E, int precision) {
     return carve_fwd(nullptr, rows, H, I, E, precision).bytes;
 }
+// Enough for any batch of up to `rows` rows: the few-row kernels have more partial
+// sums per row than the tiles, so a smaller batch that takes them may need more
+// than this one.
 size_t mlp_bwd_workspace_bytes(int64_t rows, int H, int I, int E, int precision) {
-    return carve_bwd(nullptr, rows, H, I, E, precision).bytes;
+    const size_t tiles = carve_bwd(nullptr, rows, H, I, E, precision, false).bytes;
+    const int64_t most = most_few_rows(E, H, I);
+    if (precision != MOE_BF16 || most < 0) return tiles;
+    const size_t few = carve_bwd(nullptr, rows < most ? rows : most, H, I, E, precision).bytes;
+    return few > tiles ? few : tiles;
 }
 }  // namespace moe
 

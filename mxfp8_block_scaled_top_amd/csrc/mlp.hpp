@@ -91,10 +91,11 @@ hipError_t launch_grads(int dtype, int use, const GemmArgs& dgrad, const GemmArg
 hipError_t launch_dprob_reduce(const float* part, const int32_t* split, int E, int64_t rows,
                                int ntiles, float* dprob, hipStream_t s);
 // bf16 products for few rows per expert (gemm_few.hip), with A1 as MXFP8 rows:
-// whether the sizes take them, their dprob partial sums per row (dgrad of N = I
+// whether the sizes take them and up to how many rows, their dprob partial sums per row (dgrad of N = I
 // columns), the forward's and the dgrads' products, and in one launch both
 // weight gradients and the sums of dprob.
 bool use_few_rows(int64_t rows, int E, int H, int I);
+int64_t most_few_rows(int E, int H, int I);
 int few_tiles(int N);
 hipError_t launch_few(int use, const GemmArgs& g, hipStream_t s);
 hipError_t launch_few_grads(const GemmArgs& gate_up, const GemmArgs& down, const float* part,

@@ -1,5 +1,5 @@
 """What the checkpointed grouped MLP asks of the buffers it is given, on the host
-(no GPU needed): the sizes of the saved tensors."""
+(no GPU needed): the sizes of the saved tensors and of the workspaces."""
 import os
 
 import pytest
@@ -56,3 +56,19 @@ def test_every_member_is_checked(precision):
         if name != "a2":          # exactly what is needed passes
             need = dict(moe._saved_needs(precision, ROWS, H, I, E))[name]
             _check(saved | {name: t[:need].clone()}, precision)
+
+
+def _edges(E, I):
+    """Counts of rows around those where the rule for few rows changes."""
+    near = [64 * E, 256 * E, (1 << 21) // I]
+    return sorted({max(0, n + d) for n in near for d in (-40, -1, 0, 1, 4, 44, 300)} | {0, 1, 100000})
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+@pytest.mark.parametrize("e,h,i", [(8, 4096, 14336), (64, 2048, 1408), (8, 2048, 1408), (1, 128, 128),
+                                   (16, 65536, 128), (2, 65664, 128), (3, 128, 65664)])
+def test_workspace_of_a_batch_serves_smaller_ones(precision, e, h, i):
+    for op in (moe.MOE_OP_MLP_FWD, moe.MOE_OP_MLP_BWD):
+        rows = _edges(e, i)
+        need = [moe.moe_workspace_bytes(op, n, h, i, e, 1, precision) for n in rows]
+        assert all(need) and need == sorted(need), (op, [r for r, a, b in zip(rows, need, need[1:]) if a > b])

@@ -1,5 +1,6 @@
-"""GPU: the checkpointed grouped MLP given saved tensors of other sizes: refused
-before any launch, and larger ones accepted with the same results."""
+"""GPU: the checkpointed grouped MLP given saved tensors of other sizes (refused
+before any launch, larger ones accepted with the same results) and a larger
+batch's workspace."""
 import pytest
 import torch
 
@@ -54,3 +55,22 @@ def test_saved_of_other_sizes(precision):
     assert torch.equal(yp, y2) and torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
     for e in range(E):
         assert torch.equal(got[1][e], want[1][e]) and torch.equal(got[2][e], want[2][e])
+
+
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+def test_workspace_of_a_larger_batch(precision):
+    """One workspace for the largest batch, on either side of the few-row rule."""
+    H, I, E, most = 128, 16640, 2, 130          # the rule takes up to 128 rows
+    say(f"mlp ckpt workspace of {most} rows precision={precision}")
+    bytes_ = [moe.moe_workspace_bytes(op, most, H, I, E, 1, precision)
+              for op in (moe.MOE_OP_MLP_FWD, moe.MOE_OP_MLP_BWD)]
+    ws = [torch.empty(max(n, 256), dtype=torch.uint8, device="cuda") for n in bytes_]
+    for sizes in ([66, 64], [64, 64], [100, 0], [1, 0], [0, 0]):
+        xp, dyp, args = _inputs(sizes, H, I, 2)
+        yp, saved = moe.grouped_mlp_fwd_ckpt(xp, *args, precision, workspace=ws[0])
+        got = moe.grouped_mlp_bwd_ckpt(dyp, xp, *args, saved, precision, ws[1])
+        y2, _ = moe.grouped_mlp_fwd_ckpt(xp, *args, precision)
+        want = moe.grouped_mlp_bwd_ckpt(dyp, xp, *args, saved, precision)
+        torch.cuda.synchronize()
+        assert torch.equal(yp, y2) and torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+        assert all(torch.equal(a, b) for k in (1, 2) for a, b in zip(got[k], want[k]))
