@@ -47,7 +47,8 @@
  * given: it is read as given.  MOE_ERR_HIP reports a failed launch; the HIP
  * error itself is left for the caller's next hipGetLastError().
  *
- * Alignment.  Tensor base pointers must be 16-byte aligned (MOE_ERR_ALIGN).
+ * Alignment.  Tensor base pointers must be 16-byte aligned (MOE_ERR_ALIGN), and
+ * so must the workspaces of moe_layernorm_bwd and grouped_mlp_*_ckpt.
  *
  * Threading.  Stateless apart from a cached device-architecture check; calls
  * may be made from several host threads on different streams, provided that

@@ -310,6 +310,13 @@ int check_a1(const moe_saved* s, const A1Ckpt& ck) {
     return ck.codes && ck.scales ? MOE_OK : MOE_ERR_NULL;
 }
 
+// The checkpointed calls: also the workspace and the 8-bit operands kept for the
+// weight gradients, which are read and written in 16-byte pieces.
+bool aligned_ckpt(const moe_saved* s, const void* workspace) {
+    return aligned16(workspace) && aligned16(s->a2_col_codes) && aligned16(s->a2_col_scales) &&
+           aligned16(s->xp_col_codes) && aligned16(s->xp_col_scales);
+}
+
 void set_a1(GemmArgs& g, const moe_saved* s, const A1Ckpt& ck) {
     if (ck.used) {
         g.a1_codes = ck.codes;
@@ -344,6 +351,7 @@ int mlp_fwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* xp
     if (!aligned16(xp) || !aligned16(yp) || (!ck.used && !aligned16(saved->a1)) ||
         !aligned16(saved->a2) || !aligned16(ck.codes) || !aligned16(ck.scales))
         return MOE_ERR_ALIGN;
+    if (ck.used && !aligned_ckpt(saved, workspace)) return MOE_ERR_ALIGN;
     for (int e = 0; e < E; ++e)
         if (!aligned16(w_gate_up[e]) || !aligned16(w_down[e])) return MOE_ERR_ALIGN;
     if (workspace_bytes < mlp_fwd_workspace_bytes(rows, H, I, E, precision))
@@ -527,6 +535,7 @@ int mlp_bwd(int precision, int E, int H, int I, int64_t rows, const uint16_t* dy
         (!ck.used && !aligned16(saved->a1)) || !aligned16(saved->a2) || !aligned16(ck.codes) ||
         !aligned16(ck.scales))
         return MOE_ERR_ALIGN;
+    if (ck.used && !aligned_ckpt(saved, workspace)) return MOE_ERR_ALIGN;
     for (int e = 0; e < E; ++e)
         if (!aligned16(w_gate_up[e]) || !aligned16(w_down[e]) || !aligned16(dw_gate_up[e]) ||
             !aligned16(dw_down[e]))

@@ -1,5 +1,7 @@
 """What the checkpointed grouped MLP asks of the buffers it is given, on the host
-(no GPU needed): the sizes of the saved tensors and of the workspaces."""
+(no GPU needed): the sizes of the saved tensors and of the workspaces,
+and their alignment."""
+import ctypes
 import os
 
 import pytest
@@ -72,3 +74,23 @@ def test_workspace_of_a_batch_serves_smaller_ones(precision, e, h, i):
         rows = _edges(e, i)
         need = [moe.moe_workspace_bytes(op, n, h, i, e, 1, precision) for n in rows]
         assert all(need) and need == sorted(need), (op, [r for r, a, b in zip(rows, need, need[1:]) if a > b])
+
+
+@pytest.mark.parametrize("bwd", [False, True], ids=["fwd", "bwd"])
+@pytest.mark.parametrize("precision", ALL, ids=IDS)
+@pytest.mark.parametrize("what", ["workspace", "a2", "a2_col_codes", "a2_col_scales", "xp_col_codes",
+                                  "xp_col_scales"])
+def test_misaligned_buffers(bwd, precision, what):
+    """4104 is 8 bytes past a 16-byte address; no address here is read."""
+    p = ctypes.c_void_p(4096)
+    ws = ctypes.c_void_p(4104 if what == "workspace" else 4096)
+    saved = moe._Saved(None, *[4104 if n == what else 4096 for n, _ in moe._Saved._fields_[1:6]])
+    tab = (ctypes.c_void_p * 2)(4096, 4096)
+    f, n = moe.lib(), 1 << 40
+    if bwd:
+        st = f.grouped_mlp_bwd_ckpt(precision, 2, 128, 256, 8, p, None, p, p, tab, tab, p, ctypes.byref(saved),
+                                    p, p, p, tab, tab, p, ws, n, None)
+    else:
+        st = f.grouped_mlp_fwd_ckpt(precision, 2, 128, 256, 8, p, None, p, tab, tab, p, p, ctypes.byref(saved),
+                                    p, p, ws, n, None)
+    assert st == 3
