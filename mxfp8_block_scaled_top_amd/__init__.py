@@ -740,7 +740,8 @@ def moe_layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, checkpoint: b
     """Layer norm of the rows of x (bf16 or fp32 [T, H]); gamma and beta bf16
     or fp32 [H], or None.  Returns (y bf16 [T, H], saved): saved holds mean and
     rstd (fp32 [T]) and, with checkpoint, the normalized rows in 8 bits
-    (xhat_codes, xhat_scales); without it the backward needs x."""
+    (xhat_codes, xhat_scales) and an empty tensor of x's type (x_type); without
+    it the backward needs x."""
     T, H, dev = _first(x, "x", _EITHER)
     for t, n in ((gamma, "gamma"), (beta, "beta")):
         if t is not None:
@@ -756,6 +757,7 @@ def moe_layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, checkpoint: b
     if checkpoint:
         codes, scales = _checkpoint(T, H, dev)
         saved["xhat_codes"], saved["xhat_scales"] = codes, scales
+        saved["x_type"] = torch.empty(0, dtype=x.dtype)
     _call("moe_layernorm_fwd", dev, _TYPES[x.dtype], _TYPES[w.dtype] if w is not None else 1, T, H,
           _ptr(x), _ptr(gamma), _ptr(beta), eps, _ptr(y), _ptr(mean), _ptr(rstd), _ptr(codes),
           _ptr(scales))
@@ -767,15 +769,16 @@ def moe_layernorm_bwd(dy, saved: dict, gamma=None, x=None, dres=None, dx_dtype=N
     """Returns (dx [T, H], dgamma [H] or None, dbeta [H] or None).  The
     normalized rows come from saved's checkpoint when it has one, else from x.
     dres: gradient added to dx (its type).  dx_dtype: type of dx, of x and
-    dres when they are given.  dgamma and dbeta have gamma's type (fp32
-    without gamma)."""
+    dres when they are given; by default x's, dres's or that of the forward's x
+    (saved's x_type; bf16 when saved has none).  dgamma and dbeta have gamma's
+    type (fp32 without gamma)."""
     T, H, dev = _first(dy, "dy", torch.bfloat16)
     codes, scales = _saved_pair(saved, "xhat", T, H, dev)
     _arg(saved.get("rstd"), "rstd", torch.float32, (T,), dev)
     if x is not None:
         _arg(x, "x", _EITHER, (T, H), dev)
     if dx_dtype is None:
-        dx_dtype = next((t.dtype for t in (x, dres) if t is not None), torch.bfloat16)
+        dx_dtype = next((t.dtype for t in (x, dres, saved.get("x_type")) if t is not None), torch.bfloat16)
     if dx_dtype not in _TYPES or (x is not None and x.dtype != dx_dtype):
         raise MoEError(f"dx_dtype must be x's, torch.bfloat16 or torch.float32, got {dx_dtype}")
     mean = None
