@@ -701,8 +701,9 @@ int grouped_linear_bwd(int precision, int E, int N, int K, int64_t rows, const u
  *              checkpoint of xh that moe_layernorm_bwd takes in place of x,
  *              uint8 [T, H] and [T, H/32]: MXFP8 in the layout and by the rule
  *              of mxfp8_quantize axis=1, from the fp32 xh.
- * A row with a NaN or an infinity gives NaN in its own y, mean and rstd; its
- * checkpoint is unspecified.
+ * A row with a NaN or an infinity gives NaN in its own y and rstd (its mean is
+ * what the sum gives); its checkpoint is unspecified.  Sums and squares are
+ * fp32: a row whose squared deviations add up past 2^128 has rstd 0 and xh 0.
  */
 int moe_layernorm_fwd(int x_type, int w_type, int64_t T, int H, const void* x, const void* gamma,
                       const void* beta, float eps, uint16_t* y, float* mean, float* rstd,

@@ -38,3 +38,26 @@ def test_constant_rows_of_large_values(H, xt):
     assert ((dx.double().cpu() - r["dx"]).abs() <= e + half * (r["dx"].abs() + e)).all()
     assert not dgamma.any()
     assert ((dbeta.double().cpu() - r["dbeta"]).abs() <= (T + 64) * U * size.sum(0)).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("H", [96, 320, 4096])
+def test_non_finite_stays_in_its_row(bad, H):
+    """With a checkpoint: the other rows keep their y, statistics, codes and
+    gradients; the row itself has NaN (its mean: what its sum gives)."""
+    say(f"layernorm with {bad} and a checkpoint H={H}")
+    T, row, g = 40, 11, torch.Generator().manual_seed(H)
+    x, dy = torch.randn(T, H, generator=g).to(BF).cuda(), torch.randn(T, H, generator=g).to(BF).cuda()
+    y0, s0 = moe.moe_layernorm_fwd(x, checkpoint=True)
+    d0 = moe.moe_layernorm_bwd(dy, s0)[0]
+    x[row, H - 7] = bad
+    y1, s1 = moe.moe_layernorm_fwd(x, checkpoint=True)
+    d1 = moe.moe_layernorm_bwd(dy, s1)[0]
+    d2 = moe.moe_layernorm_bwd(dy, s1 | {"xhat_codes": None, "xhat_scales": None}, x=x)[0]
+    d3 = moe.moe_layernorm_bwd(dy, s0 | {"xhat_codes": None, "xhat_scales": None}, x=x.nan_to_num(0, 0, 0))[0]
+    torch.cuda.synchronize()
+    keep = torch.arange(T, device="cuda") != row
+    for a, b in ((y1, y0), (d1, d0), (d2, d3), *((s1[k], s0[k]) for k in s0 if k != "x_type")):
+        assert torch.equal(a[keep], b[keep])
+    assert y1[row].isnan().all() and s1["rstd"][row].isnan() and d2[row].isnan().all()
+    assert not s1["mean"][row].isfinite()
