@@ -74,3 +74,19 @@ def test_workspace_of_a_larger_batch(precision):
         torch.cuda.synchronize()
         assert torch.equal(yp, y2) and torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
         assert all(torch.equal(a, b) for k in (1, 2) for a, b in zip(got[k], want[k]))
+
+
+@pytest.mark.parametrize("precision", ALL[1:], ids=IDS[1:])
+def test_without_the_weights_copies(precision):
+    """saved without the weights' columnwise copies: the backward makes them itself."""
+    sizes, H, I = [300, 0, 45], 256, 384
+    say(f"mlp ckpt without weight copies precision={precision}")
+    xp, dyp, args = _inputs(sizes, H, I, 3)
+    yp, saved = moe.grouped_mlp_fwd_ckpt(xp, *args, precision)
+    bare = moe.alloc_saved(sum(sizes), H, I, len(sizes), precision, "cuda", weight_cols=False, checkpoint=True)
+    y2, bare = moe.grouped_mlp_fwd_ckpt(xp, *args, precision, bare)
+    want = moe.grouped_mlp_bwd_ckpt(dyp, xp, *args, saved, precision)
+    got = moe.grouped_mlp_bwd_ckpt(dyp, xp, *args, bare, precision)
+    torch.cuda.synchronize()
+    assert torch.equal(yp, y2) and torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+    assert all(torch.equal(a, b) for k in (1, 2) for a, b in zip(got[k], want[k]))

@@ -61,3 +61,34 @@ def test_non_finite_stays_in_its_row(bad, H):
         assert torch.equal(a[keep], b[keep])
     assert y1[row].isnan().all() and s1["rstd"][row].isnan() and d2[row].isnan().all()
     assert not s1["mean"][row].isfinite()
+
+
+@pytest.mark.parametrize("wt", [BF, F32], ids=["w_bf16", "w_f32"])
+def test_one_weight_alone(wt):
+    """gamma without beta and beta without gamma: as with the other one's neutral values."""
+    say(f"layernorm with one weight w={wt}")
+    g = torch.Generator().manual_seed(3)
+    x, dy = torch.randn(70, 160, generator=g).to(BF).cuda(), torch.randn(70, 160, generator=g).to(BF).cuda()
+    w = (1 + 0.2 * torch.randn(160, generator=g)).to(wt).cuda()
+    one, zero = torch.ones_like(w), torch.zeros_like(w)
+    assert torch.equal(moe.moe_layernorm_fwd(x, w)[0], moe.moe_layernorm_fwd(x, w, zero)[0])
+    assert torch.equal(moe.moe_layernorm_fwd(x, None, w)[0], moe.moe_layernorm_fwd(x, one, w)[0])
+    _, s = moe.moe_layernorm_fwd(x)
+    a, b = moe.moe_layernorm_bwd(dy, s, None, x=x), moe.moe_layernorm_bwd(dy, s, torch.ones(160, device="cuda"), x=x)
+    torch.cuda.synchronize()
+    assert a[1].dtype == F32 and all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_squares_past_the_range():
+    """Deviations whose squares leave fp32: rstd and xh are 0, y is beta, in those rows alone."""
+    say("layernorm with squares past fp32")
+    x = torch.randn(6, 256, generator=torch.Generator().manual_seed(4))
+    clean, s0 = moe.moe_layernorm_fwd(x.cuda(), checkpoint=True)
+    x[2] *= 2.0 ** 100
+    beta = torch.full((256,), 0.5, device="cuda")
+    y, s = moe.moe_layernorm_fwd(x.cuda(), checkpoint=True)
+    z, _ = moe.moe_layernorm_fwd(x.cuda(), None, beta)
+    torch.cuda.synchronize()
+    keep = torch.arange(6) != 2
+    assert torch.equal(y.cpu()[keep], clean.cpu()[keep])
+    assert s["rstd"][2] == 0 and not y[2].any() and (z[2] == 0.5).all() and not s["xhat_scales"][2].any()
