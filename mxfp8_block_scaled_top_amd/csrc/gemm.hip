@@ -294,6 +294,9 @@ __device__ __forceinline__ uint32_t lds_u32(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
 }
 
+// (M0 is a register that the compiler reserves: it keeps nothing there over other
+// instructions, writes it right before an instruction of its own that reads it, and
+// takes no clobber of it.  These kernels have no such instruction.)
 __device__ __forceinline__ void dma16(const i32x4& rs, uint32_t voff, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  ::"s"(lds), "v"(voff), "s"(rs) : "memory");
@@ -1358,9 +1361,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int ntn, int mtm, u
         // 2p + 1 on, and each step loads the next pair but one into what is.
         // Against steps of 64 bytes per row (Mixtral shape, 16384 rows, ms):
         // gate_up with SwiGLU 3.32 -> 2.92, down 1.53 -> 1.31 (1.47 PFLOP/s),
-        // dgrads 1.86 -> 1.73 and 2.69 -> 2.58.  What bounds it now is power:
-        // without DMAs and LDS reads the clock rises from 1.7 to 2.2 GHz at
-        // nearly the same cycles.
+        // dgrads 1.86 -> 1.73 and 2.69 -> 2.58, each by itself; inside the whole
+        // layer step, the card warm, gate_up takes 3.0 to 3.1 and down 1.6.  The
+        // card is at its power limit: without DMAs and LDS reads the clock rises
+        // from 1.7 to 2.2 GHz at nearly the same cycles.  That is not a floor: a
+        // library product of the shape gets more products out of the same power.
         Feed<L_KMAJ> fa;
         Feed<LB> fb;
         fa.init(ka, lane, wave);

@@ -31,7 +31,7 @@
 //     writes overlap, where a 256 x 256 tile has the CU to itself.
 // Measured, 8 experts of 2048 x 1408 with 4 rows each (138 MB of weights):
 // forward 33 us, backward 52 us (the weights' bytes alone, at a large copy's
-// rate: 27 and 53 us); 256 x 256 tiles 76 and 160 us.
+// rate: 27 and 53 us); 256 x 256 tiles 73 and 117 us.
 #include "common.hpp"
 #include "kernels.hpp"
 #include "mlp.hpp"
@@ -400,16 +400,28 @@ __global__ __launch_bounds__(256) void few_grads_kernel(FewGrads g) {
 
 }  // namespace
 
-// The rule, from times of both forms (forward / backward, us, few against
-// 256 x 256 tiles).  Up to 64 rows per expert the weights' bytes lead:
+// The rule, from times of both forms with the rows spread evenly (forward /
+// backward, us, few against 256 x 256 tiles).  Up to 64 rows per expert the
+// weights' bytes lead:
 //   H, I, E           rows per expert
-//   4096, 14336, 8    64: 686 / 1486 against 725 / 1646;  128: 1257 / 2230 against 762 / 1800
-//   2048, 1408, 64    32: 280 / 544 against 344 / 766;  64: 353 / 697 against 336 / 800
+//   4096, 14336, 8    16: 513 / 1077 against 720 / 1230;  64: 684 / 1490 against 795 / 1411
+//                     128 (not taken): 1253 / 2337 against 824 / 1557
+//   2048, 1408, 64    16: 280 / 507 against 295 / 697;  64: 349 / 697 against 311 / 785
+//                     128 (not taken): 577 / 1032 against 326 / 853
 // Further up to 256 while the experts have so few 256-wide tiles that these
 // leave most compute units idle (rows I <= 2^21):
-//   2048, 1408, 8     128: 83 / 121 against 80 / 179;  256: 144 / 204 against 84 / 201
-//   1024, 4096, 2     256: 70 / 101 against 102 / 218
-//   512, 1024, 8      256: 38 / 53 against 48 / 113
+//   2048, 1408, 8     64: 51 / 77 against 77 / 128;  128: 84 / 120 against 78 / 136
+//                     186: 110 / 178 against 77 / 140;  256 (not taken): 140 / 202 against 78 / 152
+//   1024, 4096, 2     256: 71 / 100 against 101 / 192
+//   512, 1024, 8      256: 38 / 53 against 49 / 88
+// Near its upper ends it gives back what it wins below.  The host does not know
+// how the rows are spread.  Uneven ones cost this form more, since every 64 (16)
+// rows of an expert read its weights again, from L2; Zipf loads (exponent 1.2),
+// and all rows at one expert:
+//   4096, 14336, 8    64: 868 / 1766 against 746 / 1367;  one: 610 / 1280 against 344 / 1084
+//   2048, 1408, 64    64: 416 / 762 against 350 / 778;  one: 309 / 547 against 91 / 362
+//   2048, 1408, 64    16: 317 / 516 against 293 / 695;  one: 221 / 348 against 80 / 284
+//   2048, 1408, 8     64: 70 / 91 against 77 / 127;  one: 48 / 83 against 75 / 133
 // Wider weights than 65536 stay with the tiles (the grids here are bounded for
 // those that are not).  Both conditions hold up to some count of rows: the rule
 // is its larger one (-1: none).

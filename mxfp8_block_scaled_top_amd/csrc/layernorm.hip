@@ -22,8 +22,8 @@
 //
 // Measured with bf16 rows, 168 MB a pass: forward with checkpoint 31 us at
 // 16384 x 2048 and 8192 x 4096 (5.4 TB/s; a large copy reaches 5.2); backward
-// from the checkpoint 40 us (4.3 TB/s), of which the rows' kernel 36 us and
-// the second one 4 us.  One row of 4096: 3.1 us, the launch and two trips to
+// from the checkpoint 40 to 43 us (4.0 to 4.3 TB/s), of which the rows' kernel
+// 36 us and the second one 4 us.  One row of 4096: 3.1 us, the launch and two trips to
 // memory.
 #include "common.hpp"
 #include "kernels.hpp"
@@ -583,9 +583,10 @@ void with_fwd_shape(int H, F&& f) {
 
 // The backward's: one step per lane, since every column of a row also has two
 // running sums, and many rows side by side, since every workgroup writes a
-// partial row of them.  (16384 x 2048 from codes: 42 us; with 4 steps of one
-// wave on a row 83 us, the registers leaving one wave per SIMD; with half as
-// many rows in a workgroup and twice the workgroups 47 us.)  Rows above 8192
+// partial row of them.  16384 x 2048 on inputs in turn, from codes / bf16 / fp32:
+// 43 / 44 / 70 us; one wave on a row with 4 steps, 4 rows in a workgroup
+// 41 / 44 / 76, with 8 rows 51 / 54 / 165, its fp32 form spilling; these 4 waves
+// with half as many rows and twice the workgroups 42 / 41 / 72.  Rows above 8192
 // would spill their sums: those are added by a kernel of their own, which
 // reads the rows again (2048 x 16384: 60 us; with the sums beside the row 76).
 constexpr int kLnSumsH = 8192;      // wider: the sums in a kernel of their own

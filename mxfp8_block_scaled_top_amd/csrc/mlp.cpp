@@ -13,6 +13,11 @@
 //   down wgrad    dW2 = dYp^T A2       (ragged K = rows of the expert)
 //   gate_up dgrad dXp = dA1 W1
 //   gate_up wgrad dW1 = dA1^T Xp       (ragged K)
+// The checkpointed calls (A1 as MXFP8 rows) run a dgrad and the weight gradient of
+// the same weight in one launch, the down pair before the dprob sums and the
+// gate_up pair behind them.  In BF16 with few rows per expert (use_few_rows) they
+// run the four products that read weights as gemm_few.hip's, then both weight
+// gradients and the dprob sums in one launch.
 // MXFP8 mode first quantizes the GEMM operands that arrive in bf16 (Xp, dYp,
 // both weight sets) along the contraction axis of the GEMM that reads them.
 #include "moe_mi355x.h"
