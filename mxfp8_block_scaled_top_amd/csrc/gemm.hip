@@ -1361,9 +1361,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int ntn, int mtm, u
         // 2p + 1 on, and each step loads the next pair but one into what is.
         // Against steps of 64 bytes per row (Mixtral shape, 16384 rows, ms):
         // gate_up with SwiGLU 3.32 -> 2.92, down 1.53 -> 1.31 (1.47 PFLOP/s),
-        // dgrads 1.86 -> 1.73 and 2.69 -> 2.58, each by itself; inside the whole
-        // layer step, the card warm, gate_up takes 3.0 to 3.1 and down 1.6.  The
-        // card is at its power limit: without DMAs and LDS reads the clock rises
+        // dgrads 1.86 -> 1.73 and 2.69 -> 2.58, both sides in turn; over 30
+        // forwards in a row, and inside the layer step, gate_up takes 2.9 to 3.1
+        // and down 1.5 to 1.6.  The card is at its power limit: without DMAs and LDS reads the clock rises
         // from 1.7 to 2.2 GHz at nearly the same cycles.  That is not a floor: a
         // library product of the shape gets more products out of the same power.
         Feed<L_KMAJ> fa;
