@@ -48,7 +48,8 @@
  * error itself is left for the caller's next hipGetLastError().
  *
  * Alignment.  Tensor base pointers must be 16-byte aligned (MOE_ERR_ALIGN), and
- * so must the workspaces of moe_layernorm_bwd and grouped_mlp_*_ckpt.
+ * so must the workspaces of moe_layernorm_bwd, moe_rmsnorm_bwd, moe_balance_fwd,
+ * grouped_linear_block_bwd and grouped_mlp_*_ckpt.
  *
  * Threading.  Stateless apart from a cached device-architecture check; calls
  * may be made from several host threads on different streams, provided that
@@ -102,7 +103,8 @@ typedef enum moe_op {
     MOE_OP_ROUTER_BWD = 4,    /* T, H, E used (k must still be valid) */
     MOE_OP_LINEAR_FWD = 5,    /* grouped_linear_fwd: T = rows, H = in_features K,
                                  I = out_features N, E, precision (k must be 1) */
-    MOE_OP_LINEAR_BWD = 6     /* grouped_linear_bwd: as MOE_OP_LINEAR_FWD */
+    MOE_OP_LINEAR_BWD = 6,    /* grouped_linear_bwd: as MOE_OP_LINEAR_FWD */
+    MOE_OP_LINEAR_BLOCK_BWD = 7   /* grouped_linear_block_bwd: as MOE_OP_LINEAR_FWD (precision unused) */
 } moe_op;
 
 /* Limits of this version. */
@@ -772,6 +774,205 @@ int moe_swiglu_bwd(int64_t rows, int I, const uint16_t* da2, const uint16_t* a1,
                    const uint8_t* a1_codes, const uint8_t* a1_scales, const float* prob,
                    uint16_t* da1, float* dprob, hipStream_t stream);
 
+/*
+ * moe_rmsnorm_fwd -- root-mean-square norm in front of the router and the
+ * experts, with the residual's addition and the rows in 8 bits.
+ * [AutoModel, "MoE 微调的痛点": the MoE layer takes the place of the block's
+ *  feed-forward; Mixtral's blocks are pre-norm with an RMS norm.]
+ *
+ * Per row t:  h = x + residual, rounded to the stream's type (h = x without
+ *   residual);  rstd = (sum_h h^2 / H + eps)^-1/2;  y = h rstd gamma.
+ * Sums, rstd and y in fp32.  The norm is that of the rounded h, which
+ * moe_rmsnorm_bwd reads.
+ *
+ * x_type       MOE_TYPE_BF16 or MOE_TYPE_F32: x.
+ * stream_type  type of residual and h: x_type or, with a residual, MOE_TYPE_F32
+ *              beside a bf16 x (otherwise MOE_ERR_ARG).
+ * w_type       type of gamma.
+ * T, H         rows (0 <= T <= INT32_MAX) and width: a multiple of 8, 8..32768.
+ * x            [T, H].   residual: [T, H] or NULL.   gamma: [H], or NULL for 1.
+ * eps          >= 0.
+ * h            [T, H] out, needed with a residual (may be residual itself), not
+ *              written without.
+ * y            bf16 [T, H] out, or NULL when codes are given.
+ * rstd         fp32 [T] out, or NULL (inference).
+ * codes, scales   both or neither (MOE_ERR_ARG): y in the 8-bit rows of
+ *              fp8_block_quantize, from the fp32 y: uint8 [T, H] and fp32
+ *              [ceil(H/128), T].
+ * A row with a NaN or an infinity gives NaN in its own outputs (an infinity:
+ * rstd 0, and NaN where it stands).  Squares are fp32: a row whose
+ * squares add up past 2^128 has rstd 0 and y 0.  A row of zeros with eps = 0
+ * gives NaN.
+ */
+int moe_rmsnorm_fwd(int x_type, int stream_type, int w_type, int64_t T, int H, const void* x,
+                    const void* residual, const void* gamma, float eps, void* h, uint16_t* y,
+                    float* rstd, uint8_t* codes, float* scales, hipStream_t stream);
+
+/*
+ * moe_rmsnorm_bwd -- backward of moe_rmsnorm_fwd.
+ * [The same passage.]
+ *
+ *   xh = h rstd;  g = dy gamma;  dx = rstd (g - xh mean_h(g xh)) + dres
+ *   dgamma = sum_t dy xh
+ * dx is the gradient of x and of residual alike.  (8-bit rows pass dy on
+ * unchanged: the rounding counts as the identity.)  Sums in fp32; dgamma is
+ * added up in a fixed order (the same bits every time) and rounded once.
+ *
+ * stream_type  type of h, dres and dx.   w_type: of gamma and dgamma.
+ * dy           bf16 [T, H].   h, rstd: from the forward (h is x there without
+ *              a residual).
+ * dres         [T, H] gradient that reaches h past the norm, added before dx's
+ *              one rounding; or NULL.  May be dx.
+ * dx           [T, H] out.
+ * dx_branch    bf16 [T, H] out: the same sum rounded to bf16, for the branch
+ *              that gave x beside an fp32 stream; or NULL.
+ * dgamma       [H] out, or NULL; zeros when T = 0.
+ * workspace    moe_rmsnorm_workspace_bytes(T, H) bytes when dgamma is given,
+ *              else not used.
+ */
+int moe_rmsnorm_bwd(int stream_type, int w_type, int64_t T, int H, const uint16_t* dy, const void* h,
+                    const float* rstd, const void* gamma, const void* dres, void* dx,
+                    uint16_t* dx_branch, void* dgamma, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
+/* Workspace bytes of moe_rmsnorm_bwd; 0 for sizes it refuses. */
+size_t moe_rmsnorm_workspace_bytes(int64_t T, int H);
+
+/*
+ * moe_balance_fwd -- load-balancing loss and z loss of the router, and the
+ * per-expert counts.
+ * [AutoModel, "MoE 微调的痛点" and "专家并行": each token activates a few
+ *  experts, spread over the devices; the pages do not give the loss that keeps
+ *  their loads even.  It is read as the usual product of load and mean
+ *  probability.]
+ *
+ * p = softmax over all E logits of a token, lse = log sum exp, n = tokens that
+ * count, c_e = their picks of expert e, f_e = c_e / (n k), P_e = sum_t p_te / n:
+ *   balance = balance_coef E sum_e f_e P_e,   z = z_coef sum_t lse_t^2 / n
+ *
+ * logits       fp32 [T, E].   T: tokens, 0 <= T, T*k <= INT32_MAX.   E: 1..64.
+ * topk_expert  int32 [T, k], 1 <= k <= E; an entry outside [0, E) is no pick.
+ * mask         uint8 [T], 0 for a token that does not count (its logits and
+ *              picks are not read); NULL: every token counts.
+ * losses       fp32 [3] out: balance + z, balance, z (0 when no token counts).
+ * counts       int32 [E+1] out: c_e, then n.
+ * mean_prob    fp32 [E] out: P_e, or NULL.
+ * workspace    moe_balance_workspace_bytes(E) bytes.
+ * A token whose logits are all -infinity has p = 0 and lse = 0; NaN or
+ * +infinity makes the losses NaN.  Sums are taken in a fixed order.  Finite
+ * coefficients (else MOE_ERR_ARG).
+ */
+int moe_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t* topk_expert,
+                    const uint8_t* mask, float balance_coef, float z_coef, float* losses,
+                    int32_t* counts, float* mean_prob, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
+/*
+ * moe_balance_bwd -- gradient of losses[0] with respect to the logits.
+ * [The same passages.]
+ *
+ *   dlogits_te = dloss [balance_coef E / n p_te (f_e - sum_j f_j p_tj)
+ *                       + 2 z_coef / n lse_t p_te] + dlogits_in_te
+ * The counts are constants; a token that does not count has dlogits_in alone.
+ * counts       int32 [E+1] from the forward.   mask, k and coefficients: as there.
+ * dloss        fp32 [1] device, the gradient of the loss; NULL: 1.
+ * dlogits_in   fp32 [T, E], such as moe_route_bwd's dlogits, or NULL; may be
+ *              dlogits.
+ * dlogits      fp32 [T, E] out.
+ */
+int moe_balance_bwd(const float* logits, int64_t T, int E, int k, const uint8_t* mask,
+                    float balance_coef, float z_coef, const int32_t* counts, const float* dloss,
+                    const float* dlogits_in, float* dlogits, hipStream_t stream);
+
+/* Workspace bytes of moe_balance_fwd; 0 for an E it refuses. */
+size_t moe_balance_workspace_bytes(int E);
+
+/*
+ * fp8_block_quantize -- bf16 rows to 8 bits with one fp32 scale per 128
+ * consecutive values.
+ * [BioNeMo, "MXFP8与融合MLP": 8-bit operands whose scales go with blocks of
+ *  values; here the coarser blocks of 128 with fp32 scales.]
+ *
+ *   s = max(amax, 448 2^-126) / 448,   code = E4M3 nearest (ties to even) to v / s
+ * Both quotients are fp32, correctly rounded.  A block that holds a NaN or an
+ * infinity has s = NaN or infinity and decodes to NaN throughout.
+ *
+ * rows, cols   0 <= rows <= INT32_MAX; cols a multiple of 8, from 8 (a last
+ *              block of fewer than 128 values has a scale of its own).
+ * codes        uint8 [rows, cols] out.
+ * scales       fp32 [ceil(cols/128), rows] out: the order in which
+ *              grouped_linear_block_* reads them.
+ */
+int fp8_block_quantize(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes, float* scales,
+                       hipStream_t stream);
+
+/*
+ * fp8_block_quantize_weights -- the same for weights, one scale per 128 x 128
+ * values (fewer at the edges).
+ * nmat         matrices, 1..64.   N, K: multiples of 8, from 8; N <= 2^22.
+ * w            HOST array of nmat device pointers, each bf16 [N, K].
+ * codes        HOST array, each uint8 [N, K] out.
+ * scales       HOST array, each fp32 [ceil(N/128), ceil(K/128)] out.
+ * codes_t      HOST array, each uint8 [K, N] out: the codes transposed, which
+ *              grouped_linear_block_bwd reads; or NULL.
+ */
+int fp8_block_quantize_weights(int nmat, int64_t N, int64_t K, const uint16_t* const* w,
+                               uint8_t* const* codes, float* const* scales, uint8_t* const* codes_t,
+                               hipStream_t stream);
+
+/*
+ * grouped_linear_block_fwd -- grouped_linear_fwd on operands that are already
+ * in 8 bits with blocks of 128: y_e = x^_e w^_e^T, where x^ and w^ are the
+ * values that codes and scales stand for.
+ * [BioNeMo, "GroupedLinear" and "MXFP8与融合MLP".]
+ *
+ * Each block's products are summed by the matrix instruction in fp32 and
+ * multiplied by the two scales when they are added to the fp32 accumulator; y
+ * is rounded once.  Nothing is quantized here, so weights are prepared once
+ * (fp8_block_quantize_weights) and rows come from fp8_block_quantize or
+ * moe_rmsnorm_fwd.
+ *
+ * E            experts, 1..64.   N: out_features, K: in_features, multiples of
+ *              32, N * K * 2 below 2^31 (otherwise MOE_ERR_SHAPE).
+ * rows         total rows (sum of split_sizes), 0 <= rows <= INT32_MAX.
+ * x_codes, x_scales, x_rows   uint8 [x_rows, K] and fp32 [ceil(K/128), x_rows].
+ * src_token    int32 [rows]: grouped row r is row src_token[r] of x (a row of
+ *              zeros where that is outside [0, x_rows)), x_rows * K below
+ *              2^32 - 1; or NULL: row r itself, x_rows = rows (else
+ *              MOE_ERR_SHAPE).
+ * split_sizes  int32 [E] device.   Rows behind the last expert's stay as they
+ *              are in y.
+ * w_codes      HOST array of E device pointers, each uint8 [N, K].
+ * w_scales     HOST array, each fp32 [ceil(N/128), ceil(K/128)].
+ * y            bf16 [rows, N] out.
+ */
+int grouped_linear_block_fwd(int E, int N, int K, int64_t rows, const uint8_t* x_codes,
+                             const float* x_scales, int64_t x_rows, const int32_t* src_token,
+                             const int32_t* split_sizes, const uint8_t* const* w_codes,
+                             const float* const* w_scales, uint16_t* y, hipStream_t stream);
+
+/*
+ * grouped_linear_block_bwd -- backward of grouped_linear_block_fwd:
+ *   dx_e = dy^_e w^_e,  dy^ = dy in the rows of fp8_block_quantize (along N)
+ *   dW_e = dy_e^T x^_e  (bf16 operands: dy itself, and x^ rounded to bf16;
+ *                        exact zeros for an expert with no rows)
+ * fp32 accumulation, rounded to bf16.  dx has one row per grouped row, also
+ * with src_token (moe_unpermute adds the rows of a token).
+ *
+ * dy           bf16 [rows, N].
+ * x_codes, x_scales, x_rows, src_token   as in the forward (for dW).
+ * w_codes_t    HOST array, each uint8 [K, N]: the transposed codes.
+ * w_scales     HOST array, each fp32 [ceil(N/128), ceil(K/128)].
+ * dx           bf16 [rows, K] out, or NULL (not computed; w_* may be NULL then).
+ * dw           HOST array of E device pointers, each bf16 [N, K] out, or NULL.
+ * workspace    moe_workspace_bytes(MOE_OP_LINEAR_BLOCK_BWD, rows, K, N, E, 1, 0).
+ */
+int grouped_linear_block_bwd(int E, int N, int K, int64_t rows, const uint16_t* dy,
+                             const uint8_t* x_codes, const float* x_scales, int64_t x_rows,
+                             const int32_t* src_token, const int32_t* split_sizes,
+                             const uint8_t* const* w_codes_t, const float* const* w_scales,
+                             uint16_t* dx, uint16_t* const* dw, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Launch trace (measurement aid).  moe_trace_enable(capacity) creates, once,

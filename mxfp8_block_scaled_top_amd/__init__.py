@@ -11,6 +11,8 @@ moe_route, moe_route_bwd, moe_router_fwd, moe_router_bwd, moe_permute,
 moe_unpermute, mxfp8_quantize, mxfp8_quantize_both, mxfp8_dequantize, grouped_mlp_fwd,
 grouped_mlp_bwd, grouped_mlp_fwd_ckpt, grouped_mlp_bwd_ckpt, grouped_linear_fwd,
 grouped_linear_bwd, moe_layernorm_fwd, moe_layernorm_bwd, moe_swiglu_fwd, moe_swiglu_bwd,
+moe_rmsnorm_fwd, moe_rmsnorm_bwd, moe_balance_fwd, moe_balance_bwd, fp8_block_quantize,
+fp8_block_quantize_weights, grouped_linear_block_fwd, grouped_linear_block_bwd,
 moe_workspace_bytes, moe_workspace_region.
 """
 from __future__ import annotations
@@ -27,7 +29,7 @@ LIB_PATH = os.environ.get("MOE_MI355X_LIB") or os.path.join(_PKG, "_lib", "libmo
 MOE_BF16, MOE_MXFP8, MOE_FP8 = 0, 1, 2
 MOE_ROUTE_RENORM, MOE_ROUTE_SOFTMAX_ALL = 0, 1
 MOE_OP_ROUTE, MOE_OP_MLP_FWD, MOE_OP_MLP_BWD, MOE_OP_ROUTER_FWD, MOE_OP_ROUTER_BWD = 0, 1, 2, 3, 4
-MOE_OP_LINEAR_FWD, MOE_OP_LINEAR_BWD = 5, 6
+MOE_OP_LINEAR_FWD, MOE_OP_LINEAR_BWD, MOE_OP_LINEAR_BLOCK_BWD = 5, 6, 7
 # moe_workspace_region regions (include/moe_mi355x.h)
 WS_REGIONS = {
     "xp_codes": 0, "xp_scales": 1, "w1_codes": 2, "w1_scales": 3, "w2_codes": 4, "w2_scales": 5,
@@ -99,6 +101,18 @@ def lib() -> ctypes.CDLL:
             "moe_layernorm_bwd": (I32, [I32, I32, I64, I32, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
             "moe_swiglu_fwd": (I32, [I64, I32, P, P, P, P, P, P]),
             "moe_swiglu_bwd": (I32, [I64, I32, P, P, P, P, P, P, P, P]),
+            "moe_rmsnorm_workspace_bytes": (SZ, [I64, I32]),
+            "moe_rmsnorm_fwd": (I32, [I32, I32, I32, I64, I32, P, P, P, ctypes.c_float, P, P, P, P, P, P]),
+            "moe_rmsnorm_bwd": (I32, [I32, I32, I64, I32, P, P, P, P, P, P, P, P, P, SZ, P]),
+            "moe_balance_workspace_bytes": (SZ, [I32]),
+            "moe_balance_fwd": (I32, [P, I64, I32, I32, P, P, ctypes.c_float, ctypes.c_float, P, P, P, P,
+                                      SZ, P]),
+            "moe_balance_bwd": (I32, [P, I64, I32, I32, P, ctypes.c_float, ctypes.c_float, P, P, P, P, P]),
+            "fp8_block_quantize": (I32, [P, I64, I64, P, P, P]),
+            "fp8_block_quantize_weights": (I32, [I32, I64, I64, P, P, P, P, P]),
+            "grouped_linear_block_fwd": (I32, [I32, I32, I32, I64, P, P, I64, P, P, P, P, P, P]),
+            "grouped_linear_block_bwd": (I32, [I32, I32, I32, I64, P, P, P, I64, P, P, P, P, P, P, P, SZ,
+                                               P]),
             "moe_trace_enable": (I32, [I32]),
             "moe_trace_filter": (None, [ctypes.c_char_p]),
             "moe_trace_disable": (None, []),
@@ -843,6 +857,258 @@ def moe_swiglu_bwd(da2, saved: dict, prob=None):
     _call("moe_swiglu_bwd", dev, rows, I, _ptr(da2), _ptr(a1), _ptr(codes), _ptr(scales),
           _ptr(prob), _ptr(da1), _ptr(dprob))
     return da1, dprob
+
+
+def moe_rmsnorm_fwd(x, gamma=None, eps: float = 1e-6, residual=None, bf16: bool = True,
+                    fp8: bool = False):
+    """RMS norm of the rows of h = x + residual (x bf16 or fp32 [T, H];
+    residual of x's type, or fp32 beside a bf16 x; None: h = x).  gamma bf16 or
+    fp32 [H], or None.  Returns (y bf16 [T, H], or None without bf16, saved):
+    saved holds h (the new residual stream) and rstd (fp32 [T]) for the backward
+    and, with fp8, the normed rows in 8 bits, codes (uint8 [T, H]) and scales
+    (fp32 [ceil(H/128), T]), as grouped_linear_block_fwd takes them."""
+    T, H, dev = _first(x, "x", _EITHER)
+    if not bf16 and not fp8:
+        raise MoEError("one of bf16 and fp8 has to be wanted")
+    if residual is not None:
+        _arg(residual, "residual", _EITHER if x.dtype == torch.bfloat16 else torch.float32, (T, H), dev)
+    if gamma is not None:
+        _arg(gamma, "gamma", _EITHER, (H,), dev)
+    h = x if residual is None else torch.empty_like(residual)
+    y = torch.empty_like(x, dtype=torch.bfloat16) if bf16 else None
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    saved = {"h": h, "rstd": rstd}
+    codes = scales = None
+    if fp8:
+        codes, scales = _block_rows(T, H, dev)
+        saved["codes"], saved["scales"] = codes, scales
+    _call("moe_rmsnorm_fwd", dev, _TYPES[x.dtype], _TYPES[h.dtype],
+          _TYPES[gamma.dtype] if gamma is not None else 1, T, H, _ptr(x), _ptr(residual), _ptr(gamma), eps,
+          _ptr(h), _ptr(y), _ptr(rstd), _ptr(codes), _ptr(scales))
+    return y, saved
+
+
+def moe_rmsnorm_bwd(dy, saved: dict, gamma=None, dres=None, branch: bool = False,
+                    want_dgamma: bool = True, workspace=None):
+    """Returns (dx [T, H] of saved h's type, dgamma [H] or None, the same dx in
+    bf16 with branch, else None).  dres: gradient added to dx (its type).
+    dgamma has gamma's type (fp32 without gamma)."""
+    T, H, dev = _first(dy, "dy", torch.bfloat16)
+    h, rstd = saved.get("h"), saved.get("rstd")
+    _arg(h, "h", _EITHER, (T, H), dev)
+    _arg(rstd, "rstd", torch.float32, (T,), dev)
+    if dres is not None:
+        _arg(dres, "dres", h.dtype, (T, H), dev)
+    if gamma is not None:
+        _arg(gamma, "gamma", _EITHER, (H,), dev)
+    wt = gamma.dtype if gamma is not None else torch.float32
+    dx = torch.empty_like(h)
+    dxb = torch.empty_like(dy) if branch else None
+    dgamma = torch.empty(H, dtype=wt, device=dev) if want_dgamma else None
+    if workspace is not None:
+        _work_arg(workspace, dev)
+    elif want_dgamma:
+        workspace = _workspace(lib().moe_rmsnorm_workspace_bytes(T, H), dev)
+    _call("moe_rmsnorm_bwd", dev, _TYPES[h.dtype], _TYPES[wt], T, H, _ptr(dy), _ptr(h), _ptr(rstd),
+          _ptr(gamma), _ptr(dres), _ptr(dx), _ptr(dxb), _ptr(dgamma), _ptr(workspace),
+          0 if workspace is None else workspace.numel())
+    return dx, dgamma, dxb
+
+
+def _mask_arg(mask, T: int, device) -> None:
+    if mask is not None:
+        _arg(mask, "mask", (torch.bool, torch.uint8), (T,), device)
+
+
+def moe_balance_fwd(logits, topk_expert, mask=None, balance_coef: float = 0.01, z_coef: float = 0.0):
+    """Balance loss and z loss of the router.  logits fp32 [T, E], topk_expert
+    int32 [T, k], mask bool or uint8 [T] (0: the token does not count) or None.
+    Returns (loss fp32 scalar, saved): saved holds counts (int32 [E]), tokens
+    (int32 [1]), mean_prob (fp32 [E]), the losses balance and z one by one, and
+    what the backward takes."""
+    T, E, dev = _first(logits, "logits", torch.float32)
+    if not isinstance(topk_expert, torch.Tensor) or topk_expert.dim() != 2:
+        raise MoEError("topk_expert must be a matrix")
+    k = topk_expert.shape[1]
+    _arg(topk_expert, "topk_expert", torch.int32, (T, k), dev)
+    _mask_arg(mask, T, dev)
+    losses = torch.empty(3, dtype=torch.float32, device=dev)
+    counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    mean_prob = torch.empty(E, dtype=torch.float32, device=dev)
+    ws = _workspace(lib().moe_balance_workspace_bytes(E), dev)
+    _call("moe_balance_fwd", dev, _ptr(logits), T, E, k, _ptr(topk_expert), _ptr(mask), balance_coef,
+          z_coef, _ptr(losses), _ptr(counts), _ptr(mean_prob), _ptr(ws), ws.numel())
+    return losses[0], {"counts": counts[:E], "tokens": counts[E:], "mean_prob": mean_prob,
+                       "balance": losses[1], "z": losses[2], "all_counts": counts, "k": k,
+                       "coefs": (balance_coef, z_coef)}
+
+
+def moe_balance_bwd(logits, saved: dict, mask=None, dloss=None, dlogits=None, out=None):
+    """Gradient of moe_balance_fwd's loss with respect to the logits, fp32
+    [T, E].  mask: the forward's.  dloss: fp32 tensor of one value (None: 1).
+    dlogits: a gradient of the logits that is added, such as moe_route_bwd's.
+    out: where the result goes (may be dlogits itself)."""
+    T, E, dev = _first(logits, "logits", torch.float32)
+    counts = saved.get("all_counts")
+    _arg(counts, "saved all_counts", torch.int32, (E + 1,), dev)
+    _mask_arg(mask, T, dev)
+    if dloss is not None:
+        if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
+            raise MoEError("dloss must be a tensor of one value")
+        _arg(dloss, "dloss", torch.float32, dloss.shape, dev)
+    if dlogits is not None:
+        _arg(dlogits, "dlogits", torch.float32, (T, E), dev)
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _arg(out, "out", torch.float32, (T, E), dev)
+    _call("moe_balance_bwd", dev, _ptr(logits), T, E, saved["k"], _ptr(mask), *saved["coefs"], _ptr(counts),
+          _ptr(dloss), _ptr(dlogits), _ptr(out))
+    return out
+
+
+def _block_rows(rows: int, cols: int, device):
+    """(codes [rows, cols], scales [ceil(cols/128), rows]) of 8-bit rows in blocks of 128."""
+    return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+            torch.empty(((cols + 127) // 128, rows), dtype=torch.float32, device=device))
+
+
+def fp8_block_quantize(x):
+    """bf16 rows [R, C] to 8 bits with one fp32 scale per 128 values: (codes
+    uint8 [R, C], scales fp32 [ceil(C/128), R])."""
+    R, C, dev = _first(x, "x", torch.bfloat16)
+    codes, scales = _block_rows(R, C, dev)
+    _call("fp8_block_quantize", dev, _ptr(x), R, C, _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def _table(t, name: str, dtype, shape, device):
+    """One dense matrix per expert, a list of them or a tensor [E, ...], as a
+    host table of device addresses; shape None: that of the first.  Returns
+    (table, E, shape)."""
+    if isinstance(t, torch.Tensor):
+        if t.dim() != 3 or not t.shape[0]:
+            raise MoEError(f"{name} must be a tensor [E, rows, columns] or a list of matrices")
+        if shape is None:
+            shape = tuple(t.shape[1:])
+        _arg(t, name, dtype, (t.shape[0], *shape), device)
+        E, step, base = t.shape[0], t[0].numel() * t.element_size(), t.data_ptr()
+        return (ctypes.c_void_p * E)(*range(base, base + E * step, step) if step else [base] * E), E, shape
+    if not isinstance(t, (list, tuple)) or not len(t) or not isinstance(t[0], torch.Tensor):
+        raise MoEError(f"{name} must be a tensor [E, rows, columns] or a list of matrices")
+    if shape is None:
+        shape = tuple(t[0].shape)
+    if len(shape) != 2:
+        raise MoEError(f"{name} must hold matrices")
+    for m in t:
+        _arg(m, name, dtype, shape, device)
+    return _ptr_array(t), len(t), shape
+
+
+def fp8_block_quantize_weights(w, transposed: bool = False) -> dict:
+    """Weights of E experts (bf16 [E, N, K], or a list of [N, K]) to 8 bits with
+    one fp32 scale per 128 x 128 values: codes (uint8 [E, N, K]), scales (fp32
+    [E, ceil(N/128), ceil(K/128)]) and, with transposed, codes_t (uint8
+    [E, K, N]), which the data gradient needs."""
+    first = w if isinstance(w, torch.Tensor) else (w[0] if len(w) else None)
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise MoEError("w must be device tensors")
+    dev = first.device
+    tab, E, (N, K) = _table(w, "w", torch.bfloat16, None, dev)
+    q = {"codes": torch.empty((E, N, K), dtype=torch.uint8, device=dev),
+         "scales": torch.empty((E, (N + 127) // 128, (K + 127) // 128), dtype=torch.float32, device=dev),
+         "codes_t": torch.empty((E, K, N), dtype=torch.uint8, device=dev) if transposed else None}
+    tabs = [_table(q[n], n, q[n].dtype, tuple(q[n].shape[1:]), dev)[0] if q[n] is not None else None
+            for n in ("codes", "scales", "codes_t")]
+    _call("fp8_block_quantize_weights", dev, E, N, K, ctypes.addressof(tab),
+          *[0 if t is None else ctypes.addressof(t) for t in tabs])
+    return q
+
+
+def _block_x(x, name: str, device=None):
+    """8-bit rows: (codes, scales, rows, K, device) of a dict."""
+    codes, scales = x.get("codes"), x.get("scales")
+    rows, K, dev = _first(codes, name + " codes", torch.uint8)
+    if device is not None and dev != device:
+        raise MoEError(f"{name} codes are on {dev}, not on {device}")
+    _arg(scales, name + " scales", torch.float32, ((K + 127) // 128, rows), dev)
+    return codes, scales, rows, K, dev
+
+
+def _block_w(w, key: str, shape, device):
+    """Host tables of the experts' codes (saved under `key`; shape None: any)
+    and scales."""
+    if not isinstance(w, dict) or w.get(key) is None:
+        raise MoEError(f"w must hold {key} (fp8_block_quantize_weights)")
+    codes, E, got = _table(w[key], key, torch.uint8, shape, device)
+    N, K = got if key == "codes" else got[::-1]
+    scales, Es, _ = _table(w.get("scales"), "scales", torch.float32, ((N + 127) // 128, (K + 127) // 128),
+                           device)
+    if Es != E:
+        raise MoEError(f"{E} experts' codes but {Es} experts' scales")
+    return codes, scales, E, N, K
+
+
+def grouped_linear_block_fwd(x, split_sizes, w: dict, src_token=None):
+    """y_e = x_e w_e^T in 8 bits with blocks of 128.  x: a dict with codes and
+    scales of 8-bit rows (moe_rmsnorm_fwd's saved, say), or bf16 [rows, K], which
+    is quantized first; w: the dict of fp8_block_quantize_weights.  With
+    src_token (int32 [rows]) grouped row r is row src_token[r] of x.  Returns
+    (y bf16 [rows, N], saved): saved is the 8-bit x for the backward."""
+    if isinstance(x, torch.Tensor):
+        codes, scales = fp8_block_quantize(x)
+        x = {"codes": codes, "scales": scales}
+    elif not isinstance(x, dict):
+        raise MoEError("x must be a matrix or a dict of codes and scales")
+    codes, scales, x_rows, K, dev = _block_x(x, "x")
+    rows = x_rows
+    if src_token is not None:
+        rows = src_token.numel() if isinstance(src_token, torch.Tensor) else 0
+        _arg(src_token, "src_token", torch.int32, (rows,), dev)
+    wc, ws, E, N, Kw = _block_w(w, "codes", None, dev)
+    if Kw != K:
+        raise MoEError(f"x has {K} columns, the weights {Kw}")
+    _arg(split_sizes, "split_sizes", torch.int32, (E,), dev)
+    y = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
+    _call("grouped_linear_block_fwd", dev, E, N, K, rows, _ptr(codes), _ptr(scales), x_rows,
+          _ptr(src_token), _ptr(split_sizes), ctypes.addressof(wc), ctypes.addressof(ws), _ptr(y))
+    return y, {"codes": codes, "scales": scales}
+
+
+def grouped_linear_block_bwd(dy, x: dict, split_sizes, w: dict, src_token=None, want_dx: bool = True,
+                             want_dw: bool = True, dw=None, workspace=None):
+    """Backward of grouped_linear_block_fwd.  x: the forward's 8-bit rows
+    (saved); w needs codes_t.  dw: where the weight gradients go (bf16 [E, N, K]
+    or a list of [N, K]; by default a new tensor).  Returns (dx bf16 [rows, K] or
+    None, dw or None)."""
+    rows, N, dev = _first(dy, "dy", torch.bfloat16)
+    if not isinstance(x, dict):
+        raise MoEError("x must be a dict of codes and scales")
+    codes, scales, x_rows, K, _ = _block_x(x, "x", dev)
+    if src_token is not None:
+        _arg(src_token, "src_token", torch.int32, (rows,), dev)
+    elif x_rows != rows:
+        raise MoEError(f"x has {x_rows} rows, dy {rows}")
+    wc = ws = dwt = None
+    E = split_sizes.numel() if isinstance(split_sizes, torch.Tensor) else 0
+    if want_dx:
+        wc, ws, E, _, _ = _block_w(w, "codes_t", (K, N), dev)
+    _arg(split_sizes, "split_sizes", torch.int32, (E,), dev)
+    if want_dw:
+        if dw is None:
+            dw = torch.empty((E, N, K), dtype=torch.bfloat16, device=dev)
+        dwt, Ew, _ = _table(dw, "dw", torch.bfloat16, (N, K), dev)
+        if Ew != E:
+            raise MoEError(f"dw must have one matrix per expert ({E})")
+    dx = torch.empty((rows, K), dtype=torch.bfloat16, device=dev) if want_dx else None
+    if workspace is None:
+        workspace = _workspace(moe_workspace_bytes(MOE_OP_LINEAR_BLOCK_BWD, rows, K, N, E, 1, 0), dev)
+    else:
+        _work_arg(workspace, dev)
+    _call("grouped_linear_block_bwd", dev, E, N, K, rows, _ptr(dy), _ptr(codes), _ptr(scales), x_rows,
+          _ptr(src_token), _ptr(split_sizes), *[0 if t is None else ctypes.addressof(t) for t in (wc, ws)],
+          _ptr(dx), 0 if dwt is None else ctypes.addressof(dwt), _ptr(workspace), workspace.numel())
+    return dx, (dw if want_dw else None)
 
 
 def trace_enable(capacity: int) -> None:

@@ -25,8 +25,9 @@ LIB = os.path.join(LIBDIR, "libmoe_mi355x.so")
 ARCH = "gfx950"
 
 SOURCES = ["route.hip", "router.hip", "permute.hip", "mxfp8.hip", "gemm.hip", "gemm_few.hip",
-           "check.hip", "layernorm.hip", "swiglu.hip", "capi.cpp", "mlp.cpp", "linear.cpp",
-           "sublayer.cpp", "trace.cpp"]
+           "check.hip", "layernorm.hip", "swiglu.hip", "rmsnorm.hip", "balance.hip",
+           "quant128.hip", "gemm_block.hip", "capi.cpp", "mlp.cpp", "linear.cpp",
+           "linear_block.cpp", "sublayer.cpp", "trace.cpp"]
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17",

@@ -1,0 +1,333 @@
+// Balance loss and z loss of the router's logits, per-expert counts, and the
+// logits' gradient, for gfx950.
+//
+//   p = softmax(logits of a token),  lse = log sum exp,  n = tokens that count,
+//   c_e = their picks of expert e,   f_e = c_e / (n k),  P_e = sum_t p_te / n
+//   loss = a E sum_e f_e P_e + z sum_t lse_t^2 / n
+//   dlogits_te = dloss [ a E / n p_te (f_e - sum_j f_j p_tj) + 2 z / n lse_t p_te ]
+//
+// Bound by launches for usual sizes (4 MB of logits at 16384 x 64), by HBM bytes
+// beyond.  A token has 2^j lanes with 1 or 4 experts each, so its maximum and sums are
+// lane shifts, and each lane adds up its own experts' probabilities over the
+// tokens it walks.  Sums are taken in a fixed order: a workgroup's partial
+// rows, which a second kernel adds (in one launch where one workgroup has all
+// tokens); counts are integers.  No float atomics.
+#include "common.hpp"
+#include "kernels.hpp"
+#include "trace.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxParts = 256;      // workgroups of the forward
+
+// Largest or sum over each G neighbouring lanes, the same for all of them.
+struct Max { static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); } };
+struct Sum { static __device__ __forceinline__ float of(float a, float b) { return a + b; } };
+template <class Op, int kCtrl>
+__device__ __forceinline__ float dpp_op(float v) {
+    return Op::of(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), kCtrl, 0xf, 0xf, true)));
+}
+template <int G, class Op>
+__device__ __forceinline__ float over(float v) {
+    if (G >= 2) v = dpp_op<Op, 0xB1>(v);        // quad_perm: lane ^ 1, lane ^ 2
+    if (G >= 4) v = dpp_op<Op, 0x4E>(v);
+    if (G >= 8) v = dpp_op<Op, 0x141>(v);       // row_half_mirror, row_mirror
+    if (G >= 16) v = dpp_op<Op, 0x140>(v);
+    if (G >= 32) v = Op::of(v, __shfl_xor(v, 16));
+    if (G >= 64) v = Op::of(v, __shfl_xor(v, 32));
+    return v;
+}
+
+struct BalArgs {
+    const float* logits;
+    const int32_t* topk;
+    const uint8_t* mask;        // NULL: every token counts
+    int64_t T;
+    int E, k;
+    float coef, zcoef;
+};
+
+// A token's logits in its lanes' registers (V experts each, -inf past E) to
+// probabilities, and its log sum exp.  A token without a finite or infinite
+// logit above -inf has no softmax: p = 0, lse = 0.
+template <int V, int G>
+__device__ __forceinline__ void softmax(float (&x)[V], float& lse) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
+    m = over<G, Max>(m);
+    const float top = m == -INFINITY ? 0.f : m;
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = expf(x[i] - top);
+        t += x[i];
+    }
+    t = over<G, Sum>(t);
+    const float inv = t == 0.f ? 0.f : 1.f / t;
+    lse = t == 0.f ? 0.f : top + logf(t);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] *= inv;
+}
+
+template <int V>
+__device__ __forceinline__ void load_logits(const float* row, int e0, int E, float (&x)[V]) {
+    if constexpr (V == 4) {
+        float4 w = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (e0 < E) w = *(const float4*)(row + e0);
+        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+    } else {
+        x[0] = e0 < E ? row[e0] : -INFINITY;
+    }
+}
+
+// What the sums become: losses [total, balance, z], counts [E] and the number
+// of tokens behind them, mean probabilities.  The thread of expert e has its
+// sums; one wave.
+__device__ void finish(const BalArgs& a, int e, double prob, int count, double z, int tokens,
+                       float* loss, int32_t* counts, float* mean_prob) {
+    const double n = tokens > 0 ? tokens : 1;
+    const float pe = (float)(prob / n);
+    double b = e < a.E ? (double)pe * (count / (n * a.k)) : 0.0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) b += __shfl_xor(b, o);
+    if (e < a.E) {
+        counts[e] = count;
+        if (mean_prob) mean_prob[e] = pe;
+    }
+    if (e == 0) {
+        counts[a.E] = tokens;
+        const double lb = (double)a.coef * a.E * b, lz = (double)a.zcoef * z / n;
+        loss[0] = (float)(lb + lz);
+        loss[1] = (float)lb;
+        loss[2] = (float)lz;
+    }
+}
+
+// Partial sums of a workgroup: [kMaxParts][E] probabilities, [kMaxParts] of
+// lse^2, then as integers [kMaxParts][E] counts and [kMaxParts] tokens.  With
+// one workgroup they are the sums, and it writes the outputs.
+template <int V, int G>
+__global__ __launch_bounds__(kThreads) void balance_fwd_kernel(BalArgs a, float* part, float* loss,
+                                                               int32_t* counts, float* mean_prob) {
+    constexpr int kSlots = kThreads / G;            // tokens at once
+    __shared__ float sp[kThreads / 64][64], sz[kThreads / 64];
+    __shared__ int sc[64], sn;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (tid < 64) sc[tid] = 0;
+    if (tid == 0) sn = 0;
+    __syncthreads();
+    const int e0 = (tid % G) * V;
+    float prob[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) prob[i] = 0.f;
+    float z = 0.f;
+    int n = 0;
+    for (int64_t t = (int64_t)blockIdx.x * kSlots + tid / G; t < a.T; t += (int64_t)gridDim.x * kSlots) {
+        if (a.mask && !a.mask[t]) continue;         // the same for the token's lanes
+        float x[V], lse;
+        load_logits<V>(a.logits + t * a.E, e0, a.E, x);
+        for (int j = tid % G; j < a.k; j += G) {
+            const int e = a.topk[t * a.k + j];
+            if ((unsigned)e < (unsigned)a.E) atomicAdd(&sc[e], 1);
+        }
+        softmax<V, G>(x, lse);
+#pragma unroll
+        for (int i = 0; i < V; ++i) prob[i] += x[i];
+        if (tid % G == 0) {
+            if (a.zcoef != 0.f) z += lse * lse;     // a row of the lowest logits: past fp32's range
+            ++n;
+        }
+    }
+    // the tokens of a wave, then the waves in order
+#pragma unroll
+    for (int o = G; o < 64; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < V; ++i) prob[i] += __shfl_xor(prob[i], o);
+    z = wave_sum(z);
+    if (n) atomicAdd(&sn, n);
+    if (lane < G)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e0 + i < 64) sp[wave][e0 + i] = prob[i];
+    if (lane == 0) sz[wave] = z;
+    __syncthreads();
+    if (tid >= 64) return;
+    const float p = tid < a.E ? (sp[0][tid] + sp[1][tid]) + (sp[2][tid] + sp[3][tid]) : 0.f;
+    const float zz = (sz[0] + sz[1]) + (sz[2] + sz[3]);
+    if (gridDim.x == 1) {
+        finish(a, tid, p, sc[tid], zz, sn, loss, counts, mean_prob);
+        return;
+    }
+    const int b = blockIdx.x;
+    int32_t* ci = (int32_t*)(part + kMaxParts * (a.E + 1));
+    if (tid < a.E) {
+        part[b * a.E + tid] = p;
+        ci[b * a.E + tid] = sc[tid];
+    }
+    if (tid == 0) {
+        part[kMaxParts * a.E + b] = zz;
+        ci[kMaxParts * a.E + b] = sn;
+    }
+}
+
+// The np partial sums added: thread (q, e) takes every 16th of expert e's.
+__global__ __launch_bounds__(1024) void balance_sum_kernel(BalArgs a, const float* __restrict__ part, int np,
+                                                           float* loss, int32_t* counts,
+                                                           float* mean_prob) {
+    __shared__ double sp[16][64], sz[16];
+    __shared__ int sc[16][64], sn[16];
+    const int e = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int32_t* ci = (const int32_t*)(part + kMaxParts * (a.E + 1));
+    double p = 0, z = 0;
+    int c = 0, n = 0;
+    if (e < a.E)
+#pragma unroll 8
+        for (int b = q; b < np; b += 16) {
+            p += part[b * a.E + e];
+            c += ci[b * a.E + e];
+        }
+    for (int b = q + 16 * e; b < np; b += 1024) {       // lane e's: all in one step
+        z += part[kMaxParts * a.E + b];
+        n += ci[kMaxParts * a.E + b];
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        z += __shfl_xor(z, o);
+        n += __shfl_xor(n, o);
+    }
+    sp[q][e] = p;
+    sc[q][e] = c;
+    if (e == 0) {
+        sz[q] = z;
+        sn[q] = n;
+    }
+    __syncthreads();
+    if (q) return;
+    p = z = 0;
+    c = n = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        p += sp[w][e];
+        c += sc[w][e];
+        z += sz[w];
+        n += sn[w];
+    }
+    finish(a, e, p, c, z, n, loss, counts, mean_prob);
+}
+
+template <int V, int G>
+__global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BalArgs a, const int32_t* __restrict__ counts,
+                                                               const float* __restrict__ dloss,
+                                                               const float* add, float* dlogits) {
+    constexpr int kSlots = kThreads / G;
+    const int e0 = (threadIdx.x % G) * V;
+    const int tokens = counts[a.E];
+    const float n = tokens > 0 ? (float)tokens : 1.f;
+    const float up = dloss ? dloss[0] : 1.f;
+    const float cb = up * (a.coef * (float)a.E / n), cz = up * (2.f * a.zcoef / n);
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = e0 + i < a.E ? (float)counts[e0 + i] / (n * (float)a.k) : 0.f;
+    for (int64_t t = (int64_t)blockIdx.x * kSlots + threadIdx.x / G; t < a.T;
+         t += (int64_t)gridDim.x * kSlots) {
+        float d[V], x[V];
+        const bool in = e0 < a.E;
+        const bool live = !(a.mask && !a.mask[t]);      // the same for the token's lanes
+        float old[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = old[i] = 0.f;
+        if (add && in) {
+            if constexpr (V == 4) {
+                const float4 w = *(const float4*)(add + t * a.E + e0);
+                old[0] = w.x; old[1] = w.y; old[2] = w.z; old[3] = w.w;
+            } else {
+                old[0] = add[t * a.E + e0];
+            }
+        }
+        if (live) {
+            float lse, s = 0.f;
+            load_logits<V>(a.logits + t * a.E, e0, a.E, x);
+            softmax<V, G>(x, lse);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s += x[i] * f[i];
+            s = over<G, Sum>(s);
+#pragma unroll
+            for (int i = 0; i < V; ++i) d[i] = x[i] * (cb * (f[i] - s) + cz * lse);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] += old[i];
+        if (in) {
+            if constexpr (V == 4) *(float4*)(dlogits + t * a.E + e0) = make_float4(d[0], d[1], d[2], d[3]);
+            else dlogits[t * a.E + e0] = d[0];
+        }
+    }
+}
+
+template <int N> struct Num { static constexpr int v = N; };
+// Experts per lane and lanes per token: 16 bytes a lane where rows allow it.
+template <class F>
+void with_lanes(int E, F&& f) {
+    if (E % 4 == 0) {
+        if (E <= 4) f(Num<4>{}, Num<1>{});
+        else if (E <= 8) f(Num<4>{}, Num<2>{});
+        else if (E <= 16) f(Num<4>{}, Num<4>{});
+        else if (E <= 32) f(Num<4>{}, Num<8>{});
+        else f(Num<4>{}, Num<16>{});
+    } else {
+        if (E <= 1) f(Num<1>{}, Num<1>{});
+        else if (E <= 2) f(Num<1>{}, Num<2>{});
+        else if (E <= 4) f(Num<1>{}, Num<4>{});
+        else if (E <= 8) f(Num<1>{}, Num<8>{});
+        else if (E <= 16) f(Num<1>{}, Num<16>{});
+        else if (E <= 32) f(Num<1>{}, Num<32>{});
+        else f(Num<1>{}, Num<64>{});
+    }
+}
+
+unsigned passes(int64_t T, int slots, int most) {
+    const int64_t n = (T + slots - 1) / slots;
+    return (unsigned)(n < 1 ? 1 : n < most ? n : most);
+}
+
+}  // namespace
+
+size_t balance_workspace_bytes(int E) { return (size_t)kMaxParts * 2 * (E + 1) * sizeof(float); }
+
+hipError_t launch_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t* topk,
+                              const uint8_t* mask, float coef, float zcoef, float* loss, int32_t* counts,
+                              float* mean_prob, void* ws, hipStream_t s) {
+    const BalArgs a{logits, topk, mask, T, E, k, coef, zcoef};
+    unsigned np = 1;
+    {
+        TraceScope ts("balance_fwd", s);
+        with_lanes(E, [&](auto v, auto g) {
+            np = passes(T, kThreads / decltype(g)::v, kMaxParts);
+            balance_fwd_kernel<decltype(v)::v, decltype(g)::v>
+                <<<np, kThreads, 0, s>>>(a, (float*)ws, loss, counts, mean_prob);
+        });
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || np == 1) return e;
+    TraceScope ts("balance_sum", s);
+    balance_sum_kernel<<<1, 1024, 0, s>>>(a, (const float*)ws, (int)np, loss, counts, mean_prob);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_bwd(const float* logits, int64_t T, int E, int k, const uint8_t* mask, float coef,
+                              float zcoef, const int32_t* counts, const float* dloss, const float* add,
+                              float* dlogits, hipStream_t s) {
+    if (T == 0) return hipSuccess;
+    const BalArgs a{logits, nullptr, mask, T, E, k, coef, zcoef};
+    TraceScope ts("balance_bwd", s);
+    with_lanes(E, [&](auto v, auto g) {
+        balance_bwd_kernel<decltype(v)::v, decltype(g)::v>
+            <<<passes(T, kThreads / decltype(g)::v, 2048), kThreads, 0, s>>>(a, counts, dloss, add, dlogits);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -65,6 +65,7 @@ size_t moe_workspace_bytes(int op, int64_t T, int H, int I, int E, int k, int pr
         case MOE_OP_ROUTER_BWD: return router_bwd_workspace_bytes(T, H, E);
         case MOE_OP_LINEAR_FWD: return k == 1 ? linear_fwd_workspace_bytes(T, I, H, E, precision) : 0;
         case MOE_OP_LINEAR_BWD: return k == 1 ? linear_bwd_workspace_bytes(T, I, H, E, precision) : 0;
+        case MOE_OP_LINEAR_BLOCK_BWD: return k == 1 ? linear_block_bwd_workspace_bytes(T, I, H, E) : 0;
         default: return 0;
     }
 }

@@ -124,4 +124,49 @@ hipError_t launch_swiglu_bwd(const bf16_t* da2, const bf16_t* a1, const uint8_t*
                              const uint8_t* scales, const float* prob, int64_t rows, int I,
                              bf16_t* da1, float* dprob, hipStream_t s);
 
+// ---- RMS norm with the residual's addition (h = x + residual in the stream's
+// type, s_f32; written when there is a residual), y and / or 8-bit rows
+size_t rmsnorm_workspace_bytes(int64_t T, int H);
+hipError_t launch_rmsnorm_fwd(const void* x, bool x_f32, const void* residual, bool s_f32, int64_t T,
+                              int H, const void* gamma, bool w_f32, float eps, void* h, bf16_t* y,
+                              float* rstd, uint8_t* codes, float* scales, hipStream_t s);
+hipError_t launch_rmsnorm_bwd(const bf16_t* dy, const void* h, bool s_f32, const float* rstd, int64_t T,
+                              int H, const void* gamma, bool w_f32, const void* dres, void* dx,
+                              bf16_t* branch, void* dgamma, void* ws, hipStream_t s);
+
+// ---- balance and z loss of the router's logits
+size_t balance_workspace_bytes(int E);
+hipError_t launch_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t* topk,
+                              const uint8_t* mask, float coef, float zcoef, float* loss, int32_t* counts,
+                              float* mean_prob, void* ws, hipStream_t s);
+hipError_t launch_balance_bwd(const float* logits, int64_t T, int E, int k, const uint8_t* mask, float coef,
+                              float zcoef, const int32_t* counts, const float* dloss, const float* add,
+                              float* dlogits, hipStream_t s);
+
+// ---- 8-bit blocks of 128 (block8.hpp): rows (scales [blocks][rows]), weights
+// (scales [N/128][K/128], transposed codes on request), rows to bf16
+hipError_t launch_quant_rows128(const bf16_t* x, int64_t rows, int cols, uint8_t* codes, float* scales,
+                                hipStream_t s, const char* name);
+hipError_t launch_quant_weights128(const MatTable& w, int nmat, int N, int K, const MatTable& codes,
+                                   const MatTable& scales, const MatTable* codes_t, hipStream_t s);
+hipError_t launch_dequant_rows128(const uint8_t* codes, const float* scales, const int32_t* src, int64_t x_rows,
+                                  int64_t rows, int cols, bf16_t* out, hipStream_t s, const char* name);
+
+// One grouped product of such operands: y rows of expert e = x rows times w_e^T.
+struct BlockGemm {
+    const uint8_t* x;           // [x_rows, K] codes
+    const float* x_scale;       // [K/128][x_rows]
+    int64_t x_rows;
+    const int32_t* src;         // row r is x row src[r]; NULL: r
+    const int32_t* split;
+    int E;
+    int64_t rows;
+    int N, K;
+    MatTable w;                 // [N, K] codes
+    MatTable w_scale;           // block (n, k) at n * sn + k * sk
+    int sn, sk;
+    bf16_t* y;                  // [rows, N]
+};
+hipError_t launch_gemm_block(const BlockGemm& p, hipStream_t s, const char* name);
+
 }  // namespace moe

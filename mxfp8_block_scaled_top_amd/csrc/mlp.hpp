@@ -114,6 +114,7 @@ int mlp_workspace_region(int op, int region, int64_t rows, int H, int I, int E, 
 size_t mlp_saved_bytes(int precision, int member, int64_t rows, int H, int I, int E);
 size_t linear_fwd_workspace_bytes(int64_t rows, int N, int K, int E, int precision);
 size_t linear_bwd_workspace_bytes(int64_t rows, int N, int K, int E, int precision);
+size_t linear_block_bwd_workspace_bytes(int64_t rows, int N, int K, int E);
 size_t mlp_bwd_workspace_bytes(int64_t rows, int H, int I, int E, int precision);
 
 }  // namespace moe

@@ -1,5 +1,5 @@
-// C ABI of the layer norm and of the ScaledSwiGLU by itself: argument
-// validation and launches.  The contracts are in include/moe_mi355x.h.
+// C ABI of the norms, of the balance loss and of the ScaledSwiGLU by itself:
+// argument validation and launches.  The contracts are in include/moe_mi355x.h.
 #include "moe_mi355x.h"
 
 #include <hip/hip_runtime.h>
@@ -32,9 +32,92 @@ int check_swiglu(int64_t rows, int I, const void* codes, const void* scales) {
     return MOE_OK;
 }
 
+// x, the stream it joins, gamma; without a residual the stream is x
+int check_rmsnorm(int x_type, int stream_type, int w_type, int64_t T, int H, const void* residual) {
+    if (bad_type(x_type) || bad_type(stream_type) || bad_type(w_type)) return MOE_ERR_ARG;
+    if (x_type != stream_type && (x_type == MOE_TYPE_F32 || (T > 0 && !residual))) return MOE_ERR_ARG;
+    if (T < 0 || T > INT32_MAX || H < 8 || (H % 8) || H > kMaxNormH) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+int check_balance(int64_t T, int E, int k, float coef, float zcoef) {
+    if (E < 1 || E > kMaxExperts || k < 1 || k > E || T < 0 || T > INT32_MAX / k) return MOE_ERR_SHAPE;
+    if (coef - coef != 0.f || zcoef - zcoef != 0.f) return MOE_ERR_ARG;     // finite
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t moe_rmsnorm_workspace_bytes(int64_t T, int H) {
+    if (T < 0 || T > INT32_MAX || H < 8 || (H % 8) || H > kMaxNormH) return 0;
+    return rmsnorm_workspace_bytes(T, H);
+}
+
+int moe_rmsnorm_fwd(int x_type, int stream_type, int w_type, int64_t T, int H, const void* x,
+                    const void* residual, const void* gamma, float eps, void* h, uint16_t* y, float* rstd,
+                    uint8_t* codes, float* scales, hipStream_t stream) {
+    const int st = check_rmsnorm(x_type, stream_type, w_type, T, H, residual);
+    if (st != MOE_OK) return st;
+    if ((codes == nullptr) != (scales == nullptr) || !(eps >= 0.f)) return MOE_ERR_ARG;
+    if (T > 0 && (!x || (residual && !h) || (!y && !codes))) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(y) ||
+        !aligned16(codes) || !aligned16(scales))
+        return MOE_ERR_ALIGN;
+    if (!moe_device_supported()) return MOE_ERR_UNSUPPORTED;
+    return hip_status(launch_rmsnorm_fwd(x, x_type == MOE_TYPE_F32, residual, stream_type == MOE_TYPE_F32, T,
+                                         H, gamma, w_type == MOE_TYPE_F32, eps, h, y, rstd, codes, scales,
+                                         stream));
+}
+
+int moe_rmsnorm_bwd(int stream_type, int w_type, int64_t T, int H, const uint16_t* dy, const void* h,
+                    const float* rstd, const void* gamma, const void* dres, void* dx, uint16_t* dx_branch,
+                    void* dgamma, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const int st = check_rmsnorm(stream_type, stream_type, w_type, T, H, nullptr);
+    if (st != MOE_OK) return st;
+    if (T > 0 && (!dy || !h || !rstd || !dx)) return MOE_ERR_NULL;
+    if (!aligned16(dy) || !aligned16(h) || !aligned16(gamma) || !aligned16(dres) || !aligned16(dx) ||
+        !aligned16(dx_branch) || !aligned16(dgamma) || !aligned16(workspace))
+        return MOE_ERR_ALIGN;
+    if (dgamma) {
+        if (!workspace) return MOE_ERR_NULL;
+        if (workspace_bytes < rmsnorm_workspace_bytes(T, H)) return MOE_ERR_WORKSPACE;
+    }
+    if (!moe_device_supported()) return MOE_ERR_UNSUPPORTED;
+    return hip_status(launch_rmsnorm_bwd(dy, h, stream_type == MOE_TYPE_F32, rstd, T, H, gamma,
+                                         w_type == MOE_TYPE_F32, dres, dx, dx_branch, dgamma, workspace,
+                                         stream));
+}
+
+size_t moe_balance_workspace_bytes(int E) {
+    return E < 1 || E > kMaxExperts ? 0 : balance_workspace_bytes(E);
+}
+
+int moe_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t* topk_expert,
+                    const uint8_t* mask, float balance_coef, float z_coef, float* losses, int32_t* counts,
+                    float* mean_prob, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const int st = check_balance(T, E, k, balance_coef, z_coef);
+    if (st != MOE_OK) return st;
+    if (!losses || !counts || !workspace || (T > 0 && (!logits || !topk_expert))) return MOE_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(workspace)) return MOE_ERR_ALIGN;
+    if (workspace_bytes < balance_workspace_bytes(E)) return MOE_ERR_WORKSPACE;
+    if (!moe_device_supported()) return MOE_ERR_UNSUPPORTED;
+    return hip_status(launch_balance_fwd(logits, T, E, k, topk_expert, mask, balance_coef, z_coef, losses,
+                                         counts, mean_prob, workspace, stream));
+}
+
+int moe_balance_bwd(const float* logits, int64_t T, int E, int k, const uint8_t* mask, float balance_coef,
+                    float z_coef, const int32_t* counts, const float* dloss, const float* dlogits_in,
+                    float* dlogits, hipStream_t stream) {
+    const int st = check_balance(T, E, k, balance_coef, z_coef);
+    if (st != MOE_OK) return st;
+    if (!counts || (T > 0 && (!logits || !dlogits))) return MOE_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(dlogits_in) || !aligned16(dlogits)) return MOE_ERR_ALIGN;
+    if (!moe_device_supported()) return MOE_ERR_UNSUPPORTED;
+    return hip_status(launch_balance_bwd(logits, T, E, k, mask, balance_coef, z_coef, counts, dloss,
+                                         dlogits_in, dlogits, stream));
+}
 
 size_t moe_layernorm_workspace_bytes(int64_t T, int H) {
     if (T < 0 || T > INT32_MAX || H < 8 || (H % 8) || H > kMaxNormH) return 0;

@@ -7,16 +7,20 @@ Only calls into libmoe_mi355x; the buffers are torch device tensors
 allocated once per shape (``LayerBuffers``) so that a timed loop allocates
 nothing.  With ``LayerBuffers(..., checkpoint=True)`` the expert MLP keeps its
 gate_up output in 8 bits; ``layer_step_norm`` is the pre-norm sublayer, a
-layer norm in front of the router.
+layer norm in front of the router, and ``layer_step_block`` the sublayer of an
+RMS norm whose 8-bit rows go to experts in 8-bit blocks of 128, with the
+router's balance loss.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (MOE_BF16, MOE_OP_MLP_BWD, MOE_OP_MLP_FWD, alloc_saved, grouped_mlp_bwd,
-               grouped_mlp_bwd_ckpt, grouped_mlp_fwd, grouped_mlp_fwd_ckpt, moe_layernorm_bwd,
-               moe_layernorm_fwd, moe_permute, moe_permute_prob, moe_route, moe_route_bwd,
-               moe_router_bwd, moe_router_fwd, moe_unpermute, moe_workspace_bytes)
+from . import (MOE_BF16, MOE_OP_MLP_BWD, MOE_OP_MLP_FWD, alloc_saved, grouped_linear_block_bwd,
+               grouped_linear_block_fwd, grouped_mlp_bwd, grouped_mlp_bwd_ckpt, grouped_mlp_fwd,
+               grouped_mlp_fwd_ckpt, moe_balance_bwd, moe_balance_fwd, moe_layernorm_bwd,
+               moe_layernorm_fwd, moe_permute, moe_permute_prob, moe_rmsnorm_bwd, moe_rmsnorm_fwd,
+               moe_route, moe_route_bwd, moe_router_bwd, moe_router_fwd, moe_swiglu_bwd,
+               moe_swiglu_fwd, moe_unpermute, moe_workspace_bytes)
 
 
 class LayerBuffers:
@@ -123,4 +127,40 @@ def layer_step_norm(x, gamma, beta, w_router, w1, w2, dy, k, precision=MOE_BF16,
         out["dn"] = out["dx"]
         out["dx"], out["dgamma"], out["dbeta"] = moe_layernorm_bwd(
             out["dn"], saved, gamma, x=None if checkpoint else x, dres=dres, dx_dtype=x.dtype)
+    return out
+
+
+def layer_step_block(x, residual, gamma, w_router, w1, w2, k, dy=None, dres=None, mask=None, eps=1e-6,
+                     balance_coef=0.01, z_coef=0.001, dloss=None, softmax_all=False) -> dict:
+    """The pre-norm sublayer with experts in 8-bit blocks of 128.  h = x +
+    residual (residual None: x) is the new residual stream; its RMS norm goes to
+    the router in bf16 and to the experts in 8 bits, gathered by token; w1
+    ([E, 2I, H]) and w2 ([E, H, I]) are dicts of fp8_block_quantize_weights
+    (with codes_t for the backward).  "y" is the experts' output, without the
+    residual, "loss" the balance and z loss over the tokens of mask.  With dy
+    also the backward: dres (h's type) is the gradient that reaches h past the
+    sublayer, dloss that of the loss; "dx" is the gradient of h, of x and of
+    residual ("dx_branch" in bf16 for a bf16 x beside an fp32 residual)."""
+    n, saved = moe_rmsnorm_fwd(x, gamma, eps, residual=residual, fp8=True)
+    r = moe_router_fwd(n, w_router, k, softmax_all)
+    loss, bal = moe_balance_fwd(r["logits"], r["topk_expert"], mask, balance_coef, z_coef)
+    split, src = r["split_sizes"], r["src_token"]
+    pp = moe_permute_prob(r["dest_row"], r["topk_prob"])
+    a1, n8 = grouped_linear_block_fwd(saved, split, w1, src_token=src)
+    a2, act = moe_swiglu_fwd(a1, pp)
+    yp, a8 = grouped_linear_block_fwd(a2, split, w2)
+    out = {"n": n, "norm_saved": saved, "h": saved["h"], "route": r, "logits": r["logits"], "loss": loss,
+           "balance": bal, "pp": pp, "a1": a1, "a2": a2, "yp": yp, "y": moe_unpermute(yp, r["dest_row"])}
+    if dy is None:
+        return out
+    dyp = moe_permute(dy, r["dest_row"])[0]
+    da2, out["dw2"] = grouped_linear_block_bwd(dyp, a8, split, w2)
+    da1, out["dpp"] = moe_swiglu_bwd(da2, act, pp)
+    dxp, out["dw1"] = grouped_linear_block_bwd(da1, n8, split, w1, src_token=src)
+    dl = moe_route_bwd(r["topk_prob"], out["dpp"], r["dest_row"], r["topk_expert"], len(w1["codes"]),
+                       r["logits"] if softmax_all else None, softmax_all)
+    out["dlogits"] = moe_balance_bwd(r["logits"], bal, mask, dloss, dlogits=dl, out=dl)
+    out["dn"], out["dw_router"] = moe_router_bwd(dl, n, w_router, r["dest_row"], dxp)
+    out["dx"], out["dgamma"], out["dx_branch"] = moe_rmsnorm_bwd(
+        out["dn"], saved, gamma, dres=dres, branch=x.dtype != saved["h"].dtype)
     return out

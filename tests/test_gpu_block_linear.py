@@ -1,0 +1,422 @@
+"""GPU: the 128-block quantizers (bit for bit) and the grouped products of such operands.
+
+A product's bound: the 128 products of a block are exact in fp32 (8 significant bits); the matrix
+instruction adds them with an error of about 2^-16 of their root mean square, counted here as 2^-13 of
+their 2-norm; the two scales' product and the fma round (2 u each, u = 2^-24, of the block's sum), and the
+running sum rounds once per block (u times the sum of the blocks' magnitudes).  bf16 outputs add half
+a step, 2^-8 of the value.  Weight gradients: x^ in bf16, 2^-8 of each product, and an fp32 sum over the rows."""
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_block_scaled_top_amd as moe
+from oracle import block8 as B
+from tests.helpers import need_gpu, np_, say
+from tests.test_gpu_rmsnorm import graph_check
+
+pytestmark = pytest.mark.gpu
+
+U, H8 = 2.0 ** -24, 2.0 ** -8
+BF = torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _randn(*shape, seed, scale=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale).to(BF)
+
+
+# ------------------------------------------------------------------ quantizers
+def _wild(R, C, seed):
+    """Values over the whole range of bf16: zeros, subnormals, rows near both ends."""
+    rng = np.random.default_rng(seed)
+    v = rng.standard_normal((R, C)).astype(np.float32) * np.exp2(rng.integers(-148, 126, (R, 1))).astype(np.float32)
+    v[rng.random((R, C)) < 0.05] = 0.0
+    return torch.from_numpy(v).clamp(-3e38, 3e38).to(BF)
+
+
+@pytest.mark.parametrize("R,C", [(1, 8), (1, 4096), (3, 128), (130, 136), (65, 264), (7, 1416), (500, 520), (33, 14336)])
+def test_rows_bit_exact(R, C):
+    say(f"block quantize rows {R} x {C}")
+    for x in (_randn(R, C, seed=C), _wild(R, C, R + C)):
+        codes, scales = moe.fp8_block_quantize(x.cuda())
+        torch.cuda.synchronize()
+        c, s = B.quantize_rows(x)
+        assert np.array_equal(np_(scales), s) and np.array_equal(np_(codes), c)
+
+
+def test_rows_ties_and_every_mantissa():
+    """Blocks whose scale is a power of two over 7 (amax = 2^k, many exact ties) and every bf16 mantissa."""
+    say("block quantize ties")
+    m = torch.arange(128).float() / 128 + 1
+    x = torch.stack([torch.cat([m * 2.0 ** -j, torch.tensor([2.0]), torch.zeros(127)])[:128].contiguous()
+                     for j in range(0, 12)])
+    x[:, 0] = 2.0
+    x = torch.cat([x, x * 1.75, -x]).to(BF)
+    codes, scales = moe.fp8_block_quantize(x.cuda())
+    torch.cuda.synchronize()
+    c, s = B.quantize_rows(x)
+    assert np.array_equal(np_(scales), s) and np.array_equal(np_(codes), c)
+
+
+def test_rows_non_finite():
+    say("block quantize non-finite")
+    x = _randn(6, 384, seed=1)
+    x[1, 5], x[2, 200], x[3, 383] = float("nan"), float("inf"), -float("inf")
+    codes, scales = moe.fp8_block_quantize(x.cuda())
+    torch.cuda.synchronize()
+    v = B.rows_value(np_(codes), np_(scales))
+    bad = torch.zeros(6, 384, dtype=torch.bool)
+    bad[1, :128] = bad[2, 128:256] = bad[3, 256:] = True
+    assert torch.equal(v.isnan(), bad)
+    c, s = B.quantize_rows(x.masked_fill(bad, 0.0))
+    assert np.array_equal(np_(codes)[~bad.numpy()], c[~bad.numpy()])
+
+
+@pytest.mark.parametrize("E,N,K", [(1, 8, 8), (2, 128, 128), (3, 136, 264), (1, 520, 1416), (5, 40, 296), (64, 32, 160)])
+def test_weights_bit_exact(E, N, K):
+    say(f"block quantize weights {E} x {N} x {K}")
+    for w in (_randn(E, N, K, seed=K), _wild(E * N, K, N).reshape(E, N, K)):
+        q = moe.fp8_block_quantize_weights(w.cuda(), transposed=True)
+        only = moe.fp8_block_quantize_weights([t.contiguous() for t in w.cuda()])
+        torch.cuda.synchronize()
+        assert only["codes_t"] is None
+        for e in range(E):
+            c, s = B.quantize_weight(w[e])
+            assert np.array_equal(np_(q["scales"][e]), s) and np.array_equal(np_(q["codes"][e]), c)
+            assert np.array_equal(np_(q["codes_t"][e]), c.T)
+            assert torch.equal(only["codes"][e], q["codes"][e]) and torch.equal(only["scales"][e], q["scales"][e])
+
+
+def test_no_rows_and_rows_past_32_bits():
+    say("block quantize T=0 and 2^31 values")
+    codes, scales = moe.fp8_block_quantize(torch.empty((0, 256), dtype=BF, device="cuda"))
+    assert codes.shape == (0, 256) and scales.shape == (2, 0)
+    T, C, n = 540_000, 4096, 1000
+    x = torch.ones((T, C), dtype=BF, device="cuda")
+    x[-n:] = _randn(n, C, seed=2).cuda()
+    codes, scales = moe.fp8_block_quantize(x)
+    c1, s1 = moe.fp8_block_quantize(x[-n:].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(codes[-n:], c1) and torch.equal(scales[:, -n:], s1) and (codes[:-n] == 0x7E).all()
+
+
+# ------------------------------------------------------------------ products
+def _problem(split, E, N, K, seed, tokens=0, extra=0):
+    rows = sum(split) + extra
+    src_rows = tokens or rows
+    x = _randn(src_rows, K, seed=seed) * (0.25 + torch.rand(src_rows, 1, generator=torch.Generator().manual_seed(seed + 1)) * 4)
+    x[:, ::37] *= 16
+    w = _randn(E, N, K, seed=seed + 2, scale=K ** -0.5)
+    src = torch.randint(0, tokens, (rows,), generator=torch.Generator().manual_seed(seed + 3)).int() if tokens else None
+    xc, xs = B.quantize_rows(x.to(BF))
+    wq = [B.quantize_weight(t) for t in w]
+    p = {"split": split, "rows": rows, "E": E, "N": N, "K": K,
+         "x8": {"codes": torch.from_numpy(xc).cuda(), "scales": torch.from_numpy(xs).cuda()},
+         "w8": {"codes": torch.from_numpy(np.stack([c for c, _ in wq])).cuda(),
+                "scales": torch.from_numpy(np.stack([s for _, s in wq])).cuda(),
+                "codes_t": torch.from_numpy(np.stack([np.ascontiguousarray(c.T) for c, _ in wq])).cuda()},
+         "xbf": x.to(BF), "src": None if src is None else src.cuda(),
+         "sd": torch.tensor(split, dtype=torch.int32, device="cuda")}
+    xv = B.rows_value(xc, xs)
+    if src is not None:
+        good = (src >= 0) & (src < tokens)
+        xv = xv[src.clamp(0, tokens - 1).long()] * good[:, None]
+    p["x"], p["w"] = xv, [B.weight_value(c, s) for c, s in wq]
+    return p
+
+
+def _product_bound(a, b):
+    """|fp32 error| of a [M, K] times b [N, K]^T by blocks of 128 along K."""
+    M, N = a.shape[0], b.shape[0]
+    two, mag = torch.zeros(M, N).double(), torch.zeros(M, N).double()
+    for k in range(0, a.shape[1], 128):
+        x, w = a[:, k:k + 128], b[:, k:k + 128]
+        two += (x.square() @ w.square().T).sqrt()
+        mag += (x.abs() @ w.abs().T)
+    return 2.0 ** -13 * two + (a.shape[1] // 128 + 5) * U * mag
+
+
+def _check(got, ref, bound, what):
+    d = (got.double().cpu() - ref).abs()
+    lim = bound + H8 * (ref.abs() + bound) + 1e-37
+    assert (d <= lim).all(), (what, float((d / lim).max()))
+
+
+def _check_fwd(p, y):
+    at = 0
+    for e, n in enumerate(p["split"]):
+        a = p["x"][at:at + n]
+        _check(y[at:at + n], a @ p["w"][e].T, _product_bound(a, p["w"][e]), f"expert {e}")
+        at += n
+
+
+SHAPES = [([1], 32, 32), ([2], 64, 96), ([0, 1, 0, 1], 288, 160), ([3, 0, 5], 160, 128), ([16, 17, 15], 96, 256),
+          ([64, 1, 65], 320, 416), ([129, 0, 127, 3], 544, 288), ([300], 1056, 1408), ([257, 511], 256, 640),
+          ([1] * 64, 64, 128), ([40, 0, 0, 90], 2080, 2048), ([700, 5], 768, 384), ([1, 1], 512, 4096), ([5], 4128, 64)]
+
+
+@pytest.mark.parametrize("split,N,K", SHAPES)
+@pytest.mark.parametrize("gather", [False, True], ids=["rows", "gather"])
+def test_forward(split, N, K, gather):
+    say(f"block product {split[:6]} N={N} K={K} gather={gather}")
+    p = _problem(split, len(split), N, K, seed=N + K, tokens=max(1, sum(split) // 2 + 1) if gather else 0)
+    y, saved = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"], src_token=p["src"])
+    y2, saved2 = moe.grouped_linear_block_fwd(p["xbf"].cuda(), p["sd"], p["w8"], src_token=p["src"])
+    torch.cuda.synchronize()
+    assert y.dtype == BF and y.shape == (p["rows"], N)
+    _check_fwd(p, y)
+    assert torch.equal(y, y2) and torch.equal(saved2["codes"], p["x8"]["codes"]) and saved["codes"] is p["x8"]["codes"]
+
+
+@pytest.mark.parametrize("split,N,K", SHAPES)
+@pytest.mark.parametrize("gather", [False, True], ids=["rows", "gather"])
+def test_backward(split, N, K, gather):
+    say(f"block product backward {split[:6]} N={N} K={K} gather={gather}")
+    p = _problem(split, len(split), N, K, seed=N + 2 * K, tokens=max(1, sum(split) // 2 + 1) if gather else 0)
+    dy = _randn(p["rows"], N, seed=5)
+    dx, dw = moe.grouped_linear_block_bwd(dy.cuda(), p["x8"], p["sd"], p["w8"], src_token=p["src"])
+    torch.cuda.synchronize()
+    dyq = B.rows_value(*B.quantize_rows(dy))
+    rx, rw = B.linear_bwd(dy, dyq, p["x"], p["w"], split)
+    assert dx.shape == (p["rows"], K) and dw.shape == (len(split), N, K)
+    at = 0
+    for e, n in enumerate(split):
+        _check(dx[at:at + n], rx[at:at + n], _product_bound(dyq[at:at + n], p["w"][e].T.contiguous()), f"dx {e}")
+        mag = dy[at:at + n].double().abs().T @ p["x"][at:at + n].abs()
+        _check(dw[e], rw[e], (H8 + (n + 8) * U) * mag, f"dw {e}")
+        if n == 0:
+            assert not dw[e].any()
+        at += n
+    # one gradient alone, and into the caller's buffers: the same bits
+    only, none = moe.grouped_linear_block_bwd(dy.cuda(), p["x8"], p["sd"], p["w8"], src_token=p["src"], want_dw=False)
+    buf = [torch.full((N, K), 9.0, dtype=BF, device="cuda") for _ in split]
+    none2, same = moe.grouped_linear_block_bwd(dy.cuda(), p["x8"], p["sd"], p["w8"], src_token=p["src"], want_dx=False,
+                                               dw=buf)
+    torch.cuda.synchronize()
+    assert none is None and none2 is None and same is buf and torch.equal(only, dx)
+    assert all(torch.equal(a, b) for a, b in zip(buf, dw))
+
+
+def test_input_gradient_against_differences():
+    """dx of sum(y dy) where dy is exact in 8 bits (+-1, so dy^ = dy) against central differences of the
+    float64 product with respect to x^ (linear: exact); half a bf16 step and the product's bound."""
+    say("block product dx against differences")
+    p = _problem([3, 2], 2, 64, 96, seed=3)
+    dy = (torch.randint(0, 2, (5, 64), generator=torch.Generator().manual_seed(1)) * 2 - 1).to(BF)
+    dx, dw = moe.grouped_linear_block_bwd(dy.cuda(), p["x8"], p["sd"], p["w8"])
+    torch.cuda.synchronize()
+
+    def f(x, w):
+        return float((B.linear_fwd(x, w, [3, 2]) * dy.double()).sum())
+    for r, k in ((0, 0), (2, 95), (4, 31)):
+        e = torch.zeros_like(p["x"])
+        e[r, k] = 0.5
+        d = f(p["x"] + e, p["w"]) - f(p["x"] - e, p["w"])
+        assert abs(d - float(dx[r, k])) <= H8 * abs(d) + 1e-4
+    e = torch.zeros_like(p["w"][1])
+    e[63, 7] = 0.5
+    d = f(p["x"], [p["w"][0], p["w"][1] + e]) - f(p["x"], [p["w"][0], p["w"][1] - e])
+    assert abs(d - float(dw[1, 63, 7])) <= H8 * abs(d) + H8 * float(p["x"][3:, 7].abs().sum())
+
+
+def test_scales_of_any_size():
+    """Scales far from 1 and products that leave fp32's range: as the formula says."""
+    say("block product wide scales")
+    p = _problem([9, 30], 2, 96, 256, seed=8)
+    up = torch.tensor([2.0 ** 90, 2.0 ** -100])
+    x8 = {"codes": p["x8"]["codes"], "scales": (p["x8"]["scales"].cpu() * up[:, None]).cuda()}
+    y, _ = moe.grouped_linear_block_fwd(x8, p["sd"], p["w8"])
+    torch.cuda.synchronize()
+    x = p["x"] * up.double().repeat_interleave(128)
+    at = 0
+    for e, n in enumerate(p["split"]):
+        _check(y[at:at + n], x[at:at + n] @ p["w"][e].T, _product_bound(x[at:at + n], p["w"][e]), "wide")
+        at += n
+
+
+def test_rows_behind_the_last_expert_stay():
+    say("block product guard rows")
+    p = _problem([5, 70], 2, 160, 192, seed=4, extra=60)
+    L, q = moe.lib(), (lambda t: t.data_ptr())
+    y = torch.full((p["rows"] + 9, 160), 3.0, dtype=BF, device="cuda")
+    wc, ws = moe._ptr_array(list(p["w8"]["codes"])), moe._ptr_array(list(p["w8"]["scales"]))
+    s = torch.cuda.current_stream().cuda_stream
+    assert L.grouped_linear_block_fwd(2, 160, 192, p["rows"], q(p["x8"]["codes"]), q(p["x8"]["scales"]), p["rows"], None,
+                                      q(p["sd"]), wc, ws, q(y), s) == 0
+    torch.cuda.synchronize()
+    _check_fwd(p, y)
+    assert (y[75:] == 3).all()
+    dx = torch.full((p["rows"] + 9, 192), 4.0, dtype=BF, device="cuda")
+    dw = torch.full((2 * 160 * 192 + 64,), 5.0, dtype=BF, device="cuda")
+    n = moe.moe_workspace_bytes(moe.MOE_OP_LINEAR_BLOCK_BWD, p["rows"], 192, 160, 2, 1, 0)
+    wk = torch.full((n + 64,), 6, dtype=torch.uint8, device="cuda")
+    dy = _randn(p["rows"], 160, seed=6).cuda()
+    dwp = moe._ptr_array([dw[:160 * 192], dw[160 * 192:]])
+    wt = moe._ptr_array(list(p["w8"]["codes_t"]))
+    assert L.grouped_linear_block_bwd(2, 160, 192, p["rows"], q(dy), q(p["x8"]["codes"]), q(p["x8"]["scales"]), p["rows"],
+                                      None, q(p["sd"]), wt, ws, q(dx), dwp, q(wk), n, s) == 0
+    torch.cuda.synchronize()
+    assert (dx[75:] == 4).all() and (dw[2 * 160 * 192:] == 5).all() and (wk[n:] == 6).all()
+    r = B.linear_bwd(dy.cpu(), B.rows_value(*B.quantize_rows(dy.cpu())), p["x"], p["w"], p["split"])
+    mag = dy.cpu()[5:75].double().abs().T @ p["x"][5:75].abs()
+    _check(dw[160 * 192:2 * 160 * 192].reshape(160, 192), r[1][1], (H8 + 90 * U) * mag, "dw")
+
+
+@pytest.mark.parametrize("split", [[-5, 20, 30], [50, 50, 50], [0, 0, 0], [2 ** 31 - 1, 2 ** 31 - 1, 5], [40, -2 ** 31, 1]])
+def test_bad_sizes_stay_inside(split):
+    """Sizes that do not sum to the rows: negative ones count as 0, and what passes the rows is cut."""
+    say(f"block product sizes {split}")
+    p = _problem([20, 30, 10], 3, 96, 160, seed=7)
+    sd = torch.tensor(split, dtype=torch.int64).to(torch.int32).cuda()
+    buf = torch.full((p["rows"] + 40, 96), 3.0, dtype=BF, device="cuda")
+    L, q = moe.lib(), (lambda t: t.data_ptr())
+    wc, ws = moe._ptr_array(list(p["w8"]["codes"])), moe._ptr_array(list(p["w8"]["scales"]))
+    assert L.grouped_linear_block_fwd(3, 96, 160, p["rows"], q(p["x8"]["codes"]), q(p["x8"]["scales"]), p["rows"], None,
+                                      q(sd), wc, ws, q(buf), torch.cuda.current_stream().cuda_stream) == 0
+    dy = _randn(p["rows"], 96, seed=9).cuda()
+    dx, dw = moe.grouped_linear_block_bwd(dy, p["x8"], sd, p["w8"])
+    torch.cuda.synchronize()
+    cut, left = [], p["rows"]
+    for n in split:
+        cut.append(min(max(n, 0), left))
+        left -= cut[-1]
+    assert (buf[sum(cut):] == 3).all()
+    at = 0
+    for e, n in enumerate(cut):
+        a = p["x"][at:at + n]
+        _check(buf[at:at + n], a @ p["w"][e].T, _product_bound(a, p["w"][e]), "cut")
+        at += n
+
+
+@pytest.mark.parametrize("bad", [-1, 31, 2 ** 31 - 1, -2 ** 31])
+def test_tokens_out_of_range_are_rows_of_zeros(bad):
+    say(f"block product src_token {bad}")
+    p = _problem([40, 33], 2, 96, 160, seed=9, tokens=31)
+    clean, _ = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"], src_token=p["src"])
+    src = p["src"].clone()
+    src[[0, 17, 72]] = bad
+    y, _ = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"], src_token=src)
+    dy = _randn(73, 96, seed=3).cuda()
+    _, dw = moe.grouped_linear_block_bwd(dy, p["x8"], p["sd"], p["w8"], src_token=src)
+    dz = dy.clone()
+    dz[[0, 17, 72]] = 0
+    _, want = moe.grouped_linear_block_bwd(dz, p["x8"], p["sd"], p["w8"], src_token=p["src"])
+    torch.cuda.synchronize()
+    keep = torch.ones(73, dtype=torch.bool)
+    keep[[0, 17, 72]] = False
+    assert not y[~keep].any() and torch.equal(y[keep], clean[keep])
+    assert torch.equal(dw, want)
+
+
+def test_nan_stays_in_its_row_and_column():
+    say("block product NaN")
+    for split in ([40, 30], [3, 2]):
+        p = _problem(split, 2, 96, 160, seed=10)
+        rows = sum(split)
+        clean, _ = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"])
+        codes = p["x8"]["codes"].clone()
+        codes[1, 150] = 0x7F
+        y, _ = moe.grouped_linear_block_fwd({"codes": codes, "scales": p["x8"]["scales"]}, p["sd"], p["w8"])
+        sc = p["x8"]["scales"].clone()
+        sc[1, rows - 1] = float("nan")
+        z, _ = moe.grouped_linear_block_fwd({"codes": p["x8"]["codes"], "scales": sc}, p["sd"], p["w8"])
+        wc = p["w8"]["codes"].clone()
+        wc[0, 33, 7] = 0xFF
+        v, _ = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"] | {"codes": wc})
+        torch.cuda.synchronize()
+        keep = torch.arange(rows) != 1
+        assert y[1].isnan().all() and torch.equal(y[keep], clean[keep])
+        assert z[-1].isnan().all() and torch.equal(z[:-1], clean[:-1])
+        col = torch.arange(96) != 33
+        assert v[:split[0], 33].isnan().all() and torch.equal(v[:, col], clean[:, col])
+        assert torch.equal(v[split[0]:], clean[split[0]:])
+
+
+def test_empty_calls():
+    say("block product without rows")
+    p = _problem([4], 1, 64, 96, seed=11)
+    none = {"codes": p["x8"]["codes"][:0], "scales": p["x8"]["scales"][:, :0].contiguous()}
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y, _ = moe.grouped_linear_block_fwd(none, zero, p["w8"])
+    dx, dw = moe.grouped_linear_block_bwd(torch.empty((0, 64), dtype=BF, device="cuda"), none, zero, p["w8"])
+    torch.cuda.synchronize()
+    assert y.shape == (0, 64) and dx.shape == (0, 96) and not dw.any()
+    # rows that gather from no token at all
+    src = torch.zeros(4, dtype=torch.int32, device="cuda")
+    y, _ = moe.grouped_linear_block_fwd(none, p["sd"], p["w8"], src_token=src)
+    torch.cuda.synchronize()
+    assert not y.any()
+
+
+@pytest.mark.parametrize("T,N,K", [(1_060_000, 32, 4096), (1_060_000, 2048, 32)])
+def test_offsets_past_32_bits(T, N, K):
+    """Operands and outputs above 4 GB: the last rows are what they are by themselves."""
+    say(f"block product {T} x {N} x {K}")
+    n = 700
+    p = _problem([n], 1, N, K, seed=12)
+    codes = torch.full((T, K), 0x38, dtype=torch.uint8, device="cuda")
+    scales = torch.ones((p["x8"]["scales"].shape[0], T), device="cuda")
+    codes[-n:], scales[:, -n:] = p["x8"]["codes"], p["x8"]["scales"]
+    y, _ = moe.grouped_linear_block_fwd({"codes": codes, "scales": scales}, torch.tensor([T], dtype=torch.int32, device="cuda"),
+                                        p["w8"])
+    ref, _ = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"])
+    torch.cuda.synchronize()
+    _check_fwd(p, ref)
+    _check_fwd(p, y[-n:])
+
+
+def test_same_bits_in_a_graph_and_on_two_streams():
+    say("block product in a graph, on two streams")
+    p = _problem([300, 0, 211, 5], 4, 288, 416, seed=13, tokens=400)
+    dy = _randn(p["rows"], 288, seed=1).cuda()
+    n = moe.moe_workspace_bytes(moe.MOE_OP_LINEAR_BLOCK_BWD, p["rows"], 416, 288, 4, 1, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def step():
+        y, _ = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"], src_token=p["src"])
+        return [y, *moe.grouped_linear_block_bwd(dy, p["x8"], p["sd"], p["w8"], src_token=p["src"], workspace=ws)]
+
+    q = moe.fp8_block_quantize_weights(_randn(4, 288, 416, seed=3).cuda())
+    graph_check(step, lambda: moe.grouped_linear_block_fwd(p["xbf"].cuda(), p["sd"], q, src_token=p["src"]))
+    ref = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for s in (a, b):
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                outs.append(moe.grouped_linear_block_bwd(dy, p["x8"], p["sd"], p["w8"], src_token=p["src"]))
+    torch.cuda.synchronize()
+    for dx, dw in outs:
+        assert torch.equal(dx, ref[1]) and torch.equal(dw, ref[2])
+
+
+def test_binding_refusals():
+    say("block product binding refusals")
+    p = _problem([4, 4], 2, 64, 96, seed=14)
+    x, w, sd = p["x8"], p["w8"], p["sd"]
+    dy = torch.zeros((8, 64), dtype=BF, device="cuda")
+    src = torch.zeros(8, dtype=torch.int32, device="cuda")
+    for call in (
+            lambda: moe.fp8_block_quantize(dy.float()), lambda: moe.fp8_block_quantize(dy[:, :12].contiguous()),
+            lambda: moe.fp8_block_quantize(dy.t()),
+            lambda: moe.fp8_block_quantize_weights(dy), lambda: moe.fp8_block_quantize_weights([dy, dy[:4]]),
+            lambda: moe.fp8_block_quantize_weights(dy[None].expand(65, 8, 64).contiguous()),
+            lambda: moe.grouped_linear_block_fwd(x, sd, w["codes"]), lambda: moe.grouped_linear_block_fwd(x, sd[:1], w),
+            lambda: moe.grouped_linear_block_fwd({"codes": x["codes"]}, sd, w),
+            lambda: moe.grouped_linear_block_fwd(x | {"scales": x["scales"][:, :4]}, sd, w),
+            lambda: moe.grouped_linear_block_fwd(x, sd, w | {"scales": w["scales"][:1]}),
+            lambda: moe.grouped_linear_block_fwd(x, sd, w | {"codes": w["codes"][:, :, :64].contiguous()}),
+            lambda: moe.grouped_linear_block_fwd(x, sd, w, src_token=src.long()),
+            lambda: moe.grouped_linear_block_fwd(dy, sd, w), lambda: moe.grouped_linear_block_bwd(dy, x, sd, w, src[:3]),
+            lambda: moe.grouped_linear_block_bwd(dy[:4], x, sd, w), lambda: moe.grouped_linear_block_bwd(dy, dy, sd, w),
+            lambda: moe.grouped_linear_block_bwd(dy, x, sd, w | {"codes_t": None}),
+            lambda: moe.grouped_linear_block_bwd(dy, x, sd, w, dw=w["codes"]),
+            lambda: moe.grouped_linear_block_bwd(dy, x, sd, w, dw=[dy]),
+            lambda: moe.grouped_linear_block_bwd(dy, x, sd, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(moe.MoEError):
+            call()
