@@ -29,9 +29,10 @@ int check_block(int E, int N, int K, int64_t rows, int64_t x_rows, const void* s
     if (N < 32 || K < 32 || (N % 32) || (K % 32)) return MOE_ERR_SHAPE;
     if (rows < 0 || rows > INT32_MAX || x_rows < 0 || x_rows > INT32_MAX) return MOE_ERR_SHAPE;
     if (!src_token && x_rows != rows) return MOE_ERR_SHAPE;
-    // offsets inside one bf16 weight (gradient) and inside the gathered codes
+    // offsets inside one bf16 weight (gradient), 256 rows and the gathered codes
     if ((int64_t)N * K * 2 >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
-    if (src_token && x_rows * K >= (int64_t)UINT32_MAX) return MOE_ERR_SHAPE;
+    if (N > (1 << 22) || K > (1 << 22)) return MOE_ERR_SHAPE;
+    if (src_token && x_rows * K >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
     // workgroups of a launch (tiles of 64 rows and 128 columns at least)
     const int64_t widest = N > K ? N : K;
     if ((rows / 64 + E) * ((widest + 127) / 128) > INT32_MAX) return MOE_ERR_SHAPE;

@@ -204,7 +204,8 @@ def test_block_quantize_weights_refuses(L, change, status):
 BLOCK_SHAPES = [({"E": 0}, SHAPE), ({"E": 65}, SHAPE), ({"N": 0}, SHAPE), ({"N": 48}, SHAPE), ({"K": 16}, SHAPE),
                 ({"K": 100}, SHAPE), ({"rows": -1}, SHAPE), ({"rows": 1 << 31}, SHAPE), ({"xr": -1}, SHAPE),
                 ({"xr": 9}, SHAPE), ({"N": 1 << 15, "K": 1 << 15}, SHAPE),
-                ({"src": P, "xr": (1 << 31) - 1, "K": 64}, SHAPE), ({"split": None}, NULL)]
+                ({"src": P, "xr": 1 << 25, "K": 64}, SHAPE), ({"N": (1 << 22) + 32}, SHAPE), ({"K": 1 << 23}, SHAPE),
+                ({"split": None}, NULL)]
 
 
 @pytest.mark.parametrize("change,status", BLOCK_SHAPES + [
