@@ -855,7 +855,7 @@ size_t moe_rmsnorm_workspace_bytes(int64_t T, int H);
  * mask         uint8 [T], 0 for a token that does not count (its logits and
  *              picks are not read); NULL: every token counts.
  * losses       fp32 [3] out: balance + z, balance, z (0 when no token counts).
- * counts       int32 [E+1] out: c_e, then n.
+ * counts       int32 [E] out: c_e.   tokens: int32 [1] out: n.
  * mean_prob    fp32 [E] out: P_e, or NULL.
  * workspace    moe_balance_workspace_bytes(E) bytes.
  * A token whose logits are all -infinity has p = 0 and lse = 0; NaN or
@@ -864,8 +864,8 @@ size_t moe_rmsnorm_workspace_bytes(int64_t T, int H);
  */
 int moe_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t* topk_expert,
                     const uint8_t* mask, float balance_coef, float z_coef, float* losses,
-                    int32_t* counts, float* mean_prob, void* workspace, size_t workspace_bytes,
-                    hipStream_t stream);
+                    int32_t* counts, int32_t* tokens, float* mean_prob, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream);
 
 /*
  * moe_balance_bwd -- gradient of losses[0] with respect to the logits.
@@ -874,15 +874,15 @@ int moe_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t*
  *   dlogits_te = dloss [balance_coef E / n p_te (f_e - sum_j f_j p_tj)
  *                       + 2 z_coef / n lse_t p_te] + dlogits_in_te
  * The counts are constants; a token that does not count has dlogits_in alone.
- * counts       int32 [E+1] from the forward.   mask, k and coefficients: as there.
+ * counts, tokens   from the forward.   mask, k and coefficients: as there.
  * dloss        fp32 [1] device, the gradient of the loss; NULL: 1.
  * dlogits_in   fp32 [T, E], such as moe_route_bwd's dlogits, or NULL; may be
  *              dlogits.
  * dlogits      fp32 [T, E] out.
  */
 int moe_balance_bwd(const float* logits, int64_t T, int E, int k, const uint8_t* mask,
-                    float balance_coef, float z_coef, const int32_t* counts, const float* dloss,
-                    const float* dlogits_in, float* dlogits, hipStream_t stream);
+                    float balance_coef, float z_coef, const int32_t* counts, const int32_t* tokens,
+                    const float* dloss, const float* dlogits_in, float* dlogits, hipStream_t stream);
 
 /* Workspace bytes of moe_balance_fwd; 0 for an E it refuses. */
 size_t moe_balance_workspace_bytes(int E);

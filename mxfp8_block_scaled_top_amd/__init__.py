@@ -17,6 +17,7 @@ moe_workspace_bytes, moe_workspace_region.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -106,8 +107,8 @@ def lib() -> ctypes.CDLL:
             "moe_rmsnorm_bwd": (I32, [I32, I32, I64, I32, P, P, P, P, P, P, P, P, P, SZ, P]),
             "moe_balance_workspace_bytes": (SZ, [I32]),
             "moe_balance_fwd": (I32, [P, I64, I32, I32, P, P, ctypes.c_float, ctypes.c_float, P, P, P, P,
-                                      SZ, P]),
-            "moe_balance_bwd": (I32, [P, I64, I32, I32, P, ctypes.c_float, ctypes.c_float, P, P, P, P, P]),
+                                      P, SZ, P]),
+            "moe_balance_bwd": (I32, [P, I64, I32, I32, P, ctypes.c_float, ctypes.c_float, P, P, P, P, P, P]),
             "fp8_block_quantize": (I32, [P, I64, I64, P, P, P]),
             "fp8_block_quantize_weights": (I32, [I32, I64, I64, P, P, P, P, P]),
             "grouped_linear_block_fwd": (I32, [I32, I32, I32, I64, P, P, I64, P, P, P, P, P, P]),
@@ -924,8 +925,8 @@ def moe_balance_fwd(logits, topk_expert, mask=None, balance_coef: float = 0.01, 
     """Balance loss and z loss of the router.  logits fp32 [T, E], topk_expert
     int32 [T, k], mask bool or uint8 [T] (0: the token does not count) or None.
     Returns (loss fp32 scalar, saved): saved holds counts (int32 [E]), tokens
-    (int32 [1]), mean_prob (fp32 [E]), the losses balance and z one by one, and
-    what the backward takes."""
+    (int32 [1]), mean_prob (fp32 [E]), losses (fp32 [3]: the loss, its balance
+    and its z part) and what the backward takes."""
     T, E, dev = _first(logits, "logits", torch.float32)
     if not isinstance(topk_expert, torch.Tensor) or topk_expert.dim() != 2:
         raise MoEError("topk_expert must be a matrix")
@@ -933,13 +934,13 @@ def moe_balance_fwd(logits, topk_expert, mask=None, balance_coef: float = 0.01, 
     _arg(topk_expert, "topk_expert", torch.int32, (T, k), dev)
     _mask_arg(mask, T, dev)
     losses = torch.empty(3, dtype=torch.float32, device=dev)
-    counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    tokens = torch.empty(1, dtype=torch.int32, device=dev)
     mean_prob = torch.empty(E, dtype=torch.float32, device=dev)
     ws = _workspace(lib().moe_balance_workspace_bytes(E), dev)
     _call("moe_balance_fwd", dev, _ptr(logits), T, E, k, _ptr(topk_expert), _ptr(mask), balance_coef,
-          z_coef, _ptr(losses), _ptr(counts), _ptr(mean_prob), _ptr(ws), ws.numel())
-    return losses[0], {"counts": counts[:E], "tokens": counts[E:], "mean_prob": mean_prob,
-                       "balance": losses[1], "z": losses[2], "all_counts": counts, "k": k,
+          z_coef, _ptr(losses), _ptr(counts), _ptr(tokens), _ptr(mean_prob), _ptr(ws), ws.numel())
+    return losses[0], {"counts": counts, "tokens": tokens, "mean_prob": mean_prob, "losses": losses, "k": k,
                        "coefs": (balance_coef, z_coef)}
 
 
@@ -949,8 +950,9 @@ def moe_balance_bwd(logits, saved: dict, mask=None, dloss=None, dlogits=None, ou
     dlogits: a gradient of the logits that is added, such as moe_route_bwd's.
     out: where the result goes (may be dlogits itself)."""
     T, E, dev = _first(logits, "logits", torch.float32)
-    counts = saved.get("all_counts")
-    _arg(counts, "saved all_counts", torch.int32, (E + 1,), dev)
+    counts, tokens = saved.get("counts"), saved.get("tokens")
+    _arg(counts, "saved counts", torch.int32, (E,), dev)
+    _arg(tokens, "saved tokens", torch.int32, (1,), dev)
     _mask_arg(mask, T, dev)
     if dloss is not None:
         if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
@@ -963,7 +965,7 @@ def moe_balance_bwd(logits, saved: dict, mask=None, dloss=None, dlogits=None, ou
     else:
         _arg(out, "out", torch.float32, (T, E), dev)
     _call("moe_balance_bwd", dev, _ptr(logits), T, E, saved["k"], _ptr(mask), *saved["coefs"], _ptr(counts),
-          _ptr(dloss), _ptr(dlogits), _ptr(out))
+          _ptr(tokens), _ptr(dloss), _ptr(dlogits), _ptr(out))
     return out
 
 
@@ -992,8 +994,8 @@ def _table(t, name: str, dtype, shape, device):
         if shape is None:
             shape = tuple(t.shape[1:])
         _arg(t, name, dtype, (t.shape[0], *shape), device)
-        E, step, base = t.shape[0], t[0].numel() * t.element_size(), t.data_ptr()
-        return (ctypes.c_void_p * E)(*range(base, base + E * step, step) if step else [base] * E), E, shape
+        E, step, base = t.shape[0], shape[0] * shape[1] * t.element_size(), t.data_ptr()
+        return array.array("Q", range(base, base + E * step, step) if step else [base] * E), E, shape
     if not isinstance(t, (list, tuple)) or not len(t) or not isinstance(t[0], torch.Tensor):
         raise MoEError(f"{name} must be a tensor [E, rows, columns] or a list of matrices")
     if shape is None:
@@ -1002,7 +1004,12 @@ def _table(t, name: str, dtype, shape, device):
         raise MoEError(f"{name} must hold matrices")
     for m in t:
         _arg(m, name, dtype, shape, device)
-    return _ptr_array(t), len(t), shape
+    return array.array("Q", [m.data_ptr() for m in t]), len(t), shape
+
+
+def _host(table) -> int:
+    """The address of a host table (None: 0)."""
+    return 0 if table is None else table.buffer_info()[0]
 
 
 def fp8_block_quantize_weights(w, transposed: bool = False) -> dict:
@@ -1020,8 +1027,7 @@ def fp8_block_quantize_weights(w, transposed: bool = False) -> dict:
          "codes_t": torch.empty((E, K, N), dtype=torch.uint8, device=dev) if transposed else None}
     tabs = [_table(q[n], n, q[n].dtype, tuple(q[n].shape[1:]), dev)[0] if q[n] is not None else None
             for n in ("codes", "scales", "codes_t")]
-    _call("fp8_block_quantize_weights", dev, E, N, K, ctypes.addressof(tab),
-          *[0 if t is None else ctypes.addressof(t) for t in tabs])
+    _call("fp8_block_quantize_weights", dev, E, N, K, _host(tab), *map(_host, tabs))
     return q
 
 
@@ -1071,7 +1077,7 @@ def grouped_linear_block_fwd(x, split_sizes, w: dict, src_token=None):
     _arg(split_sizes, "split_sizes", torch.int32, (E,), dev)
     y = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
     _call("grouped_linear_block_fwd", dev, E, N, K, rows, _ptr(codes), _ptr(scales), x_rows,
-          _ptr(src_token), _ptr(split_sizes), ctypes.addressof(wc), ctypes.addressof(ws), _ptr(y))
+          _ptr(src_token), _ptr(split_sizes), _host(wc), _host(ws), _ptr(y))
     return y, {"codes": codes, "scales": scales}
 
 
@@ -1106,8 +1112,8 @@ def grouped_linear_block_bwd(dy, x: dict, split_sizes, w: dict, src_token=None, 
     else:
         _work_arg(workspace, dev)
     _call("grouped_linear_block_bwd", dev, E, N, K, rows, _ptr(dy), _ptr(codes), _ptr(scales), x_rows,
-          _ptr(src_token), _ptr(split_sizes), *[0 if t is None else ctypes.addressof(t) for t in (wc, ws)],
-          _ptr(dx), 0 if dwt is None else ctypes.addressof(dwt), _ptr(workspace), workspace.numel())
+          _ptr(src_token), _ptr(split_sizes), _host(wc), _host(ws), _ptr(dx), _host(dwt), _ptr(workspace),
+          workspace.numel())
     return dx, (dw if want_dw else None)
 
 

@@ -84,11 +84,11 @@ __device__ __forceinline__ void load_logits(const float* row, int e0, int E, flo
     }
 }
 
-// What the sums become: losses [total, balance, z], counts [E] and the number
-// of tokens behind them, mean probabilities.  The thread of expert e has its
+// What the sums become: losses [total, balance, z], counts [E], the number of
+// tokens, mean probabilities.  The thread of expert e has its
 // sums; one wave.
 __device__ void finish(const BalArgs& a, int e, double prob, int count, double z, int tokens,
-                       float* loss, int32_t* counts, float* mean_prob) {
+                       float* loss, int32_t* counts, int32_t* ntok, float* mean_prob) {
     const double n = tokens > 0 ? tokens : 1;
     const float pe = (float)(prob / n);
     double b = e < a.E ? (double)pe * (count / (n * a.k)) : 0.0;
@@ -99,7 +99,7 @@ __device__ void finish(const BalArgs& a, int e, double prob, int count, double z
         if (mean_prob) mean_prob[e] = pe;
     }
     if (e == 0) {
-        counts[a.E] = tokens;
+        *ntok = tokens;
         const double lb = (double)a.coef * a.E * b, lz = (double)a.zcoef * z / n;
         loss[0] = (float)(lb + lz);
         loss[1] = (float)lb;
@@ -112,7 +112,7 @@ __device__ void finish(const BalArgs& a, int e, double prob, int count, double z
 // one workgroup they are the sums, and it writes the outputs.
 template <int V, int G>
 __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(BalArgs a, float* part, float* loss,
-                                                               int32_t* counts, float* mean_prob) {
+                                                               int32_t* counts, int32_t* ntok, float* mean_prob) {
     constexpr int kSlots = kThreads / G;            // tokens at once
     __shared__ float sp[kThreads / 64][64], sz[kThreads / 64];
     __shared__ int sc[64], sn;
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(BalArgs a, float*
     const float p = tid < a.E ? (sp[0][tid] + sp[1][tid]) + (sp[2][tid] + sp[3][tid]) : 0.f;
     const float zz = (sz[0] + sz[1]) + (sz[2] + sz[3]);
     if (gridDim.x == 1) {
-        finish(a, tid, p, sc[tid], zz, sn, loss, counts, mean_prob);
+        finish(a, tid, p, sc[tid], zz, sn, loss, counts, ntok, mean_prob);
         return;
     }
     const int b = blockIdx.x;
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(BalArgs a, float*
 // The np partial sums added: thread (q, e) takes every 16th of expert e's.
 __global__ __launch_bounds__(1024) void balance_sum_kernel(BalArgs a, const float* __restrict__ part, int np,
                                                            float* loss, int32_t* counts,
-                                                           float* mean_prob) {
+                                                           int32_t* ntok, float* mean_prob) {
     __shared__ double sp[16][64], sz[16];
     __shared__ int sc[16][64], sn[16];
     const int e = threadIdx.x & 63, q = threadIdx.x >> 6;
@@ -216,16 +216,17 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(BalArgs a, const floa
         z += sz[w];
         n += sn[w];
     }
-    finish(a, e, p, c, z, n, loss, counts, mean_prob);
+    finish(a, e, p, c, z, n, loss, counts, ntok, mean_prob);
 }
 
 template <int V, int G>
 __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BalArgs a, const int32_t* __restrict__ counts,
+                                                               const int32_t* __restrict__ ntok,
                                                                const float* __restrict__ dloss,
                                                                const float* add, float* dlogits) {
     constexpr int kSlots = kThreads / G;
     const int e0 = (threadIdx.x % G) * V;
-    const int tokens = counts[a.E];
+    const int tokens = *ntok;
     const float n = tokens > 0 ? (float)tokens : 1.f;
     const float up = dloss ? dloss[0] : 1.f;
     const float cb = up * (a.coef * (float)a.E / n), cz = up * (2.f * a.zcoef / n);
@@ -299,7 +300,7 @@ size_t balance_workspace_bytes(int E) { return (size_t)kMaxParts * 2 * (E + 1) *
 
 hipError_t launch_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t* topk,
                               const uint8_t* mask, float coef, float zcoef, float* loss, int32_t* counts,
-                              float* mean_prob, void* ws, hipStream_t s) {
+                              int32_t* ntok, float* mean_prob, void* ws, hipStream_t s) {
     const BalArgs a{logits, topk, mask, T, E, k, coef, zcoef};
     unsigned np = 1;
     {
@@ -307,25 +308,25 @@ hipError_t launch_balance_fwd(const float* logits, int64_t T, int E, int k, cons
         with_lanes(E, [&](auto v, auto g) {
             np = passes(T, kThreads / decltype(g)::v, kMaxParts);
             balance_fwd_kernel<decltype(v)::v, decltype(g)::v>
-                <<<np, kThreads, 0, s>>>(a, (float*)ws, loss, counts, mean_prob);
+                <<<np, kThreads, 0, s>>>(a, (float*)ws, loss, counts, ntok, mean_prob);
         });
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || np == 1) return e;
     TraceScope ts("balance_sum", s);
-    balance_sum_kernel<<<1, 1024, 0, s>>>(a, (const float*)ws, (int)np, loss, counts, mean_prob);
+    balance_sum_kernel<<<1, 1024, 0, s>>>(a, (const float*)ws, (int)np, loss, counts, ntok, mean_prob);
     return hipGetLastError();
 }
 
 hipError_t launch_balance_bwd(const float* logits, int64_t T, int E, int k, const uint8_t* mask, float coef,
-                              float zcoef, const int32_t* counts, const float* dloss, const float* add,
-                              float* dlogits, hipStream_t s) {
+                              float zcoef, const int32_t* counts, const int32_t* ntok, const float* dloss,
+                              const float* add, float* dlogits, hipStream_t s) {
     if (T == 0) return hipSuccess;
     const BalArgs a{logits, nullptr, mask, T, E, k, coef, zcoef};
     TraceScope ts("balance_bwd", s);
     with_lanes(E, [&](auto v, auto g) {
         balance_bwd_kernel<decltype(v)::v, decltype(g)::v>
-            <<<passes(T, kThreads / decltype(g)::v, 2048), kThreads, 0, s>>>(a, counts, dloss, add, dlogits);
+            <<<passes(T, kThreads / decltype(g)::v, 2048), kThreads, 0, s>>>(a, counts, ntok, dloss, add, dlogits);
     });
     return hipGetLastError();
 }

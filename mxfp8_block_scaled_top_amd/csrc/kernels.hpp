@@ -138,10 +138,10 @@ hipError_t launch_rmsnorm_bwd(const bf16_t* dy, const void* h, bool s_f32, const
 size_t balance_workspace_bytes(int E);
 hipError_t launch_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t* topk,
                               const uint8_t* mask, float coef, float zcoef, float* loss, int32_t* counts,
-                              float* mean_prob, void* ws, hipStream_t s);
+                              int32_t* tokens, float* mean_prob, void* ws, hipStream_t s);
 hipError_t launch_balance_bwd(const float* logits, int64_t T, int E, int k, const uint8_t* mask, float coef,
-                              float zcoef, const int32_t* counts, const float* dloss, const float* add,
-                              float* dlogits, hipStream_t s);
+                              float zcoef, const int32_t* counts, const int32_t* tokens, const float* dloss,
+                              const float* add, float* dlogits, hipStream_t s);
 
 // ---- 8-bit blocks of 128 (block8.hpp): rows (scales [blocks][rows]), weights
 // (scales [N/128][K/128], transposed codes on request), rows to bf16

@@ -96,27 +96,27 @@ size_t moe_balance_workspace_bytes(int E) {
 
 int moe_balance_fwd(const float* logits, int64_t T, int E, int k, const int32_t* topk_expert,
                     const uint8_t* mask, float balance_coef, float z_coef, float* losses, int32_t* counts,
-                    float* mean_prob, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                    int32_t* tokens, float* mean_prob, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     const int st = check_balance(T, E, k, balance_coef, z_coef);
     if (st != MOE_OK) return st;
-    if (!losses || !counts || !workspace || (T > 0 && (!logits || !topk_expert))) return MOE_ERR_NULL;
+    if (!losses || !counts || !tokens || !workspace || (T > 0 && (!logits || !topk_expert))) return MOE_ERR_NULL;
     if (!aligned16(logits) || !aligned16(workspace)) return MOE_ERR_ALIGN;
     if (workspace_bytes < balance_workspace_bytes(E)) return MOE_ERR_WORKSPACE;
     if (!moe_device_supported()) return MOE_ERR_UNSUPPORTED;
     return hip_status(launch_balance_fwd(logits, T, E, k, topk_expert, mask, balance_coef, z_coef, losses,
-                                         counts, mean_prob, workspace, stream));
+                                         counts, tokens, mean_prob, workspace, stream));
 }
 
 int moe_balance_bwd(const float* logits, int64_t T, int E, int k, const uint8_t* mask, float balance_coef,
-                    float z_coef, const int32_t* counts, const float* dloss, const float* dlogits_in,
-                    float* dlogits, hipStream_t stream) {
+                    float z_coef, const int32_t* counts, const int32_t* tokens, const float* dloss,
+                    const float* dlogits_in, float* dlogits, hipStream_t stream) {
     const int st = check_balance(T, E, k, balance_coef, z_coef);
     if (st != MOE_OK) return st;
-    if (!counts || (T > 0 && (!logits || !dlogits))) return MOE_ERR_NULL;
+    if (!counts || !tokens || (T > 0 && (!logits || !dlogits))) return MOE_ERR_NULL;
     if (!aligned16(logits) || !aligned16(dlogits_in) || !aligned16(dlogits)) return MOE_ERR_ALIGN;
     if (!moe_device_supported()) return MOE_ERR_UNSUPPORTED;
-    return hip_status(launch_balance_bwd(logits, T, E, k, mask, balance_coef, z_coef, counts, dloss,
-                                         dlogits_in, dlogits, stream));
+    return hip_status(launch_balance_bwd(logits, T, E, k, mask, balance_coef, z_coef, counts, tokens,
+                                         dloss, dlogits_in, dlogits, stream));
 }
 
 size_t moe_layernorm_workspace_bytes(int64_t T, int H) {

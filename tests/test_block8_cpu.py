@@ -157,21 +157,21 @@ def test_rmsnorm_bwd_refuses(L, change, status):
     ({"T": -1}, SHAPE), ({"T": 1 << 30}, SHAPE), ({"E": 0}, SHAPE), ({"E": 65}, SHAPE), ({"k": 0}, SHAPE),
     ({"k": 9}, SHAPE), ({"coef": float("inf")}, ARG), ({"z": float("nan")}, ARG),
     ({"logits": None}, NULL), ({"topk": None}, NULL), ({"losses": None}, NULL), ({"counts": None}, NULL),
-    ({"ws": None}, NULL), ({"logits": MIS}, ALIGN), ({"ws": MIS}, ALIGN), ({"n": 16}, WS),
+    ({"tokens": None}, NULL), ({"ws": None}, NULL), ({"logits": MIS}, ALIGN), ({"ws": MIS}, ALIGN), ({"n": 16}, WS),
 ])
 def test_balance_fwd_refuses(L, change, status):
-    a = dict(logits=P, T=4, E=8, k=2, topk=P, mask=P, coef=0.01, z=0.0, losses=P, counts=P, prob=P, ws=P,
-             n=1 << 30) | change
+    a = dict(logits=P, T=4, E=8, k=2, topk=P, mask=P, coef=0.01, z=0.0, losses=P, counts=P, tokens=P, prob=P,
+             ws=P, n=1 << 30) | change
     assert L.moe_balance_fwd(*a.values(), None) == status
 
 
 @pytest.mark.parametrize("change,status", [
     ({"T": -1}, SHAPE), ({"E": 65}, SHAPE), ({"k": 9}, SHAPE), ({"coef": float("nan")}, ARG),
-    ({"logits": None}, NULL), ({"counts": None}, NULL), ({"out": None}, NULL),
+    ({"logits": None}, NULL), ({"counts": None}, NULL), ({"tokens": None}, NULL), ({"out": None}, NULL),
     ({"logits": MIS}, ALIGN), ({"add": MIS}, ALIGN), ({"out": MIS}, ALIGN),
 ])
 def test_balance_bwd_refuses(L, change, status):
-    a = dict(logits=P, T=4, E=8, k=2, mask=P, coef=0.01, z=0.0, counts=P, dloss=P, add=P, out=P) | change
+    a = dict(logits=P, T=4, E=8, k=2, mask=P, coef=0.01, z=0.0, counts=P, tokens=P, dloss=P, add=P, out=P) | change
     assert L.moe_balance_bwd(*a.values(), None) == status
 
 

@@ -55,8 +55,8 @@ def _check(x, topk, mask, d0, coef, z, dloss=None):
     eb = abs(coef) * E * (r["f"] * (eP + U * r["mean_prob"])).sum() + 4 * U * r["balance"].abs()
     l2 = r["lse"] * r["lse"]
     ez = abs(z) / n * (2.1 * r["lse"].abs() * el + (chain + 3) * U * l2).sum() + 3 * U * r["z"].abs()
-    _within(saved["balance"], r["balance"], eb + 1e-37, "balance")
-    _within(saved["z"], r["z"], ez + 1e-37, "z")
+    _within(saved["losses"][1], r["balance"], eb + 1e-37, "balance")
+    _within(saved["losses"][2], r["z"], ez + 1e-37, "z")
     _within(loss, r["loss"], eb + ez + U * r["loss"].abs() + 1e-37, "loss")
     up = abs(dloss) if dloss is not None else 1.0
     s = (r["p"] * r["f"]).sum(1, keepdim=True)
@@ -156,7 +156,7 @@ def test_in_place_guard_rows_and_graph():
 
     def step():
         loss, s = moe.moe_balance_fwd(X, K, M, 0.1, 0.01)
-        return [loss, s["all_counts"], s["mean_prob"], moe.moe_balance_bwd(X, s, M)]
+        return [loss, s["counts"], s["tokens"], s["mean_prob"], moe.moe_balance_bwd(X, s, M)]
 
     graph_check(step, lambda: moe.moe_balance_fwd(d0.cuda(), K))
 
