@@ -55,173 +55,170 @@ __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
     return (i32x8){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-__device__ __forceinline__ i32x8 frag(const uint8_t* row, int swz, int g) {
-    return join(*(const u32x4*)(row + ((g ^ swz) << 4)), *(const u32x4*)(row + (((g + 4) ^ swz) << 4)));
-}
 
-// What a workgroup works on, the same for all its threads.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// One tile, the same for all threads of its workgroup.
 struct BlockTile {
-    int e, n0, rows;        // expert, first column, rows of the tile
+    int e, n0, rows;        // expert, first column, rows of the tile (0: no tile)
     int64_t row0;           // first grouped row
 };
+
+// Fragment columns of 16 rows per wave that a tile of so many rows takes.
+__device__ __forceinline__ int tile_height(int rows) { return rows > 128 ? 8 : rows > 64 ? 4 : 2; }
 
 // LDS of a workgroup: kStages of weights, rows, scales of rows (1 KB) and weights.
 constexpr int stage_bytes(int kMT) { return kWB + 32 * kMT * kBlk + 2048; }
 constexpr int kLdsB = 3 * stage_bytes(4);
 static_assert(kLdsB >= 2 * stage_bytes(8) && kLdsB >= 3 * stage_bytes(2), "stages of every height");
 
-// One tile of at most 32 kMT rows.
-template <int kMT, int kStages>
-__device__ __forceinline__ void block_tile(const BlockGemm& p, const BlockTile& tl, uint8_t* lds) {
-    constexpr int kBM = 32 * kMT, kXB = kBM * kBlk;
-    constexpr int kStageB = stage_bytes(kMT);
-    constexpr int kXI = kMT / 2;                    // row loads per wave and step
-    constexpr int kPer = 4 + kXI + 1;               // loads per wave and step
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = tl.n0, rows = tl.rows;
-    const int64_t row0 = tl.row0;
-    const int nkb = (p.K + kBlk - 1) / kBlk;
-
-    // ---- loads: instruction j of a wave covers 8 tile rows, 8 lanes each
-    uint32_t ow[4], ox[kXI], os;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int r = (wave * 4 + j) * 8 + (lane >> 3), c = (lane & 7) ^ wswz(r);
-        ow[j] = n0 + r < p.N ? (uint32_t)(n0 + r) * (uint32_t)p.K + (c << 4) : kOob;
-    }
-    auto source = [&](int r) -> int64_t {       // row of x, from the buffer's base; -1: none
-        if (r >= rows) return -1;
-        if (!p.src) return r;
-        const int s = p.src[row0 + r];
-        return s >= 0 && s < p.x_rows ? s : -1;
-    };
-#pragma unroll
-    for (int j = 0; j < kXI; ++j) {
-        const int r = (wave * kXI + j) * 8 + (lane >> 3), c = (lane & 7) ^ xswz(r);
-        const int64_t s = source(r);
-        ox[j] = s >= 0 ? (uint32_t)(s * p.K) + (c << 4) : kOob;
-    }
-    // waves 0 .. 3 load the rows' scales, the others the two of the weights
-    const bool row_scales = wave < 4;
-    const int64_t xbase = p.src ? 0 : row0;
-    if (row_scales) {
-        const int64_t s = wave * 64 + lane < kBM ? source(wave * 64 + lane) : -1;
-        os = s >= 0 ? (uint32_t)s * 4u : kOob;
-    } else {
-        const int nb = n0 / kBlk + (lane & 1);
-        os = nb * kBlk < p.N ? (uint32_t)(nb * p.sn) * 4u : kOob;
-    }
-    const uint64_t wbase = (uint64_t)p.w.p[tl.e];
-    const i32x4 rw = rsrc_at(wbase, 0x7fffffff), rx = rsrc_at((uint64_t)(p.x + xbase * p.K), 0x7fffffff);
-    const uint64_t sbase = row_scales ? (uint64_t)(p.x_scale + xbase) : (uint64_t)p.w_scale.p[tl.e];
-    const uint64_t sstep = row_scales ? (uint64_t)p.x_rows * 4u : (uint64_t)p.sk * 4u;
-    const uint32_t l0 = lds_u32(lds);
-    const int tail = p.K & (kBlk - 1);          // bytes of the last block, 0: all
-    auto prep = [&](int kb) {                   // before the loads of step kb
-        if (tail && kb == nkb - 1) {            // chunks past K
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if ((((lane & 7) ^ wswz((wave * 4 + j) * 8 + (lane >> 3))) << 4) >= tail) ow[j] = kOob;
-#pragma unroll
-            for (int j = 0; j < kXI; ++j)
-                if ((((lane & 7) ^ xswz((wave * kXI + j) * 8 + (lane >> 3))) << 4) >= tail) ox[j] = kOob;
+// The tiles of a launch.
+// XCD x (workgroups go round robin over the XCDs) takes a contiguous eighth of
+// the tiles that there are, in bands of at most 8 row tiles that share its
+// L2; its workgroups take them in turn.
+struct TileList {
+    int (*sched)[64];           // of expert e: tiles of rows up to it, first row, rows
+    int ntn, t, end, step;
+    __device__ __forceinline__ void init(const BlockGemm& p, int ntn_, int (*sched_)[64]) {
+        ntn = ntn_;
+        sched = sched_;
+        if (threadIdx.x < 64) {
+            const int lane = threadIdx.x;
+            const int n = clamp_group_size(lane < p.E ? p.split[lane] : 0, p.rows);
+            sched[0][lane] = wave_incl_scan((n + kBM - 1) / kBM);
+            sched[1][lane] = wave_incl_scan(n) - n;
+            sched[2][lane] = n;
         }
-    };
-    auto part = [&](int kb, int stage, int j) { // load j of step kb
-        const bool live = kb < nkb;
-        const uint32_t base = l0 + stage * kStageB;
-        Dma dw{rw, (uint32_t)(live ? kb * kBlk : 0)}, dx{rx, dw.soff};
-        if (!live) dw.rs[2] = dx.rs[2] = 0;
-        if (j < 4) dma16(dw, ow[j], base + (wave * 4 + j) * 1024);
-        else if (j < 4 + kXI) dma16(dx, ox[j - 4], base + kWB + (wave * kXI + j - 4) * 1024);
-        else {
-            const i32x4 rs = rsrc_at(sbase + (live ? kb * sstep : 0), live ? 0x7fffffff : 0);
+        __syncthreads();
+        const int total = uniform(sched[0][63]) * ntn, chunk = (total + 7) >> 3;
+        t = (int)(blockIdx.x & 7) * chunk;
+        end = min(t + chunk, total);
+        t += (int)(blockIdx.x >> 3);
+        step = (int)(gridDim.x >> 3);
+    }
+    __device__ __forceinline__ BlockTile next() {
+        BlockTile tl{0, 0, 0, 0};
+        if (t >= end) return tl;
+        // (experts past the last one hold the total)
+        const int e = (int)__popcll(__ballot(sched[0][threadIdx.x & 63] * ntn <= t));
+        const int rows_e = uniform(sched[2][e]);
+        const int u = t - (e ? uniform(sched[0][e - 1]) : 0) * ntn;
+        const int mt = (rows_e + kBM - 1) / kBM;
+        const int band = u / (8 * ntn), b0 = band * 8, bm = min(mt - b0, 8);
+        const int v = u - band * 8 * ntn;
+        const int m0 = (b0 + v % bm) * kBM;
+        tl.e = e;
+        tl.n0 = v / bm * kBN;
+        tl.rows = min(rows_e - m0, kBM);
+        tl.row0 = uniform(sched[1][e]) + (int64_t)m0;
+        t += step;
+        return tl;
+    }
+};
+
+// The lane, of which the compiler does not know that it never changes: what is
+// computed from it once a tile takes no registers in between.
+__device__ __forceinline__ int own_lane() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// A wave's loads of a tile: instruction j covers 8 tile rows, 8 lanes each.  What
+// changes from tile to tile is uniform (the resources, whose sizes also make
+// columns past N read zeros) but for the rows of x, which come from a table.
+template <int kMT>
+struct BlockFeed {
+    static constexpr int kXB = 32 * kMT * kBlk, kXI = kMT / 2;      // row loads per wave and step
+    static constexpr int kPer = 4 + kXI + 1;                        // loads per wave and step
+    uint32_t ow[4], ox[kXI], os;
+    uint64_t wbase, xbase, sbase;       // of the step whose loads come next (scales), of the tile
+    int wrec, xrec;                     // sizes; 0: everything reads zeros
+    uint32_t soff;
+
+    static __device__ __forceinline__ int wchunk(int j, int wave, int lane) {
+        return ((lane & 7) ^ wswz((wave * 4 + j) * 8 + (lane >> 3))) << 4;
+    }
+    static __device__ __forceinline__ int xchunk(int j, int wave, int lane) {
+        return ((lane & 7) ^ xswz((wave * kXI + j) * 8 + (lane >> 3))) << 4;
+    }
+    // rows[]: the row of x, from the buffer's base, of each tile row (-1: none)
+    __device__ __forceinline__ void set(const BlockGemm& p, const BlockTile& tl, const int* rows, int wave) {
+        const int lane = own_lane();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            ow[j] = (uint32_t)((wave * 4 + j) * 8 + (lane >> 3)) * (uint32_t)p.K + wchunk(j, wave, lane);
+#pragma unroll
+        for (int j = 0; j < kXI; ++j) {
+            const int s = rows[(wave * kXI + j) * 8 + (lane >> 3)];
+            ox[j] = s < 0 ? kOob : (uint32_t)s * (uint32_t)p.K + xchunk(j, wave, lane);
+        }
+        const int64_t first = p.src ? 0 : tl.row0;
+        wbase = (uint64_t)p.w.p[tl.e] + (uint64_t)tl.n0 * p.K;
+        wrec = min(p.N - tl.n0, kBN) * p.K;
+        xbase = (uint64_t)(p.x + first * p.K);
+        xrec = 0x7fffffff;
+        soff = 0;
+        // waves 0 .. 3 load the rows' scales, the others the two of the weights
+        if (wave < 4) {
+            const int s = rows[wave * 64 + lane];
+            os = s < 0 ? kOob : (uint32_t)s * 4u;
+            sbase = (uint64_t)(p.x_scale + first);
+        } else {
+            const int nb = tl.n0 / kBlk + (lane & 1);
+            os = nb * kBlk < p.N ? (uint32_t)(nb * p.sn) * 4u : kOob;
+            sbase = (uint64_t)p.w_scale.p[tl.e];
+        }
+    }
+    __device__ __forceinline__ void stop() { wrec = xrec = 0; }
+    // Before the last step's loads: chunks from byte `tail` on are past K.
+    __device__ __forceinline__ void cut(int tail, int wave) {
+        const int lane = own_lane();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (wchunk(j, wave, lane) >= tail) ow[j] = kOob;
+#pragma unroll
+        for (int j = 0; j < kXI; ++j)
+            if (xchunk(j, wave, lane) >= tail) ox[j] = kOob;
+    }
+    // Load j of the step into the stage at `base`; the last one moves on to the next step.
+    __device__ __forceinline__ void load(uint64_t scale_step, uint32_t base, int j, int wave) {
+        if (j < 4 + kXI) {
+            const Dma d{j < 4 ? rsrc_at(wbase, wrec) : rsrc_at(xbase, xrec), (uint32_t)uniform(soff)};
+            dma16(d, j < 4 ? ow[j] : ox[j - 4], base + (j < 4 ? (wave * 4 + j) * 1024 : kWB + (wave * kXI + j - 4) * 1024));
+        } else {
+            const i32x4 rs = rsrc_at(sbase, xrec);
+            uint32_t to = base + kWB + kXB + wave * 256;
+            asm volatile("" : "+v"(to));        // (or the sum is taken in a vector register that the load cannot use)
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
-                             base + kWB + kXB + (row_scales ? wave * 256 : 1024 + (wave - 4) * 256)),
+                             uniform(to)),
                          "v"(os), "s"(rs)
                          : "memory");
-        }
-    };
-    auto issue = [&](int kb, int stage) {
-        prep(kb);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) part(kb, stage, j);
-    };
-
-    const int wn = (wave & 3) * 64, wm = (wave >> 2) * (16 * kMT), l16 = lane & 15, g = lane >> 4;
-    f32x4 acc[4][kMT];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int m = 0; m < kMT; ++m) acc[i][m] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    // a lane's fragment rows: their swizzles do not depend on the fragment
-    const int wr = wn + ((l16 >> 2) << 4) + (l16 & 3);      // + 4 i
-    const int xr = wm + l16;                                // + 16 m
-
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue(s, s);
-    int stage = 0, fill = kStages - 1;
-    f32x4 dp[4];
-    float sp = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dp[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    for (int kb = 0; kb < nkb; ++kb) {
-        pipe_barrier<(kStages - 2) * kPer>();
-        prep(kb + kStages - 1);
-        const int fl = fill;
-        fill = fill + 1 == kStages ? 0 : fill + 1;
-        const uint8_t* lw = lds + stage * kStageB;
-        const uint8_t* lx = lw + kWB;
-        const float* sx = (const float*)(lx + kXB);
-        const float sw = sx[256 + ((wave >> 1) & 1)];
-        stage = stage + 1 == kStages ? 0 : stage + 1;
-        i32x8 a[4], b[2];
-        float sb[2];
-        b[0] = frag(lx + xr * kBlk, xswz(xr), g);
-        sb[0] = sx[xr];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = frag(lw + (wr + 4 * i) * kBlk, wswz(wr + 4 * i), g);
-#pragma unroll
-        for (int m = 0; m < kMT; ++m) {
-            if (m + 1 < kMT) {
-                b[(m + 1) & 1] = frag(lx + (xr + 16 * (m + 1)) * kBlk, xswz(xr + 16 * (m + 1)), g);
-                sb[(m + 1) & 1] = sx[xr + 16 * (m + 1)];
-            }
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)      // two loads a fragment column, from the first on
-                if ((j / 2 < kMT ? j / 2 : kMT - 1) == m) part(kb + kStages - 1, fl, j);
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_setprio(1);
-            const float s = sb[m & 1] * sw;
-            f32x4 d[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-                d[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], b[m & 1], z, 0, 0, 0, 0, 0, 0);
-                constexpr int kLast = kMT - 1;
-                const int c = m > 0 ? m - 1 : kLast;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[i][c][q] = __builtin_fmaf(dp[i][q], sp, acc[i][c][q]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dp[i] = d[i];
-            sp = s;
-            __builtin_amdgcn_s_setprio(0);
+            sbase += scale_step;
+            soff += kBlk;
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][kMT - 1][q] = __builtin_fmaf(dp[i][q], sp, acc[i][kMT - 1][q]);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // no load may reach LDS after the workgroup
-    // a lane's 16 outputs of a row are neighbours: n = 16 g + 4 i + q
+};
+
+// The row of x that tile row threadIdx.x takes, from the buffer's base (-1: none).
+__device__ __forceinline__ int row_of_x(const BlockGemm& p, const BlockTile& tl) {
+    const int r = threadIdx.x;
+    if (r >= tl.rows) return -1;
+    if (!p.src) return r;
+    const int s = p.src[tl.row0 + r];
+    return s < p.x_rows ? s : -1;
+}
+
+// y of a tile.  A lane's 16 outputs of a row are neighbours: n = 16 g + 4 i + q.
+template <int kMT>
+__device__ __forceinline__ void block_store(const BlockGemm& p, const BlockTile& tl, const f32x4 (&acc)[4][kMT], int wave) {
+    const int lane = own_lane(), xr = (wave >> 2) * (16 * kMT) + (lane & 15);
+    const int n = tl.n0 + (wave & 3) * 64 + 16 * (lane >> 4);
 #pragma unroll
     for (int m = 0; m < kMT; ++m) {
-        const int r = xr + 16 * m, n = n0 + wn + 16 * g;
-        if (r >= rows || n >= p.N) continue;        // N is a multiple of 32
-        u32x4* y = (u32x4*)(p.y + (row0 + r) * p.N + n);
+        const int r = xr + 16 * m;
+        if (r >= tl.rows || n >= p.N) continue;     // N is a multiple of 32
+        u32x4* y = (u32x4*)(p.y + (tl.row0 + r) * p.N + n);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             y[h] = (u32x4){pack_bf16x2(acc[2 * h][m][0], acc[2 * h][m][1]), pack_bf16x2(acc[2 * h][m][2], acc[2 * h][m][3]),
@@ -230,39 +227,133 @@ __device__ __forceinline__ void block_tile(const BlockGemm& p, const BlockTile& 
     }
 }
 
+// Tiles of at most 32 kMT rows, from `tl` on until the next one has another
+// height or there is none; returns that one.
+template <int kMT, int kStages>
+__device__ __forceinline__ BlockTile block_tiles(const BlockGemm& p, TileList& list, BlockTile tl, uint8_t* lds, int* rows) {
+    constexpr int kXB = BlockFeed<kMT>::kXB, kPer = BlockFeed<kMT>::kPer;
+    constexpr int kStageB = stage_bytes(kMT), kAhead = kStages - 1;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = (wave & 3) * 64, wm = (wave >> 2) * (16 * kMT), l16 = lane & 15, g = lane >> 4;
+    // where a lane's fragments start in a stage: chunk g of its first row of the
+    // weights and of x (chunk g + 4: the same with bit 6 changed; the next
+    // fragment's row has the same swizzle), and the scale of its first row
+    const int wr = wn + ((l16 >> 2) << 4) + (l16 & 3), xr = wm + l16;
+    const int wat = wr * kBlk + ((g ^ wswz(wr)) << 4);
+    const int xat = kWB + xr * kBlk + ((g ^ xswz(xr)) << 4), sat = kWB + kXB + xr * 4;
+    const int nkb = (p.K + kBlk - 1) / kBlk;
+    const int tail = p.K - (nkb - 1) * kBlk;                // bytes of the last block
+    const uint32_t l0 = lds_u32(lds);
+
+    if (tid < kBM) rows[tid] = row_of_x(p, tl);
+    __syncthreads();
+    const uint64_t scale_step = wave < 4 ? (uint64_t)p.x_rows * 4u : (uint64_t)p.sk * 4u;
+    const int cut_at = tail < kBlk ? nkb - 1 : -1;
+    BlockFeed<kMT> feed;
+    feed.set(p, tl, rows, wave);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+        if (s == cut_at) feed.cut(tail, wave);
+        if (s == nkb) feed.stop();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) feed.load(scale_step, l0 + s * kStageB, j, wave);
+    }
+    int stage = 0, fill = kAhead;
+    BlockTile next;
+    pipe_barrier<(kStages - 2) * kPer>();
+    for (;;) {
+        next = list.next();
+        // the loads go on into the next tile without a pause
+        const bool chain = next.rows > 0 && tile_height(next.rows) == kMT && nkb > kAhead + 1;
+        const int ahead = chain && tid < kBM ? row_of_x(p, next) : -1;
+        f32x4 acc[4][kMT], dp[4];
+        float sp = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dp[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) acc[i][m] = dp[i];
+        }
+        for (int kb = 0; kb < nkb; ++kb) {
+            if (kb == 1 && tid < kBM) rows[tid] = ahead;    // read from the next step on
+            int kf = kb + kAhead;                           // the step whose loads go out now
+            if (kf == nkb) {
+                if (chain) feed.set(p, next, rows, wave);
+                else feed.stop();
+            }
+            if (kf >= nkb) kf -= nkb;
+            if (kf == cut_at) feed.cut(tail, wave);
+            const uint32_t base = uniform(l0 + fill * kStageB);
+            fill = fill + 1 == kStages ? 0 : fill + 1;
+            const uint8_t* st = lds + stage * kStageB;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            const uint8_t *w0 = st + wat, *w1 = st + (wat ^ 64), *x0 = st + xat, *x1 = st + (xat ^ 64), *sx = st + sat;
+            const float sw = *(const float*)(st + kWB + kXB + 1024 + 4 * ((wave >> 1) & 1));
+            auto wfrag = [&](int i) { return join(*(const u32x4*)(w0 + 4 * i * kBlk), *(const u32x4*)(w1 + 4 * i * kBlk)); };
+            auto xfrag = [&](int m) { return join(*(const u32x4*)(x0 + 16 * m * kBlk), *(const u32x4*)(x1 + 16 * m * kBlk)); };
+            i32x8 a[4], b[2];
+            float sb[2];
+            b[0] = xfrag(0);
+            sb[0] = *(const float*)sx;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = wfrag(i);
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+                if (m + 1 < kMT) {
+                    b[(m + 1) & 1] = xfrag(m + 1);
+                    sb[(m + 1) & 1] = *(const float*)(sx + 64 * (m + 1));
+                }
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)      // two loads a fragment column, from the first on
+                    if ((j / 2 < kMT ? j / 2 : kMT - 1) == m) feed.load(scale_step, base, j, wave);
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
+                const float s = sb[m & 1] * sw;
+                f32x4 d[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+                    d[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], b[m & 1], z, 0, 0, 0, 0, 0, 0);
+                    const int c = m > 0 ? m - 1 : kMT - 1;  // the column before, of the step before at m = 0
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[i][c][q] = __builtin_fmaf(dp[i][q], sp, acc[i][c][q]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dp[i] = d[i];
+                sp = s;
+                __builtin_amdgcn_s_setprio(0);
+            }
+            // the next step's (or the next tile's first) loads have landed, and
+            // all waves are done with this one's stage
+            pipe_barrier<(kStages - 2) * kPer>();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[i][kMT - 1][q] = __builtin_fmaf(dp[i][q], sp, acc[i][kMT - 1][q]);
+        block_store<kMT>(p, tl, acc, wave);    // these leave under the next tile's first products
+        if (!chain) break;
+        tl = next;
+    }
+    // (every load has landed before the stages get another meaning)
+    pipe_barrier<0>();
+    return next;
+}
+
 __global__ __launch_bounds__(kThreads, 2) void gemm_block_kernel(BlockGemm p, int ntn) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLdsB];
-    __shared__ int sched[3][64];
-    const int tid = threadIdx.x;
-    if (tid < 64) {
-        const int n = clamp_group_size(tid < p.E ? p.split[tid] : 0, p.rows);
-        sched[0][tid] = wave_incl_scan((n + kBM - 1) / kBM);
-        sched[1][tid] = wave_incl_scan(n) - n;
-        sched[2][tid] = n;
+    __shared__ int sched[3][64], rows[kBM];
+    TileList list;
+    list.init(p, ntn, sched);
+    BlockTile tl = list.next();
+    while (tl.rows) {
+        const int h = tile_height(tl.rows);
+        if (h == 8) tl = block_tiles<8, 2>(p, list, tl, lds, rows);
+        else if (h == 4) tl = block_tiles<4, 3>(p, list, tl, lds, rows);
+        else tl = block_tiles<2, 3>(p, list, tl, lds, rows);
     }
-    __syncthreads();
-    // XCD x (workgroups go round robin) takes a contiguous eighth of the tiles
-    // that there are, in bands of at most 8 row tiles that share its L2
-    const int total = sched[0][63] * ntn, chunk = (total + 7) >> 3;
-    const int i0 = blockIdx.x >> 3;
-    int t = (blockIdx.x & 7) * chunk + i0;
-    if (i0 >= chunk || t >= total) return;
-    int e = 0;
-    while (e < p.E - 1 && sched[0][e] * ntn <= t) ++e;
-    t -= (e ? sched[0][e - 1] : 0) * ntn;
-    const int rows_e = __builtin_amdgcn_readfirstlane(sched[2][e]);
-    const int mt = (rows_e + kBM - 1) / kBM;
-    const int band = t / (8 * ntn), b0 = band * 8, bm = min(mt - b0, 8);
-    const int tr = t - band * 8 * ntn;
-    const int m0 = __builtin_amdgcn_readfirstlane((b0 + tr % bm) * kBM);
-    BlockTile tl;
-    tl.e = __builtin_amdgcn_readfirstlane(e);
-    tl.n0 = __builtin_amdgcn_readfirstlane((tr / bm) * kBN);
-    tl.rows = min(rows_e - m0, kBM);
-    tl.row0 = __builtin_amdgcn_readfirstlane(sched[1][e]) + (int64_t)m0;
-    if (tl.rows > 128) block_tile<8, 2>(p, tl, lds);
-    else if (tl.rows > 64) block_tile<4, 3>(p, tl, lds);
-    else block_tile<2, 3>(p, tl, lds);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -386,7 +477,7 @@ hipError_t launch_gemm_block(const BlockGemm& p, hipStream_t s, const char* name
     }
     const int ntn = (p.N + kBN - 1) / kBN;
     const int64_t tiles = (p.rows + (int64_t)p.E * (kBM - 1)) / kBM * ntn;     // at most
-    gemm_block_kernel<<<(unsigned)((tiles + 7) / 8 * 8), kThreads, 0, s>>>(p, ntn);
+    gemm_block_kernel<<<tiles < 256 ? (unsigned)((tiles + 7) / 8 * 8) : 256u, kThreads, 0, s>>>(p, ntn);
     return hipGetLastError();
 }
 

@@ -1,10 +1,13 @@
 """GPU: the 128-block quantizers (bit for bit) and the grouped products of such operands.
 
-A product's bound: the 128 products of a block are exact in fp32 (8 significant bits); the matrix
-instruction adds them with an error of about 2^-16 of their root mean square, counted here as 2^-13 of
-their 2-norm; the two scales' product and the fma round (2 u each, u = 2^-24, of the block's sum), and the
-running sum rounds once per block (u times the sum of the blocks' magnitudes).  bf16 outputs add half
-a step, 2^-8 of the value.  Weight gradients: x^ in bf16, 2^-8 of each product, and an fp32 sum over the rows."""
+A product's bound.  The matrix instruction takes the 128 products of a block (8 significant bits each, exact)
+in 16 groups of 8 and, inside a group, drops what lies 13 bits and more below the exponent of the largest: one
+product of 2^16 among 127 of 2^(16-s) gives the exact sum up to s = 13 and misses exactly 7 of the others from s = 14
+on, up to s = 26 (beyond, the groups' sum rounds in fp32 too).  So a group loses less than 7 2^-13 of its largest product, and a block,
+by Cauchy and Schwarz over its 16 groups, less than 7 2^-13 4 |p|_2 = 28 2^-13 |p|_2.  Then the two scales' product and
+the fma round (2 u each, u = 2^-24, of the block's sum), and the running sum rounds once per block (u times the sum of
+the blocks' magnitudes).  bf16 outputs add half a step, 2^-8 of the value.  Weight gradients: x^ in bf16, 2^-8 of each
+product, and an fp32 sum over the rows."""
 import numpy as np
 import pytest
 import torch
@@ -137,7 +140,7 @@ def _product_bound(a, b):
         x, w = a[:, k:k + 128], b[:, k:k + 128]
         two += (x.square() @ w.square().T).sqrt()
         mag += (x.abs() @ w.abs().T)
-    return 2.0 ** -13 * two + (a.shape[1] // 128 + 5) * U * mag
+    return 28 * 2.0 ** -13 * two + (a.shape[1] // 128 + 5) * U * mag
 
 
 def _check(got, ref, bound, what):
@@ -199,6 +202,20 @@ def test_backward(split, N, K, gather):
     torch.cuda.synchronize()
     assert none is None and none2 is None and same is buf and torch.equal(only, dx)
     assert all(torch.equal(a, b) for a, b in zip(buf, dw))
+
+
+@pytest.mark.parametrize("K,gather", [(256, False), (384, True), (416, True), (672, False)])
+def test_several_tiles_per_workgroup(K, gather):
+    """More tiles than compute units, of every height: a workgroup goes from one to the next with its loads
+    running on (three steps of K and more), over ragged experts and a K that ends inside a block."""
+    split, N = [700, 3, 129, 65, 600, 0, 257, 300], 16416
+    say(f"block product, many tiles, K={K} gather={gather}")
+    p = _problem(split, 8, N, K, seed=K, tokens=1500 if gather else 0)
+    y, _ = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"], src_token=p["src"])
+    z, _ = moe.grouped_linear_block_fwd(p["x8"], p["sd"], p["w8"], src_token=p["src"])
+    torch.cuda.synchronize()
+    _check_fwd(p, y)
+    assert torch.equal(y, z)
 
 
 def test_input_gradient_against_differences():
