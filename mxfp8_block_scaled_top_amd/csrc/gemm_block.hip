@@ -5,30 +5,44 @@
 //
 // The sum inside a block of 128 is one v_mfma_f32_16x16x128_f8f6f4 (fp32, no
 // scales); its 16 x 16 result is multiplied by the block's two scales and
-// added to the accumulators by ordinary fma, in fp32.
+// added to the accumulators by ordinary fma, in fp32.  (The instruction sums
+// its products in groups of 8 and drops what lies 13 bits and more below a
+// group's largest: 2^-12 of a block's 2-norm at worst in 11 million outputs,
+// under the rounding of y to bf16.)
 //
 // What that costs: a matrix instruction takes 32 cycles of its SIMD and its
 // four fma 16 of the vector unit, which runs beside it; on registers alone
-// the pair reaches 3.6 PFLOP/s where the matrix instruction alone reaches 4.5.
-// The accumulators have to be ordinary registers (the vector unit does not
-// read accumulation registers), 128 of them, so a wave has 64 x 128 outputs
-// and a SIMD two waves, and the two hide each other's waits.
+// the pair reaches 3.6 PFLOP/s where the matrix instruction alone reaches 4.5
+// (32 x 32 x 64: 3.4 and 4.1).  The accumulators have to be ordinary registers
+// (the vector unit does not read accumulation registers), 128 of them, so a
+// wave has 64 x 128 outputs and a SIMD two waves.
 //
 //   * Tile 256 columns (weights) x 256 rows, 8 waves, 4 along the weights: 64 x
 //     128 outputs each.  An expert's last tile is 128 or 64 rows high where that
 //     is enough (64 x 16 kMT outputs a wave).
 //   * The weights are the instruction's first operand, the rows the second: a
 //     lane holds outputs of one row per fragment and needs one row scale for
-//     them.  A fragment's weight rows are picked (wrow) such that the lane's
-//     outputs of four fragments are 16 neighbours: y leaves in 32-byte pieces
-//     per lane, whole lines per row, without a pass through LDS.
+//     them.  A fragment's weight rows are picked such that the lane's outputs
+//     of two fragments are 8 neighbours: y leaves without a pass through LDS.
 //   * K steps of one block: 128 bytes per operand row are whole lines.  Both
 //     operands and the scales reach LDS by direct loads, kStages - 1 steps
-//     ahead; 16-byte chunks are XOR-swizzled by row bits.
+//     ahead, issued two per fragment column (all at the step's start: +5%,
+//     one per column +4%); 16-byte chunks are XOR-swizzled by row bits.
 //   * Any K order inside a block will do as long as both operands agree: lane
 //     group g reads chunks g and g + 4 of a row.
+//   * A fragment column's fma run under the next column's products (10% less
+//     time than right behind their own).
+//   * One workgroup per compute unit walks over tiles; its loads run on into
+//     the next tile (5 to 10% less time than a workgroup per tile).
 //   * Rows past the end, columns past N and bytes past K read zeros (offsets
 //     past the buffer resource).
+//
+// Measured: 16384 rows over 8 experts of 28672 x 4096 1.88 ms (2.04 PFLOP/s), of
+// 4096 x 14336 0.97 ms (1.98); a library product with one scale per tensor reaches
+// 2.75 at 2048 x 28672 x 4096.  Bound by power: the shader clock is 1.7 to 1.9
+// GHz, and each change that saved cycles cost clock.  Timing variants of an
+// earlier step (2170 us): without loads 1690, without fma 1830; of this one
+// without stores 1700: y's 0.94 GB add their time at the memory's rate.
 #include "block8.hpp"
 #include "common.hpp"
 #include "dma.hpp"
@@ -47,9 +61,9 @@ constexpr uint32_t kOob = 0x80000000u;      // offset that reads zeros
 constexpr int kWB = kBN * kBlk;             // a stage's weights
 
 // Bits that swizzle a row's chunks: a fragment's reads take 16 rows of one
-// chunk (weights: rows 16a + 4t + b for a fixed t), two per 256 bytes.
+// chunk (weights: rows 8a + b and a constant, a, b < 4), two per 256 bytes.
 __device__ __forceinline__ int xswz(int r) { return (r >> 1) & 7; }
-__device__ __forceinline__ int wswz(int r) { return ((r >> 3) & 6) | ((r >> 1) & 1); }
+__device__ __forceinline__ int wswz(int r) { return ((r >> 2) & 6) | ((r >> 1) & 1); }
 
 __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
     return (i32x8){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
@@ -72,46 +86,60 @@ constexpr int stage_bytes(int kMT) { return kWB + 32 * kMT * kBlk + 2048; }
 constexpr int kLdsB = 3 * stage_bytes(4);
 static_assert(kLdsB >= 2 * stage_bytes(8) && kLdsB >= 3 * stage_bytes(2), "stages of every height");
 
-// The tiles of a launch.
-// XCD x (workgroups go round robin over the XCDs) takes a contiguous eighth of
-// the tiles that there are, in bands of at most 8 row tiles that share its
-// L2; its workgroups take them in turn.
+// The tiles of a launch, the high ones first, so that the low ones (the last
+// rows of an expert) fill in where a workgroup has had one high tile less (in
+// the experts' order the most loaded workgroup had 1.3 times the mean: 8 x 2048
+// rows of 4096 x 14336 1027 -> 970 us, 1024 rows 150 -> 140; but the low tiles read
+// their weights again, 8 x 2048 rows of 28672 x 4096 1883 -> 1905).  Of each
+// height, XCD x (workgroups go round robin over the XCDs) takes a contiguous
+// eighth, in bands of at most 8 row tiles that share its L2; its workgroups
+// take its tiles in turn.
 struct TileList {
-    int (*sched)[64];           // of expert e: tiles of rows up to it, first row, rows
-    int ntn, t, end, step;
+    int (*sched)[64];       // [h][e]: row tiles of height 8, 4, 2 up to expert e; first row, rows
+    int ntn, t, step, len[3];
     __device__ __forceinline__ void init(const BlockGemm& p, int ntn_, int (*sched_)[64]) {
         ntn = ntn_;
         sched = sched_;
         if (threadIdx.x < 64) {
             const int lane = threadIdx.x;
-            const int n = clamp_group_size(lane < p.E ? p.split[lane] : 0, p.rows);
-            sched[0][lane] = wave_incl_scan((n + kBM - 1) / kBM);
-            sched[1][lane] = wave_incl_scan(n) - n;
-            sched[2][lane] = n;
+            const int n = clamp_group_size(lane < p.E ? p.split[lane] : 0, p.rows), r = n % kBM;
+            sched[0][lane] = wave_incl_scan(n / kBM + (r > 128));
+            sched[1][lane] = wave_incl_scan(r > 64 && r <= 128);
+            sched[2][lane] = wave_incl_scan(r > 0 && r <= 64);
+            sched[3][lane] = wave_incl_scan(n) - n;
+            sched[4][lane] = n;
         }
         __syncthreads();
-        const int total = uniform(sched[0][63]) * ntn, chunk = (total + 7) >> 3;
-        t = (int)(blockIdx.x & 7) * chunk;
-        end = min(t + chunk, total);
-        t += (int)(blockIdx.x >> 3);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) len[h] = max(min(total(h) - first(h), eighth(h)), 0);
+        t = (int)(blockIdx.x >> 3);
         step = (int)(gridDim.x >> 3);
     }
+    __device__ __forceinline__ int total(int h) const { return uniform(sched[h][63]) * ntn; }
+    __device__ __forceinline__ int eighth(int h) const { return (total(h) + 7) >> 3; }
+    __device__ __forceinline__ int first(int h) const { return (int)(blockIdx.x & 7) * eighth(h); }
     __device__ __forceinline__ BlockTile next() {
         BlockTile tl{0, 0, 0, 0};
-        if (t >= end) return tl;
-        // (experts past the last one hold the total)
-        const int e = (int)__popcll(__ballot(sched[0][threadIdx.x & 63] * ntn <= t));
-        const int rows_e = uniform(sched[2][e]);
-        const int u = t - (e ? uniform(sched[0][e - 1]) : 0) * ntn;
-        const int mt = (rows_e + kBM - 1) / kBM;
-        const int band = u / (8 * ntn), b0 = band * 8, bm = min(mt - b0, 8);
-        const int v = u - band * 8 * ntn;
-        const int m0 = (b0 + v % bm) * kBM;
-        tl.e = e;
-        tl.n0 = v / bm * kBN;
-        tl.rows = min(rows_e - m0, kBM);
-        tl.row0 = uniform(sched[1][e]) + (int64_t)m0;
+        int h = 0, u = t;
+        while (h < 3 && u >= len[h]) u -= len[h++];
+        if (h == 3) return tl;
         t += step;
+        u += first(h);
+        // (experts past the last one hold the total)
+        const int e = (int)__popcll(__ballot(sched[h][threadIdx.x & 63] * ntn <= u));
+        const int before = e ? uniform(sched[h][e - 1]) : 0, n = uniform(sched[4][e]);
+        u -= before * ntn;
+        int m = n / kBM;
+        if (h == 0) {
+            const int mt = uniform(sched[0][e]) - before, band = u / (8 * ntn), b0 = band * 8, bm = min(mt - b0, 8);
+            u -= band * 8 * ntn;
+            m = b0 + u % bm;
+            u /= bm;
+        }
+        tl.e = e;
+        tl.n0 = u * kBN;
+        tl.rows = min(n - m * kBM, kBM);
+        tl.row0 = uniform(sched[3][e]) + (int64_t)m * kBM;
         return tl;
     }
 };
@@ -209,21 +237,24 @@ __device__ __forceinline__ int row_of_x(const BlockGemm& p, const BlockTile& tl)
     return s < p.x_rows ? s : -1;
 }
 
-// y of a tile.  A lane's 16 outputs of a row are neighbours: n = 16 g + 4 i + q.
+// y of a tile.  A lane's outputs of a row are n = 32 h + 8 g + 4 (i & 1) + q with
+// h = i >> 1: 8 neighbours of each half, and the four lanes of a row write 64
+// neighbouring bytes per store.
 template <int kMT>
 __device__ __forceinline__ void block_store(const BlockGemm& p, const BlockTile& tl, const f32x4 (&acc)[4][kMT], int wave) {
     const int lane = own_lane(), xr = (wave >> 2) * (16 * kMT) + (lane & 15);
-    const int n = tl.n0 + (wave & 3) * 64 + 16 * (lane >> 4);
+    const int n = tl.n0 + (wave & 3) * 64 + 8 * (lane >> 4);
 #pragma unroll
     for (int m = 0; m < kMT; ++m) {
         const int r = xr + 16 * m;
-        if (r >= tl.rows || n >= p.N) continue;     // N is a multiple of 32
-        u32x4* y = (u32x4*)(p.y + (tl.row0 + r) * p.N + n);
+        if (r >= tl.rows) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            y[h] = (u32x4){pack_bf16x2(acc[2 * h][m][0], acc[2 * h][m][1]), pack_bf16x2(acc[2 * h][m][2], acc[2 * h][m][3]),
-                           pack_bf16x2(acc[2 * h + 1][m][0], acc[2 * h + 1][m][1]),
-                           pack_bf16x2(acc[2 * h + 1][m][2], acc[2 * h + 1][m][3])};
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 a = acc[2 * h][m], b = acc[2 * h + 1][m];
+            if (n + 32 * h < p.N)               // N is a multiple of 32
+                *(u32x4*)(p.y + (tl.row0 + r) * p.N + n + 32 * h) =
+                    (u32x4){pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+        }
     }
 }
 
@@ -239,7 +270,7 @@ __device__ __forceinline__ BlockTile block_tiles(const BlockGemm& p, TileList& l
     // where a lane's fragments start in a stage: chunk g of its first row of the
     // weights and of x (chunk g + 4: the same with bit 6 changed; the next
     // fragment's row has the same swizzle), and the scale of its first row
-    const int wr = wn + ((l16 >> 2) << 4) + (l16 & 3), xr = wm + l16;
+    const int wr = wn + ((l16 >> 2) << 3) + (l16 & 3), xr = wm + l16;
     const int wat = wr * kBlk + ((g ^ wswz(wr)) << 4);
     const int xat = kWB + xr * kBlk + ((g ^ xswz(xr)) << 4), sat = kWB + kXB + xr * 4;
     const int nkb = (p.K + kBlk - 1) / kBlk;
@@ -290,7 +321,10 @@ __device__ __forceinline__ BlockTile block_tiles(const BlockGemm& p, TileList& l
             stage = stage + 1 == kStages ? 0 : stage + 1;
             const uint8_t *w0 = st + wat, *w1 = st + (wat ^ 64), *x0 = st + xat, *x1 = st + (xat ^ 64), *sx = st + sat;
             const float sw = *(const float*)(st + kWB + kXB + 1024 + 4 * ((wave >> 1) & 1));
-            auto wfrag = [&](int i) { return join(*(const u32x4*)(w0 + 4 * i * kBlk), *(const u32x4*)(w1 + 4 * i * kBlk)); };
+            auto wfrag = [&](int i) {
+                const int at = (32 * (i >> 1) + 4 * (i & 1)) * kBlk;
+                return join(*(const u32x4*)(w0 + at), *(const u32x4*)(w1 + at));
+            };
             auto xfrag = [&](int m) { return join(*(const u32x4*)(x0 + 16 * m * kBlk), *(const u32x4*)(x1 + 16 * m * kBlk)); };
             i32x8 a[4], b[2];
             float sb[2];
@@ -308,7 +342,6 @@ __device__ __forceinline__ BlockTile block_tiles(const BlockGemm& p, TileList& l
                 for (int j = 0; j < kPer; ++j)      // two loads a fragment column, from the first on
                     if ((j / 2 < kMT ? j / 2 : kMT - 1) == m) feed.load(scale_step, base, j, wave);
                 __builtin_amdgcn_sched_barrier(0);
-                __builtin_amdgcn_s_setprio(1);
                 const float s = sb[m & 1] * sw;
                 f32x4 d[4];
 #pragma unroll
@@ -323,7 +356,6 @@ __device__ __forceinline__ BlockTile block_tiles(const BlockGemm& p, TileList& l
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dp[i] = d[i];
                 sp = s;
-                __builtin_amdgcn_s_setprio(0);
             }
             // the next step's (or the next tile's first) loads have landed, and
             // all waves are done with this one's stage
@@ -344,7 +376,7 @@ __device__ __forceinline__ BlockTile block_tiles(const BlockGemm& p, TileList& l
 
 __global__ __launch_bounds__(kThreads, 2) void gemm_block_kernel(BlockGemm p, int ntn) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLdsB];
-    __shared__ int sched[3][64], rows[kBM];
+    __shared__ int sched[5][64], rows[kBM];
     TileList list;
     list.init(p, ntn, sched);
     BlockTile tl = list.next();
