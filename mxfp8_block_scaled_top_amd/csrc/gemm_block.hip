@@ -65,6 +65,32 @@ constexpr int kWB = kBN * kBlk;             // a stage's weights
 __device__ __forceinline__ int xswz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int wswz(int r) { return ((r >> 2) & 6) | ((r >> 1) & 1); }
 
+// Sum over the lanes up to each one, cut at 2^32 - 1: shifts inside the rows of
+// 16 lanes, then the rows' sums passed on (no LDS).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t dpp_add_sat(uint32_t v) {
+    return __builtin_elementwise_add_sat(
+        v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRows, 0xf, false));
+}
+__device__ __forceinline__ uint32_t scan(uint32_t v) {
+    v = dpp_add_sat<0x111, 0xf>(v);     // row_shr:1, 2, 4, 8
+    v = dpp_add_sat<0x112, 0xf>(v);
+    v = dpp_add_sat<0x114, 0xf>(v);
+    v = dpp_add_sat<0x118, 0xf>(v);
+    v = dpp_add_sat<0x142, 0xa>(v);     // row_bcast:15 into rows 1 and 3
+    return dpp_add_sat<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+}
+
+// Rows of expert e (lane e of a full wave) and the first of them: a negative
+// size counts as 0, and sizes whose running total passes `rows` are cut at it.
+__device__ __forceinline__ int expert_rows(const BlockGemm& p, int& first) {
+    const int lane = threadIdx.x & 63, n = lane < p.E ? p.split[lane] : 0;
+    const uint32_t up = min(scan(n > 0 ? (uint32_t)n : 0u), (uint32_t)p.rows);
+    const int before = __shfl_up((int)up, 1);
+    first = lane ? before : 0;
+    return (int)up - first;
+}
+
 __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
     return (i32x8){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
@@ -102,11 +128,12 @@ struct TileList {
         sched = sched_;
         if (threadIdx.x < 64) {
             const int lane = threadIdx.x;
-            const int n = clamp_group_size(lane < p.E ? p.split[lane] : 0, p.rows), r = n % kBM;
-            sched[0][lane] = wave_incl_scan(n / kBM + (r > 128));
-            sched[1][lane] = wave_incl_scan(r > 64 && r <= 128);
-            sched[2][lane] = wave_incl_scan(r > 0 && r <= 64);
-            sched[3][lane] = wave_incl_scan(n) - n;
+            int first;
+            const int n = expert_rows(p, first), r = n % kBM;
+            sched[0][lane] = (int)scan(n / kBM + (r > 128));
+            sched[1][lane] = (int)scan(r > 64 && r <= 128);
+            sched[2][lane] = (int)scan(r > 0 && r <= 64);
+            sched[3][lane] = first;
             sched[4][lane] = n;
         }
         __syncthreads();
@@ -472,8 +499,8 @@ __global__ __launch_bounds__(kFewThreads) void gemm_block_few_kernel(BlockGemm p
     const int q = blockIdx.x / ntn;
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
-        const int n = clamp_group_size(lane < p.E ? p.split[lane] : 0, p.rows);
-        const int first = wave_incl_scan(n) - n;
+        int first;
+        const int n = expert_rows(p, first);
         const uint64_t has = __ballot(n > 0);
         if (lane == 0) found[0] = -1;
         if (n > 0 && __popcll(has & lanemask_lt()) == q) {
