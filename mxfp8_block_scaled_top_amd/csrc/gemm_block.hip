@@ -492,11 +492,11 @@ __device__ __forceinline__ void few_rows(const BlockGemm& p, int e, int n0, int6
     __syncthreads();
 }
 
-__global__ __launch_bounds__(kFewThreads) void gemm_block_few_kernel(BlockGemm p, int ntn) {
+__global__ __launch_bounds__(kFewThreads) void gemm_block_few_kernel(BlockGemm p) {
     __shared__ __attribute__((aligned(16))) float red[kFewWaves * 16 * kFewRow];
     __shared__ int found[3];
     // workgroups of the q-th expert that has rows
-    const int q = blockIdx.x / ntn;
+    const int q = blockIdx.y;
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
         int first;
@@ -514,7 +514,7 @@ __global__ __launch_bounds__(kFewThreads) void gemm_block_few_kernel(BlockGemm p
     if (e < 0) return;
     int64_t row0 = __builtin_amdgcn_readfirstlane(found[1]);
     int rows = __builtin_amdgcn_readfirstlane(found[2]);
-    const int n0 = (blockIdx.x % ntn) * kFewN;
+    const int n0 = blockIdx.x * kFewN;
     while (rows > 0) {
         const int n = min(rows, 16);
         few_rows(p, e, n0, row0, n, red);
@@ -530,8 +530,8 @@ hipError_t launch_gemm_block(const BlockGemm& p, hipStream_t s, const char* name
     TraceScope ts(name, s);
     if (p.rows <= kFewMean * p.E) {
         const int nt = (p.N + kFewN - 1) / kFewN;
-        const int64_t experts = p.rows < p.E ? p.rows : p.E;
-        gemm_block_few_kernel<<<(unsigned)(experts * nt), kFewThreads, 0, s>>>(p, nt);
+        const int experts = (int)(p.rows < p.E ? p.rows : p.E);
+        gemm_block_few_kernel<<<dim3((unsigned)nt, (unsigned)experts), kFewThreads, 0, s>>>(p);
         return hipGetLastError();
     }
     const int ntn = (p.N + kBN - 1) / kBN;

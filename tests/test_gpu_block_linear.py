@@ -386,6 +386,25 @@ def test_offsets_past_32_bits(T, N, K):
     _check_fwd(p, y[-n:])
 
 
+def test_widest_outputs_with_the_same_weight_for_every_expert():
+    """2^22 columns, one row each for 64 experts that share a matrix: each row is what it is alone."""
+    say("block product 64 x 4194304 x 32, shared weights")
+    N, K, E = 1 << 22, 32, 64
+    w = _randn(1, N, K, seed=20).cuda()
+    w8 = moe.fp8_block_quantize_weights(w)
+    x = _randn(E, K, seed=21).cuda()
+    many = {"codes": [w8["codes"][0]] * E, "scales": [w8["scales"][0]] * E}
+    y, x8 = moe.grouped_linear_block_fwd(x, torch.ones(E, dtype=torch.int32, device="cuda"), many)
+    for r in (0, 1, 40, 63):
+        one, _ = moe.grouped_linear_block_fwd(x[r:r + 1], torch.ones(1, dtype=torch.int32, device="cuda"), w8)
+        torch.cuda.synchronize()
+        assert torch.equal(y[r], one[0])
+    a = B.rows_value(np_(x8["codes"]), np_(x8["scales"]))
+    for n in (0, N // 2, N - 128):
+        b = B.weight_value(np_(w8["codes"][0, n:n + 128]), np_(w8["scales"][0, n // 128:n // 128 + 1]))
+        _check(y[:, n:n + 128], a @ b.T, _product_bound(a, b), f"columns from {n}")
+
+
 def test_same_bits_in_a_graph_and_on_two_streams():
     say("block product in a graph, on two streams")
     p = _problem([300, 0, 211, 5], 4, 288, 416, seed=13, tokens=400)
