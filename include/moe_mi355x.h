@@ -909,7 +909,7 @@ int fp8_block_quantize(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* c
 /*
  * fp8_block_quantize_weights -- the same for weights, one scale per 128 x 128
  * values (fewer at the edges).
- * nmat         matrices, 1..64.   N, K: multiples of 8, from 8; N <= 2^22.
+ * nmat         matrices, 1..64.   N, K: multiples of 8, from 8; N <= 2^22, K <= 2^30.
  * w            HOST array of nmat device pointers, each bf16 [N, K].
  * codes        HOST array, each uint8 [N, K] out.
  * scales       HOST array, each fp32 [ceil(N/128), ceil(K/128)] out.
@@ -964,7 +964,8 @@ int grouped_linear_block_fwd(int E, int N, int K, int64_t rows, const uint8_t* x
  * w_codes_t    HOST array, each uint8 [K, N]: the transposed codes.
  * w_scales     HOST array, each fp32 [ceil(N/128), ceil(K/128)].
  * dx           bf16 [rows, K] out, or NULL (not computed; w_* may be NULL then).
- * dw           HOST array of E device pointers, each bf16 [N, K] out, or NULL.
+ * dw           HOST array of E device pointers, each bf16 [N, K] out, or NULL;
+ *              no two alike (MOE_ERR_ARG).
  * workspace    moe_workspace_bytes(MOE_OP_LINEAR_BLOCK_BWD, rows, K, N, E, 1, 0).
  */
 int grouped_linear_block_bwd(int E, int N, int K, int64_t rows, const uint16_t* dy,

@@ -93,7 +93,8 @@ int fp8_block_quantize_weights(int nmat, int64_t N, int64_t K, const uint16_t* c
                                uint8_t* const* codes, float* const* scales, uint8_t* const* codes_t,
                                hipStream_t stream) {
     if (nmat < 1 || nmat > kMaxExperts) return MOE_ERR_SHAPE;
-    if (N < 8 || K < 8 || (N % 8) || (K % 8) || N > (1 << 22) || K > INT32_MAX) return MOE_ERR_SHAPE;
+    // blocks of 256 threads for every 128 columns, at most 2^32 - 1 threads in a row
+    if (N < 8 || K < 8 || (N % 8) || (K % 8) || N > (1 << 22) || K > (1 << 30)) return MOE_ERR_SHAPE;
     if (!w || !codes || !scales) return MOE_ERR_NULL;
     MatTable tw{}, tc{}, ts{}, tt{};
     for (int m = 0; m < nmat; ++m) {
@@ -165,6 +166,8 @@ int grouped_linear_block_bwd(int E, int N, int K, int64_t rows, const uint16_t* 
             g.w_scale.p[e] = w_scales[e];
         }
         if (dw) wg.c_tab.p[e] = dw[e];
+        for (int d = 0; dw && d < e; ++d)
+            if (dw[d] == dw[e]) return MOE_ERR_ARG;     // an output of its own for every expert
     }
     if (rows > 0 && (!dy || (dw && x_rows > 0 && (!x_codes || !x_scales)))) return MOE_ERR_NULL;
     if (!aligned16(dy) || !aligned16(x_codes) || !aligned16(x_scales) || !aligned16(dx) || !aligned16(workspace))

@@ -14,6 +14,7 @@ from oracle.mx import e4m3_decode
 
 NULL, SHAPE, ALIGN, WS, ARG = 1, 2, 3, 4, 7
 P = ctypes.c_void_p(4096)       # never dereferenced: every call below fails validation
+P2 = ctypes.c_void_p(8192)
 MIS = ctypes.c_void_p(4104)
 ODD = ctypes.c_void_p(4098)
 
@@ -191,6 +192,7 @@ def _tab(*p):
 
 @pytest.mark.parametrize("change,status", [
     ({"n": 0}, SHAPE), ({"n": 65}, SHAPE), ({"N": 4}, SHAPE), ({"K": 12}, SHAPE), ({"N": (1 << 22) + 8}, SHAPE),
+    ({"K": (1 << 30) + 8}, SHAPE),
     ({"w": None}, NULL), ({"codes": None}, NULL), ({"scales": None}, NULL), ({"w": _tab(P, None)}, NULL),
     ({"codes_t": _tab(None, P)}, NULL), ({"w": _tab(P, MIS)}, ALIGN), ({"codes": _tab(MIS, P)}, ALIGN),
     ({"codes_t": _tab(MIS, P)}, ALIGN), ({"scales": _tab(P, ODD)}, ALIGN),
@@ -223,11 +225,12 @@ def test_grouped_linear_block_fwd_refuses(L, change, status):
     ({"dy": None}, NULL), ({"x": None}, NULL), ({"xs": None}, NULL), ({"wc": None}, NULL), ({"ws": None}, NULL),
     ({"dw": _tab(P, None)}, NULL), ({"wk": None}, NULL), ({"n": 16}, WS), ({"dy": MIS}, ALIGN),
     ({"dx": MIS}, ALIGN), ({"dw": _tab(P, MIS)}, ALIGN), ({"wc": _tab(MIS, P)}, ALIGN), ({"wk": MIS}, ALIGN),
+    ({"dw": _tab(P, P)}, ARG),
 ])
 def test_grouped_linear_block_bwd_refuses(L, change, status):
     t = _tab(P, P)
-    a = dict(E=2, N=64, K=96, rows=8, dy=P, x=P, xs=P, xr=8, src=None, split=P, wc=t, ws=t, dx=P, dw=t, wk=P,
-             n=1 << 30) | change
+    a = dict(E=2, N=64, K=96, rows=8, dy=P, x=P, xs=P, xr=8, src=None, split=P, wc=t, ws=t, dx=P, dw=_tab(P, P2),
+             wk=P, n=1 << 30) | change
     assert L.grouped_linear_block_bwd(*a.values(), None) == status
 
 
