@@ -26,7 +26,7 @@ ARCH = "gfx950"
 
 SOURCES = ["route.hip", "router.hip", "permute.hip", "mxfp8.hip", "gemm.hip", "gemm_few.hip",
            "check.hip", "layernorm.hip", "swiglu.hip", "rmsnorm.hip", "balance.hip",
-           "quant128.hip", "gemm_block.hip", "capi.cpp", "mlp.cpp", "linear.cpp",
+           "quant128.hip", "gemm_block.hip", "wgrad_block.hip", "capi.cpp", "mlp.cpp", "linear.cpp",
            "linear_block.cpp", "sublayer.cpp", "trace.cpp"]
 
 FLAGS = [

@@ -169,4 +169,16 @@ struct BlockGemm {
 };
 hipError_t launch_gemm_block(const BlockGemm& p, hipStream_t s, const char* name);
 
+// Their weight gradients on bf16 operands: dw_e [N, K] = dy_e^T x_e.
+struct WgradBlock {
+    const bf16_t* dy;           // [rows, N]
+    const bf16_t* x;            // [rows, K]
+    const int32_t* split;
+    int E;
+    int64_t rows;
+    int N, K;
+    MatTable dw;
+};
+hipError_t launch_wgrad_block(const WgradBlock& p, hipStream_t s, const char* name);
+
 }  // namespace moe

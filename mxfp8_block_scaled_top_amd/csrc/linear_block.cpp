@@ -7,7 +7,13 @@
 //   wgrad     dW_e = dy_e^T x^_e       bf16 operands, x^ decoded here: blocks
 //                                      along the rows would give both operands
 //                                      a scale per output row and column, two
-//                                      vector operations per product element
+//                                      vector operations per product element;
+//                                      and x^ = code * scale rounded to bf16
+//                                      (2^-8 of each product at most) keeps dy
+//                                      as it is
+//
+// 4099 rows over 8 experts of 4096 x 14336, us: dy's codes 12, dgrad 304, decoding
+// 33, wgrad 542.
 #include "moe_mi355x.h"
 
 #include <hip/hip_runtime.h>
@@ -156,7 +162,7 @@ int grouped_linear_block_bwd(int E, int N, int K, int64_t rows, const uint16_t* 
     if (!split_sizes || !workspace) return MOE_ERR_NULL;
     if (dx && (!w_codes_t || !w_scales)) return MOE_ERR_NULL;
     BlockGemm g{};
-    GemmArgs wg{};
+    WgradBlock wg{};
     for (int e = 0; e < E; ++e) {
         if ((dx && (!w_codes_t[e] || !w_scales[e])) || (dw && !dw[e])) return MOE_ERR_NULL;
         if (dx && (!aligned16(w_codes_t[e]) || ((uintptr_t)w_scales[e] & 3))) return MOE_ERR_ALIGN;
@@ -165,7 +171,7 @@ int grouped_linear_block_bwd(int E, int N, int K, int64_t rows, const uint16_t* 
             g.w.p[e] = w_codes_t[e];
             g.w_scale.p[e] = w_scales[e];
         }
-        if (dw) wg.c_tab.p[e] = dw[e];
+        if (dw) wg.dw.p[e] = dw[e];
         for (int d = 0; dw && d < e; ++d)
             if (dw[d] == dw[e]) return MOE_ERR_ARG;     // an output of its own for every expert
     }
@@ -193,19 +199,14 @@ int grouped_linear_block_bwd(int E, int N, int K, int64_t rows, const uint16_t* 
     if (dw) {
         MOE_TRY(launch_dequant_rows128(x_codes, x_scales, src_token, x_rows, rows, K, ws.x, stream,
                                        "linear_block_decode_x"));
+        wg.dy = dy;
+        wg.x = ws.x;
         wg.split = split_sizes;
         wg.E = E;
         wg.rows = rows;
-        wg.rows_pad = padded_rows(rows, E);
-        wg.M = N;
-        wg.N = K;
-        wg.ldc = K;
-        wg.a = dy;
-        wg.lda = N;
-        wg.b.p[0] = ws.x;
-        wg.ldb = K;
-        wg.name = "linear_block_wgrad";
-        MOE_TRY(launch_gemm(DT_BF16, U_GATEUP_WGRAD, wg, stream));
+        wg.N = N;
+        wg.K = K;
+        MOE_TRY(launch_wgrad_block(wg, stream, "linear_block_wgrad"));
     }
     return MOE_OK;
 }

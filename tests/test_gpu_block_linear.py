@@ -218,6 +218,32 @@ def test_several_tiles_per_workgroup(K, gather):
     assert torch.equal(y, z)
 
 
+@pytest.mark.parametrize("split,N,K", [
+    # 320 tiles, more than compute units, of 1 to 5 steps of 32 rows, so that loads run on over one or more tiles
+    ([1, 31, 32, 33, 64, 65, 0, 96, 97, 128, 129, 2, 30, 160, 0, 5, 63, 95, 127, 34], 992, 1024),
+    # 1080 tiles, a long expert whose tiles are a workgroup's share and more
+    ([40, 0, 1500, 7, 33, 64], 4512, 2528),
+    # rows of tiles that no band of 8 divides, columns that end inside a tile
+    ([70, 200, 3], 2336, 96), ([70, 0, 200], 96, 2336)])
+def test_weight_gradients_of_many_tiles(split, N, K):
+    say(f"block product weight gradients {split[:6]} {N} x {K}")
+    rows = sum(split)
+    x8 = moe.fp8_block_quantize(_randn(rows, K, seed=30).cuda())
+    dy = _randn(rows, N, seed=31).cuda()
+    args = (dy, {"codes": x8[0], "scales": x8[1]}, torch.tensor(split, dtype=torch.int32, device="cuda"), {})
+    _, dw = moe.grouped_linear_block_bwd(*args, want_dx=False)
+    _, again = moe.grouped_linear_block_bwd(*args, want_dx=False)
+    torch.cuda.synchronize()
+    assert torch.equal(dw, again)
+    x = B.rows_value(np_(x8[0]), np_(x8[1]))
+    d = dy.cpu().double()
+    at = 0
+    for e, n in enumerate(split):
+        a, b = d[at:at + n], x[at:at + n]
+        _check(dw[e], a.T @ b, (H8 + (n + 8) * U) * (a.abs().T @ b.abs()), f"dw {e}")
+        at += n
+
+
 def test_input_gradient_against_differences():
     """dx of sum(y dy) where dy is exact in 8 bits (+-1, so dy^ = dy) against central differences of the
     float64 product with respect to x^ (linear: exact); half a bf16 step and the product's bound."""
@@ -384,6 +410,28 @@ def test_offsets_past_32_bits(T, N, K):
     torch.cuda.synchronize()
     _check_fwd(p, ref)
     _check_fwd(p, y[-n:])
+
+
+@pytest.mark.parametrize("T,N,K", [(1_060_000, 64, 2048), (1_060_000, 2048, 64)])
+def test_backward_offsets_past_32_bits(T, N, K):
+    """dy or the decoded rows above 4 GB: where all but the last rows of dy are zeros, gradients are those rows'."""
+    say(f"block product backward {T} x {N} x {K}")
+    n = 700
+    p = _problem([n], 1, N, K, seed=14)
+    codes = torch.full((T, K), 0x38, dtype=torch.uint8, device="cuda")
+    scales = torch.ones((p["x8"]["scales"].shape[0], T), device="cuda")
+    codes[-n:], scales[:, -n:] = p["x8"]["codes"], p["x8"]["scales"]
+    dy = torch.zeros((T, N), dtype=BF, device="cuda")
+    d = _randn(n, N, seed=15)
+    dy[-n:] = d.cuda()
+    dx, dw = moe.grouped_linear_block_bwd(dy, {"codes": codes, "scales": scales},
+                                          torch.tensor([T], dtype=torch.int32, device="cuda"), p["w8"])
+    torch.cuda.synchronize()
+    dyq = B.rows_value(*B.quantize_rows(d))
+    rx, rw = B.linear_bwd(d, dyq, p["x"], p["w"], [n])
+    _check(dx[-n:], rx, _product_bound(dyq, p["w"][0].T.contiguous()), "dx")
+    _check(dw[0], rw[0], (H8 + (n + 8) * U) * (d.double().abs().T @ p["x"].abs()), "dw")
+    assert not dx[:-n].any()
 
 
 def test_widest_outputs_with_the_same_weight_for_every_expert():
