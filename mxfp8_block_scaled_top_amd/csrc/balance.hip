@@ -7,11 +7,16 @@
 //   dlogits_te = dloss [ a E / n p_te (f_e - sum_j f_j p_tj) + 2 z / n lse_t p_te ]
 //
 // Bound by launches for usual sizes (4 MB of logits at 16384 x 64), by HBM bytes
-// beyond.  A token has 2^j lanes with 1 or 4 experts each, so its maximum and sums are
+// beyond.  A token has 2^j lanes with 4 experts each, so its maximum and sums are
 // lane shifts, and each lane adds up its own experts' probabilities over the
-// tokens it walks.  Sums are taken in a fixed order: a workgroup's partial
+// tokens it walks.  (Rows of other than multiples of 4 experts start anywhere:
+// loads and stores of 16 bytes need 4-byte alignment alone.  One expert a lane takes
+// three times as long, 131072 x 60 129 us both ways, so 45.)  Sums are taken in a fixed order: a workgroup's partial
 // rows, which a second kernel adds (in one launch where one workgroup has all
 // tokens); counts are integers.  No float atomics.
+//
+// Measured: 256 x 4 4.7 us and 2.1 for the gradient; 16384 x 64, 8 picks, 5.9 + 4.4 and 5.3;
+// a million tokens of 64 180 us both ways (5 TB/s).
 #include "common.hpp"
 #include "kernels.hpp"
 #include "trace.hpp"
@@ -21,7 +26,11 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxParts = 256;      // workgroups of the forward
+// Workgroups of the forward: each has a pass over 256 lanes' tokens, from 256 on as
+// many as have 16 passes.  us both ways with 256 / 512 / 1024: 16384 x 64 (1024 passes)
+// 13.4 / 13.9 / 16.6, 131072 x 8 (1024) 13.7 / 14.7 / 19.0, a million x 8 (7813) 42 / 34 / 34, 131072 x 64
+// (8192) 44 / 36 / 35, a million x 64 (62500) 326 / 219 / 180.
+constexpr int kParts = 256, kPasses = 16, kMaxParts = 1024;
 
 // Largest or sum over each G neighbouring lanes, the same for all of them.
 struct Max { static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); } };
@@ -36,8 +45,6 @@ __device__ __forceinline__ float over(float v) {
     if (G >= 4) v = dpp_op<Op, 0x4E>(v);
     if (G >= 8) v = dpp_op<Op, 0x141>(v);       // row_half_mirror, row_mirror
     if (G >= 16) v = dpp_op<Op, 0x140>(v);
-    if (G >= 32) v = Op::of(v, __shfl_xor(v, 16));
-    if (G >= 64) v = Op::of(v, __shfl_xor(v, 32));
     return v;
 }
 
@@ -50,10 +57,12 @@ struct BalArgs {
     float coef, zcoef;
 };
 
+constexpr int V = 4;        // experts of a lane
+
 // A token's logits in its lanes' registers (V experts each, -inf past E) to
 // probabilities, and its log sum exp.  A token without a finite or infinite
 // logit above -inf has no softmax: p = 0, lse = 0.
-template <int V, int G>
+template <int G>
 __device__ __forceinline__ void softmax(float (&x)[V], float& lse) {
     float m = x[0];
 #pragma unroll
@@ -73,15 +82,26 @@ __device__ __forceinline__ void softmax(float (&x)[V], float& lse) {
     for (int i = 0; i < V; ++i) x[i] *= inv;
 }
 
-template <int V>
-__device__ __forceinline__ void load_logits(const float* row, int e0, int E, float (&x)[V]) {
-    if constexpr (V == 4) {
-        float4 w = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (e0 < E) w = *(const float4*)(row + e0);
-        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
-    } else {
-        x[0] = e0 < E ? row[e0] : -INFINITY;
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// Four of a row's E values from e0 on; `none` past the end.
+__device__ __forceinline__ void load_row4(const float* row, int e0, int E, float none, float (&x)[4]) {
+    if (e0 + 4 <= E) {
+        const f32x4u w = *(const f32x4u*)(row + e0);
+        x[0] = w[0]; x[1] = w[1]; x[2] = w[2]; x[3] = w[3];
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = e0 + i < E ? row[e0 + i] : none;
+}
+__device__ __forceinline__ void store_row4(float* row, int e0, int E, const float (&x)[4]) {
+    if (e0 + 4 <= E) {
+        *(f32x4u*)(row + e0) = (f32x4u){x[0], x[1], x[2], x[3]};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (e0 + i < E) row[e0 + i] = x[i];
 }
 
 // What the sums become: losses [total, balance, z], counts [E], the number of
@@ -110,7 +130,7 @@ __device__ void finish(const BalArgs& a, int e, double prob, int count, double z
 // Partial sums of a workgroup: [kMaxParts][E] probabilities, [kMaxParts] of
 // lse^2, then as integers [kMaxParts][E] counts and [kMaxParts] tokens.  With
 // one workgroup they are the sums, and it writes the outputs.
-template <int V, int G>
+template <int G>
 __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(BalArgs a, float* part, float* loss,
                                                                int32_t* counts, int32_t* ntok, float* mean_prob) {
     constexpr int kSlots = kThreads / G;            // tokens at once
@@ -129,12 +149,12 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(BalArgs a, float*
     for (int64_t t = (int64_t)blockIdx.x * kSlots + tid / G; t < a.T; t += (int64_t)gridDim.x * kSlots) {
         if (a.mask && !a.mask[t]) continue;         // the same for the token's lanes
         float x[V], lse;
-        load_logits<V>(a.logits + t * a.E, e0, a.E, x);
+        load_row4(a.logits + t * a.E, e0, a.E, -INFINITY, x);
         for (int j = tid % G; j < a.k; j += G) {
             const int e = a.topk[t * a.k + j];
             if ((unsigned)e < (unsigned)a.E) atomicAdd(&sc[e], 1);
         }
-        softmax<V, G>(x, lse);
+        softmax<G>(x, lse);
 #pragma unroll
         for (int i = 0; i < V; ++i) prob[i] += x[i];
         if (tid % G == 0) {
@@ -219,7 +239,7 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(BalArgs a, const floa
     finish(a, e, p, c, z, n, loss, counts, ntok, mean_prob);
 }
 
-template <int V, int G>
+template <int G>
 __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BalArgs a, const int32_t* __restrict__ counts,
                                                                const int32_t* __restrict__ ntok,
                                                                const float* __restrict__ dloss,
@@ -236,23 +256,15 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BalArgs a, const 
     for (int64_t t = (int64_t)blockIdx.x * kSlots + threadIdx.x / G; t < a.T;
          t += (int64_t)gridDim.x * kSlots) {
         float d[V], x[V];
-        const bool in = e0 < a.E;
         const bool live = !(a.mask && !a.mask[t]);      // the same for the token's lanes
         float old[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] = old[i] = 0.f;
-        if (add && in) {
-            if constexpr (V == 4) {
-                const float4 w = *(const float4*)(add + t * a.E + e0);
-                old[0] = w.x; old[1] = w.y; old[2] = w.z; old[3] = w.w;
-            } else {
-                old[0] = add[t * a.E + e0];
-            }
-        }
+        if (add) load_row4(add + t * a.E, e0, a.E, 0.f, old);
         if (live) {
             float lse, s = 0.f;
-            load_logits<V>(a.logits + t * a.E, e0, a.E, x);
-            softmax<V, G>(x, lse);
+            load_row4(a.logits + t * a.E, e0, a.E, -INFINITY, x);
+            softmax<G>(x, lse);
 #pragma unroll
             for (int i = 0; i < V; ++i) s += x[i] * f[i];
             s = over<G, Sum>(s);
@@ -261,36 +273,24 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BalArgs a, const 
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] += old[i];
-        if (in) {
-            if constexpr (V == 4) *(float4*)(dlogits + t * a.E + e0) = make_float4(d[0], d[1], d[2], d[3]);
-            else dlogits[t * a.E + e0] = d[0];
-        }
+        store_row4(dlogits + t * a.E, e0, a.E, d);
     }
 }
 
 template <int N> struct Num { static constexpr int v = N; };
-// Experts per lane and lanes per token: 16 bytes a lane where rows allow it.
+// Lanes of a token.
 template <class F>
 void with_lanes(int E, F&& f) {
-    if (E % 4 == 0) {
-        if (E <= 4) f(Num<4>{}, Num<1>{});
-        else if (E <= 8) f(Num<4>{}, Num<2>{});
-        else if (E <= 16) f(Num<4>{}, Num<4>{});
-        else if (E <= 32) f(Num<4>{}, Num<8>{});
-        else f(Num<4>{}, Num<16>{});
-    } else {
-        if (E <= 1) f(Num<1>{}, Num<1>{});
-        else if (E <= 2) f(Num<1>{}, Num<2>{});
-        else if (E <= 4) f(Num<1>{}, Num<4>{});
-        else if (E <= 8) f(Num<1>{}, Num<8>{});
-        else if (E <= 16) f(Num<1>{}, Num<16>{});
-        else if (E <= 32) f(Num<1>{}, Num<32>{});
-        else f(Num<1>{}, Num<64>{});
-    }
+    if (E <= 4) f(Num<1>{});
+    else if (E <= 8) f(Num<2>{});
+    else if (E <= 16) f(Num<4>{});
+    else if (E <= 32) f(Num<8>{});
+    else f(Num<16>{});
 }
 
-unsigned passes(int64_t T, int slots, int most) {
-    const int64_t n = (T + slots - 1) / slots;
+int64_t passes(int64_t T, int lanes) { return (T + kThreads / lanes - 1) / (kThreads / lanes); }
+unsigned parts(int64_t n) {
+    const int64_t most = n / kPasses < kParts ? kParts : n / kPasses < kMaxParts ? n / kPasses : kMaxParts;
     return (unsigned)(n < 1 ? 1 : n < most ? n : most);
 }
 
@@ -305,9 +305,9 @@ hipError_t launch_balance_fwd(const float* logits, int64_t T, int E, int k, cons
     unsigned np = 1;
     {
         TraceScope ts("balance_fwd", s);
-        with_lanes(E, [&](auto v, auto g) {
-            np = passes(T, kThreads / decltype(g)::v, kMaxParts);
-            balance_fwd_kernel<decltype(v)::v, decltype(g)::v>
+        with_lanes(E, [&](auto g) {
+            np = parts(passes(T, decltype(g)::v));
+            balance_fwd_kernel<decltype(g)::v>
                 <<<np, kThreads, 0, s>>>(a, (float*)ws, loss, counts, ntok, mean_prob);
         });
     }
@@ -324,9 +324,10 @@ hipError_t launch_balance_bwd(const float* logits, int64_t T, int E, int k, cons
     if (T == 0) return hipSuccess;
     const BalArgs a{logits, nullptr, mask, T, E, k, coef, zcoef};
     TraceScope ts("balance_bwd", s);
-    with_lanes(E, [&](auto v, auto g) {
-        balance_bwd_kernel<decltype(v)::v, decltype(g)::v>
-            <<<passes(T, kThreads / decltype(g)::v, 2048), kThreads, 0, s>>>(a, counts, ntok, dloss, add, dlogits);
+    with_lanes(E, [&](auto g) {
+        const int64_t n = passes(T, decltype(g)::v);
+        balance_bwd_kernel<decltype(g)::v>
+            <<<(unsigned)(n < 2048 ? n : 2048), kThreads, 0, s>>>(a, counts, ntok, dloss, add, dlogits);
     });
     return hipGetLastError();
 }

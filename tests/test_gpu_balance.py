@@ -73,12 +73,36 @@ def _check(x, topk, mask, d0, coef, z, dloss=None):
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (2, 2, 1), (7, 3, 2), (64, 4, 4), (256, 4, 2), (300, 5, 5),
                                    (513, 8, 2), (129, 12, 3), (77, 16, 2), (250, 17, 4), (999, 32, 6), (40, 33, 1),
-                                   (2500, 60, 8), (1500, 63, 2), (4099, 64, 8)])
+                                   (2500, 60, 8), (1500, 63, 2), (4099, 64, 8), (70001, 61, 3), (300, 1, 1)])
 @pytest.mark.parametrize("masked,add", [(False, False), (True, True)], ids=["plain", "mask_add"])
 def test_losses_and_gradient(T, E, k, masked, add):
     say(f"balance T={T} E={E} k={k} mask={masked} add={add}")
     x, topk, mask, d0 = _case(T, E, k, seed=T + E, masked=masked, add=add)
     _check(x, topk, mask, d0, 0.01, 0.001, None if add else 2.5)
+
+
+def test_offsets_past_32_bits():
+    """2.2 billion logits, zeros but for the last rows; every token picks expert 0, so f = (1, 0, ..).  Probabilities
+    carry some 8 roundings (exponential, sum, quotient), the products after them 4 more: 16 u of the terms' sizes."""
+    T, E, n = 34_000_000, 64, 500
+    say(f"balance {T} x {E}")
+    logits = torch.zeros((T, E), device="cuda")
+    x = torch.randn(n, E, generator=torch.Generator().manual_seed(5))
+    logits[-n:] = x.cuda()
+    loss, saved = moe.moe_balance_fwd(logits, torch.zeros((T, 1), dtype=torch.int32, device="cuda"), balance_coef=1.0)
+    d = moe.moe_balance_bwd(logits, saved)
+    torch.cuda.synchronize()
+    p = x.double().softmax(-1)
+    P0 = (p[:, 0].sum() + (T - n) / 64) / T
+    assert saved["counts"].tolist() == [T] + [0] * 63 and int(saved["tokens"]) == T
+    assert abs(float(loss) - float(64 * P0)) <= 64 * 2.0 ** -24
+    f = torch.zeros(E).double()
+    f[0] = 1
+    want = 64 / T * p * (f - p[:, :1])
+    lim = 16 * 2.0 ** -24 * 64 / T * p * (f + p[:, :1])
+    assert ((d[-n:].cpu().double() - want).abs() <= lim).all()
+    first = 64 / T / 64 * (f - 1 / 64)
+    assert ((d[[0, 1, T // 2]].cpu().double() - first).abs() <= 16 * 2.0 ** -24 * first.abs()).all()
 
 
 def test_one_loss_alone_and_large_coefficients():
