@@ -16,6 +16,11 @@
 // 128 values is the 16 lanes of a row of lanes, so its largest magnitude takes
 // four lane shifts.  The scales are stored [blocks][rows], the order in which
 // the products read them; a row's 4-byte pieces of it are 2% of its bytes.
+//
+// Measured (a copy of 1 GiB: 5.1 TB/s): forward of 8192 x 4096 bf16 with residual, y
+// and codes 53 us (5.7 TB/s); backward of 16384 x 2048 over an fp32 stream, with the
+// residual's gradient and the bf16 copy, 96 + 5 us (5.6 TB/s).  One row of 4096: 2.9 us,
+// the time of an empty launch and a read after it.
 #include "block8.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
@@ -166,7 +171,6 @@ template <bool SF32, class S, bool kSums>
 __global__ __launch_bounds__(S::kThreads) void rms_bwd_kernel(RmsBwd a) {
     constexpr int kV = S::kV, kRows = S::kRows, kPer = S::kPer;
     constexpr int kPart = kRows * S::kLanes / 64;   // rows left after each wave has added its own
-    constexpr bool kPrefetch = SF32 && !S::kLean;
     __shared__ float red[2][16][1];
     __shared__ float comb[kSums && kPart > 1 ? 8 * kPer * kV : 1];
     const int l = S::place();
@@ -226,7 +230,6 @@ __global__ __launch_bounds__(S::kThreads) void rms_bwd_kernel(RmsBwd a) {
             res[v] = Raw8<SF32>{};
             if (a.dres && r < a.T && c < nc) res[v] = load_raw<SF32>(a.dres, r * a.H + c * 8);
         }
-        if (kPrefetch) load(r + step, next);    // in flight through this row's work
         float s[1] = {0.f};
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
@@ -263,7 +266,7 @@ __global__ __launch_bounds__(S::kThreads) void rms_bwd_kernel(RmsBwd a) {
                 if (a.branch) store8<false>(a.branch, r * a.H + c * 8, o);
             }
         }
-        if (!kPrefetch) load(r + step, next);
+        load(r + step, next);
     }
     if constexpr (!kSums) return;
     float* out = a.part + (int64_t)blockIdx.x * a.H;
@@ -366,7 +369,17 @@ __global__ __launch_bounds__(1024) void rms_dw_reduce_kernel(const float* __rest
     else ((bf16_t*)dgamma)[i] = (bf16_t)f32_to_bf16(t);
 }
 
-constexpr int kRmsSumsH = 8192;     // wider: the sums in a kernel of their own
+// Rows up to kRmsSumsH have gamma's sums beside them in registers; wider ones
+// read dy and h again for them (4096 x 8192, fp32 stream: 108 us with the sums,
+// 134 with a kernel of their own; bf16 49 and 63; 300 rows 17.0 and 15.8).
+//
+// One wave per step of a row as far as a workgroup goes, not half as many with two
+// steps each (us, one step / two: fp32 stream 16384 x 1024 52.5 / 54.5, 16384 x 2048
+// 101.2 / 103.4, 8192 x 4096 104.3 / 108.0, 4096 x 8192 108.5 / 116.6; bf16 41.0 / 41.2,
+// 42.0 / 42.2, 44.6 / 46.2, 48.8 / 53.0).  The next row is loaded at a row's end: loads
+// that are in flight through the row's work cost registers and occupancy, 16384 x 1024
+// fp32 52.5 instead of 48.8, 8192 x 4096 104.3 instead of 101.6, bf16 50.3 instead of 44.6.
+constexpr int kRmsSumsH = 8192;
 template <class F>
 void with_bwd_shape(int H, F&& f) {
     if (H <= 128) f(Shape<16, 1, 1, 32>{});
