@@ -37,10 +37,10 @@
 //   * Rows past the end, columns past N and bytes past K read zeros (offsets
 //     past the buffer resource).
 //
-// Measured: 16384 rows over 8 experts of 28672 x 4096 1.88 ms (2.04 PFLOP/s), of
-// 4096 x 14336 0.97 ms (1.98); a library product with one scale per tensor reaches
-// 2.75 at 2048 x 28672 x 4096.  Bound by power: the shader clock is 1.7 to 1.9
-// GHz, and each change that saved cycles cost clock.  Timing variants of an
+// Measured: 16384 rows over 8 experts of 28672 x 4096 1.82 to 1.91 ms (2.0 to 2.1
+// PFLOP/s, matrix cores 51% busy), of 4096 x 14336 0.97 ms (1.98); a library product
+// with one scale per tensor reaches 2.75 at 2048 x 28672 x 4096.  Bound by power: the
+// shader clock is 1.7 to 1.9 GHz, and each change that saved cycles cost clock.  Timing variants of an
 // earlier step (2170 us): without loads 1690, without fma 1830; of this one
 // without stores 1700: y's 0.94 GB add their time at the memory's rate.
 #include "block8.hpp"

@@ -19,7 +19,7 @@
 //
 // Measured (a copy of 1 GiB: 5.1 TB/s): forward of 8192 x 4096 bf16 with residual, y
 // and codes 53 us (5.7 TB/s); backward of 16384 x 2048 over an fp32 stream, with the
-// residual's gradient and the bf16 copy, 96 + 5 us (5.6 TB/s).  One row of 4096: 2.9 us,
+// residual's gradient and the bf16 copy, 94 to 102 + 5 us (5.3 to 5.7 TB/s).  One row of 4096: 2.9 us,
 // the time of an empty launch and a read after it.
 #include "block8.hpp"
 #include "common.hpp"
@@ -171,6 +171,12 @@ template <bool SF32, class S, bool kSums>
 __global__ __launch_bounds__(S::kThreads) void rms_bwd_kernel(RmsBwd a) {
     constexpr int kV = S::kV, kRows = S::kRows, kPer = S::kPer;
     constexpr int kPart = kRows * S::kLanes / 64;   // rows left after each wave has added its own
+    // The next row's loads go out ahead of a row's work for an fp32 stream, behind it
+    // for a bf16 one (us, ahead / behind, other data in every call: fp32 16384 x 2048
+    // 104.2 / 106.0, 8192 x 4096 106.0 / 110.3, 4096 x 8192 110.2 / 113.9, bf16 the same to
+    // 0.5%; the same data in every call, part of it in the last-level cache: fp32 104.3 /
+    // 101.6, bf16 50.3 / 44.6).
+    constexpr bool kPrefetch = SF32 && !S::kLean;
     __shared__ float red[2][16][1];
     __shared__ float comb[kSums && kPart > 1 ? 8 * kPer * kV : 1];
     const int l = S::place();
@@ -230,6 +236,7 @@ __global__ __launch_bounds__(S::kThreads) void rms_bwd_kernel(RmsBwd a) {
             res[v] = Raw8<SF32>{};
             if (a.dres && r < a.T && c < nc) res[v] = load_raw<SF32>(a.dres, r * a.H + c * 8);
         }
+        if (kPrefetch) load(r + step, next);
         float s[1] = {0.f};
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
@@ -266,7 +273,7 @@ __global__ __launch_bounds__(S::kThreads) void rms_bwd_kernel(RmsBwd a) {
                 if (a.branch) store8<false>(a.branch, r * a.H + c * 8, o);
             }
         }
-        load(r + step, next);
+        if (!kPrefetch) load(r + step, next);
     }
     if constexpr (!kSums) return;
     float* out = a.part + (int64_t)blockIdx.x * a.H;
@@ -373,12 +380,10 @@ __global__ __launch_bounds__(1024) void rms_dw_reduce_kernel(const float* __rest
 // read dy and h again for them (4096 x 8192, fp32 stream: 108 us with the sums,
 // 134 with a kernel of their own; bf16 49 and 63; 300 rows 17.0 and 15.8).
 //
-// One wave per step of a row as far as a workgroup goes, not half as many with two
-// steps each (us, one step / two: fp32 stream 16384 x 1024 52.5 / 54.5, 16384 x 2048
+// One wave per 512 columns of a row as far as a workgroup goes, not half as many
+// with two steps each (us, one step / two: fp32 stream 16384 x 1024 52.5 / 54.5, 16384 x 2048
 // 101.2 / 103.4, 8192 x 4096 104.3 / 108.0, 4096 x 8192 108.5 / 116.6; bf16 41.0 / 41.2,
-// 42.0 / 42.2, 44.6 / 46.2, 48.8 / 53.0).  The next row is loaded at a row's end: loads
-// that are in flight through the row's work cost registers and occupancy, 16384 x 1024
-// fp32 52.5 instead of 48.8, 8192 x 4096 104.3 instead of 101.6, bf16 50.3 instead of 44.6.
+// 42.0 / 42.2, 44.6 / 46.2, 48.8 / 53.0).
 constexpr int kRmsSumsH = 8192;
 template <class F>
 void with_bwd_shape(int H, F&& f) {
