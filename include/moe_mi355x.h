@@ -957,7 +957,8 @@ int grouped_linear_block_fwd(int E, int N, int K, int64_t rows, const uint8_t* x
  *   dW_e = dy_e^T x^_e  (bf16 operands: dy itself, and x^ rounded to bf16;
  *                        exact zeros for an expert with no rows)
  * fp32 accumulation, rounded to bf16.  dx has one row per grouped row, also
- * with src_token (moe_unpermute adds the rows of a token).
+ * with src_token (moe_unpermute adds the rows of a token); rows behind the last
+ * expert's stay as they are.
  *
  * dy           bf16 [rows, N].
  * x_codes, x_scales, x_rows, src_token   as in the forward (for dW).

@@ -15,21 +15,43 @@ namespace moe {
 
 namespace {
 
-// Rows: 16 lanes have a block, 8 neighbouring values each; a thread takes every
-// gridDim.x * 256-th chunk of the rows padded to whole blocks.
+// The chunks of a thread: every gridDim.x * 256-th of `per` a row, as row and
+// place in it.  (One division a thread.  With one of 64 bits for every chunk, us:
+// 8192 x 4096 23.7 for 22.7, 300000 x 64 19.0 for 18.2, 4099 x 14336 35.4 for 34.9.)
+struct Chunks {
+    int64_t r, dr;
+    uint32_t c, dc, per;
+    __device__ __forceinline__ Chunks(uint32_t per_) : per(per_) {
+        const uint32_t i = blockIdx.x * 256u + threadIdx.x, step = gridDim.x * 256u;    // below 2^22
+        r = i / per;
+        c = i % per;
+        dr = step / per;
+        dc = step % per;
+    }
+    __device__ __forceinline__ void next() {
+        r += dr;
+        c += dc;
+        if (c >= per) {
+            c -= per;
+            ++r;
+        }
+    }
+};
+
+// Rows: 16 lanes have a block, 8 neighbouring values each, of the rows padded to
+// whole blocks.
 __global__ __launch_bounds__(256) void quant_rows128_kernel(const bf16_t* __restrict__ x, int64_t rows,
                                                             int cols, uint8_t* __restrict__ codes,
                                                             float* __restrict__ scales) {
-    const int per = (int)blocks_of(cols) * 16, nc = cols / 8;
-    const int64_t n = rows * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / per;
-        const int c = (int)(i - r * per);
+    const int nc = cols / 8;
+    for (Chunks at((uint32_t)blocks_of(cols) * 16); at.r < rows; at.next()) {
+        const int64_t r = at.r;
+        const int c = (int)at.c;
         Raw8<false> w{};
         if (c < nc) w = load_raw<false>(x, r * cols + c * 8);
         float v[8], scale;
         unpack<false>(w, v);
-        const u32x2 q = blk_encode8(v, scale);      // n is a multiple of 16: whole blocks are active
+        const u32x2 q = blk_encode8(v, scale);      // 16 chunks a block: whole blocks are active
         if (c < nc) {
             __builtin_nontemporal_store(q, (u32x2*)(codes + r * cols + c * 8));
             if ((c & 15) == 0) scales[(int64_t)(c >> 4) * rows + r] = scale;
@@ -132,11 +154,9 @@ __global__ __launch_bounds__(256) void dequant_rows128_kernel(const uint8_t* __r
                                                               const float* __restrict__ scales,
                                                               const int32_t* __restrict__ src, int64_t x_rows,
                                                               int64_t rows, int cols, bf16_t* __restrict__ out) {
-    const int nc = cols / 8;
-    const int64_t n = rows * nc;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / nc;
-        const int c = (int)(i - r * nc);
+    for (Chunks at((uint32_t)cols / 8); at.r < rows; at.next()) {
+        const int64_t r = at.r;
+        const int c = (int)at.c;
         const int64_t from = src ? src[r] : r;
         float v[8];
 #pragma unroll
