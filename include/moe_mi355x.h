@@ -930,7 +930,9 @@ int fp8_block_quantize_weights(int nmat, int64_t N, int64_t K, const uint16_t* c
  * multiplied by the two scales when they are added to the fp32 accumulator; y
  * is rounded once.  Nothing is quantized here, so weights are prepared once
  * (fp8_block_quantize_weights) and rows come from fp8_block_quantize or
- * moe_rmsnorm_fwd.
+ * moe_rmsnorm_fwd.  Scales are fp32 from 2^-126 on, as the quantizers give them;
+ * their product may leave fp32's range where the value does not (from 2^230 on a
+ * block that sums to 0 gives NaN).
  *
  * E            experts, 1..64.   N: out_features, K: in_features, multiples of
  *              32 up to 2^22, N * K * 2 below 2^31 (otherwise MOE_ERR_SHAPE).
