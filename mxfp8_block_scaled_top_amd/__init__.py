@@ -926,7 +926,8 @@ def moe_balance_fwd(logits, topk_expert, mask=None, balance_coef: float = 0.01, 
     int32 [T, k], mask bool or uint8 [T] (0: the token does not count) or None.
     Returns (loss fp32 scalar, saved): saved holds counts (int32 [E]), tokens
     (int32 [1]), mean_prob (fp32 [E]), losses (fp32 [3]: the loss, its balance
-    and its z part) and what the backward takes."""
+    and its z part) and what the backward takes, the mask among it (not a copy:
+    it stays as it is until the backward, as the logits do)."""
     T, E, dev = _first(logits, "logits", torch.float32)
     if not isinstance(topk_expert, torch.Tensor) or topk_expert.dim() != 2:
         raise MoEError("topk_expert must be a matrix")
@@ -941,18 +942,21 @@ def moe_balance_fwd(logits, topk_expert, mask=None, balance_coef: float = 0.01, 
     _call("moe_balance_fwd", dev, _ptr(logits), T, E, k, _ptr(topk_expert), _ptr(mask), balance_coef,
           z_coef, _ptr(losses), _ptr(counts), _ptr(tokens), _ptr(mean_prob), _ptr(ws), ws.numel())
     return losses[0], {"counts": counts, "tokens": tokens, "mean_prob": mean_prob, "losses": losses, "k": k,
-                       "coefs": (balance_coef, z_coef)}
+                       "coefs": (balance_coef, z_coef), "mask": mask}
 
 
 def moe_balance_bwd(logits, saved: dict, mask=None, dloss=None, dlogits=None, out=None):
     """Gradient of moe_balance_fwd's loss with respect to the logits, fp32
-    [T, E].  mask: the forward's.  dloss: fp32 tensor of one value (None: 1).
+    [T, E].  mask: the forward's (None: the one in saved).  dloss: fp32 tensor of
+    one value (None: 1).
     dlogits: a gradient of the logits that is added, such as moe_route_bwd's.
     out: where the result goes (may be dlogits itself)."""
     T, E, dev = _first(logits, "logits", torch.float32)
     counts, tokens = saved.get("counts"), saved.get("tokens")
     _arg(counts, "saved counts", torch.int32, (E,), dev)
     _arg(tokens, "saved tokens", torch.int32, (1,), dev)
+    if mask is None:
+        mask = saved.get("mask")
     _mask_arg(mask, T, dev)
     if dloss is not None:
         if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
