@@ -936,7 +936,8 @@ int fp8_block_quantize_weights(int nmat, int64_t N, int64_t K, const uint16_t* c
  *
  * E            experts, 1..64.   N: out_features, K: in_features, multiples of
  *              32 up to 2^22, N * K * 2 below 2^31 (otherwise MOE_ERR_SHAPE).
- * rows         total rows (sum of split_sizes), 0 <= rows <= INT32_MAX.
+ * rows         total rows (sum of split_sizes), 0 <= rows <= INT32_MAX, and
+ *              (rows / 64 + E) ceil(max(N, K) / 128) <= INT32_MAX (MOE_ERR_SHAPE).
  * x_codes, x_scales, x_rows   uint8 [x_rows, K] and fp32 [ceil(K/128), x_rows].
  * src_token    int32 [rows]: grouped row r is row src_token[r] of x (a row of
  *              zeros where that is outside [0, x_rows)), x_rows * K below

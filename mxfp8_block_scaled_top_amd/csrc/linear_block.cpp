@@ -39,7 +39,7 @@ int check_block(int E, int N, int K, int64_t rows, int64_t x_rows, const void* s
     if ((int64_t)N * K * 2 >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
     if (N > (1 << 22) || K > (1 << 22)) return MOE_ERR_SHAPE;
     if (src_token && x_rows * K >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
-    // workgroups of a launch (tiles of 64 rows and 128 columns at least)
+    // the kernels count tiles of 256 rows and 256 columns in int (smaller ones here: room)
     const int64_t widest = N > K ? N : K;
     if ((rows / 64 + E) * ((widest + 127) / 128) > INT32_MAX) return MOE_ERR_SHAPE;
     return MOE_OK;

@@ -234,6 +234,19 @@ def test_grouped_linear_block_bwd_refuses(L, change, status):
     assert L.grouped_linear_block_bwd(*a.values(), None) == status
 
 
+@pytest.mark.parametrize("N,K", [(1 << 22, 32), (32, 1 << 22)])
+def test_more_tiles_than_an_int_counts_are_refused(L, N, K):
+    """(rows / 64 + E) * ceil(widest / 128) up to INT32_MAX: with 32768 blocks and 2 experts 64 * 65533 + 63 rows."""
+    t, most = _tab(P, P), 64 * ((2 ** 31 - 1) // 32768 - 2) + 63
+    w = moe.moe_workspace_bytes
+    assert w(moe.MOE_OP_LINEAR_BLOCK_BWD, most, K, N, 2, 1, 0) > 0
+    assert w(moe.MOE_OP_LINEAR_BLOCK_BWD, most + 1, K, N, 2, 1, 0) == 0
+    for rows, status in ((most, NULL), (most + 1, SHAPE)):
+        assert L.grouped_linear_block_fwd(2, N, K, rows, P, P, rows, None, None, t, t, P, None) == status
+        assert L.grouped_linear_block_bwd(2, N, K, rows, P, P, P, rows, None, None, t, t, P, _tab(P, P2), P, 1 << 62,
+                                          None) == status
+
+
 def test_workspace_bytes(L):
     f = L.moe_rmsnorm_workspace_bytes
     assert f(4, 64) >= 64 * 4 and f(0, 64) > 0 and f(-1, 64) == f(4, 12) == f(4, 0) == f(4, 65536) == 0
