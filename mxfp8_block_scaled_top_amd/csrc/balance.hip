@@ -15,7 +15,7 @@
 // rows, which a second kernel adds (in one launch where one workgroup has all
 // tokens); counts are integers.  No float atomics.
 //
-// Measured: 256 x 4 4.7 us and 2.1 for the gradient; 16384 x 64, 8 picks, 5.9 + 4.4 and 5.3;
+// Measured: 256 x 4 4.9 us and 2.2 for the gradient; 16384 x 64, 8 picks, 5.8 + 4.3 and 5.5;
 // a million tokens of 64 180 us both ways (5 TB/s).
 #include "common.hpp"
 #include "kernels.hpp"

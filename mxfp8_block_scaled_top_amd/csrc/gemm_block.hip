@@ -38,12 +38,14 @@
 //   * Rows past the end, columns past N and bytes past K read zeros (offsets
 //     past the buffer resource).
 //
-// Measured: 16384 rows over 8 experts of 28672 x 4096 1.82 to 1.91 ms (2.0 to 2.1
-// PFLOP/s, matrix cores 51% busy), of 4096 x 14336 0.97 ms (1.98); a library product
+// Measured: 16384 rows over 8 experts of 28672 x 4096 1.80 to 1.92 ms (2.0 to 2.1
+// PFLOP/s, matrix cores 50% busy), of 4096 x 14336 0.87 ms (2.2); a library product
 // with one scale per tensor reaches 2.75 at 2048 x 28672 x 4096.  Bound by power: the
-// shader clock is 1.7 to 1.9 GHz, and each change that saved cycles cost clock.  Timing variants of an
-// earlier step (2170 us): without loads 1690, without fma 1830; of this one
-// without stores 1700: y's 0.94 GB add their time at the memory's rate.
+// shader clock falls to 1.5 GHz behind the first call after a rest and settles at 2.1
+// of 2.4 some 20 calls later, and each change that saved cycles cost clock.  Timing variants of an
+// earlier step (2170 us): without loads 1690, without fma 1830; of a later one (1830)
+// without stores 1700: y's 0.94 GB add their time at the memory's rate.  (The clock
+// depends on what ran before: figures that are compared are of one run, side by side.)
 #include "block8.hpp"
 #include "common.hpp"
 #include "dma.hpp"
@@ -106,7 +108,9 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // 102 it stays a normal number too, and every step up to the fma is what it is
 // without the split (the same bits).  f is in [1, 2) but for scales out of that
 // range (and 0, infinity and NaN, which it is then itself).  (8 x 2048 rows of
-// 28672 x 4096 1883 -> 1912 us, 4099 rows of 4096 x 14336 both ways 882 -> 888.)
+// 28672 x 4096 1757 -> 1803 us, of 4096 x 14336 850 -> 874, three quarters of it for the scaled
+// form of the instruction.  Deciding by the product of the scales, per fragment
+// column: the compiler spills 240 registers, 6500 us.)
 struct BlkScale {
     float f;
     int e;
@@ -443,15 +447,26 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_block_kernel(BlockGemm p, in
 // workgroup has 32 columns, its eight waves every eighth block of K each, and
 // the fragments come straight from memory into registers.  Few registers, and
 // so eight waves per SIMD, keep the memory busy: 16 rows over 8 experts of
-// 28672 x 4096 138 us (6.8 TB/s); with the next block's loads in flight during
+// 28672 x 4096 158 us with other weights in every call (5.9 TB/s), 138 where the same
+// come again; beside these 138, with the next block's loads in flight during
 // the current one's products (78 registers for 52) 147, with two blocks at once
 // 151, with streaming loads 166 (they also keep weights that would fit out of
 // the last-level cache).  The waves' sums meet in LDS and are added in order.
 //
 // Taken up to 8 rows per expert on average; an expert with more than 16 goes
-// in passes of 16.  us here / in tiles: 8 experts of 14336 x 4096, 64 rows
-// 88 / 105, 128 rows 128 / 110; 64 experts of 2816 x 2048, 256 rows 63 / 74, 512 rows
-// 70 / 77 (Zipf loads, where the tiles would win: 84 / 71), 1024 rows 102 / 78.
+// in passes of 16, and its workgroups read its weights again in each.  The rule
+// cannot see the loads, which are on the device.  us here / in tiles, other weights
+// in every call:
+//                                  even       Zipf 1.2   half on one  all on one
+//   64 of 2816 x 2048, 512 rows    65 / 67    75 / 79     93 / 82     109 / 33
+//                      256         62 / 66    52 / 54     69 / 80      56 / 32
+//                      128         62 / 65    36 / 39     63 / 69      29 / 21
+//   8 of 14336 x 4096, 64          86 / 111   93 / 106   103 / 111     49 / 26
+//   8 of 28672 x 4096, 64         164 / 175  176 / 174   195 / 177     94 / 38
+//                      32         158 / 174  136 / 158   172 / 175     51 / 36
+// so it loses where most rows meet one expert, by 76 us at most here.  At 16 rows
+// per expert on average the tiles are faster for even loads too (8 of 14336 x 4096,
+// 128 rows 128 / 110, 64 of 2816 x 2048, 1024 rows 102 / 78).
 constexpr int kFewMean = 8;
 constexpr int kFewN = 32, kFewWaves = 8, kFewThreads = 64 * kFewWaves, kFewRow = kFewN + 4;
 

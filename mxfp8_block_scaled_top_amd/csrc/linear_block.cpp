@@ -12,8 +12,8 @@
 //                                      (2^-8 of each product at most) keeps dy
 //                                      as it is
 //
-// 4099 rows over 8 experts of 4096 x 14336, us: dy's codes 12, dgrad 304, decoding
-// 33, wgrad 542.
+// 4099 rows over 8 experts of 4096 x 14336, us, the clock settled: dy's codes 12,
+// dgrad 329, decoding 33, wgrad 476.
 #include "moe_mi355x.h"
 
 #include <hip/hip_runtime.h>

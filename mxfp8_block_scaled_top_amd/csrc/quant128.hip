@@ -2,8 +2,8 @@
 // weights in 128 x 128 blocks (with a transposed copy on request, the operand of
 // the data gradient), and rows back to bf16.
 //
-// All three are bound by HBM bytes: 8192 x 4096 rows 20 to 21 us (4.9 TB/s, a copy of
-// 1 GiB 5.1), 64 matrices of 2816 x 2048 in both orders 266 us (5.5), 4099 rows of
+// All three are bound by HBM bytes: 8192 x 4096 rows 19 to 21 us (5.0 TB/s, a copy of
+// 1 GiB 5.1), 64 matrices of 2816 x 2048 in both orders 265 us (5.6), 4099 rows of
 // 14336 decoded 33 us (5.5).
 #include "block8.hpp"
 #include "common.hpp"
@@ -16,8 +16,8 @@ namespace moe {
 namespace {
 
 // The chunks of a thread: every gridDim.x * 256-th of `per` a row, as row and
-// place in it.  (One division a thread.  With one of 64 bits for every chunk, us:
-// 8192 x 4096 23.7 for 22.7, 300000 x 64 19.0 for 18.2, 4099 x 14336 35.4 for 34.9.)
+// place in it.  (One division a thread.  With one of 64 bits for every chunk, whole calls,
+// us: 8192 x 4096 20.8 for 20.2, 300000 x 64 20.7 for 19.7, 4099 x 14336 36.6 for 35.4.)
 struct Chunks {
     int64_t r, dr;
     uint32_t c, dc, per;

@@ -33,9 +33,11 @@
 // Against a workgroup per tile (gemm.hip), with the rows' decoding, us: 4099 uneven
 // rows over 8 experts of 4096 x 14336 604 -> 577, 16384 rows 1660 -> 1620, of 28672 x 4096
 // 2897 -> 2855 (1.35 PFLOP/s); 64 experts of 2816 x 2048, 512 rows each, 563 -> 441.
-// Bound by power for long tiles and by that and the gradients' writes for short
-// ones: without the writes 4099 rows take 480, and neither streaming writes (672)
-// nor waits that let them finish later (580) make up for any of it.
+// (Side by side; at the settled clock of 60 calls in a row 4099 rows take 518, the
+// 64 experts 439.)  Bound by power for long tiles and by that and the gradients'
+// writes for short ones: without the writes 4099 rows take 365 of these 518, and neither
+// streaming writes (672 for 577) nor waits that let them finish later (580) make up for
+// any of it.
 #include "common.hpp"
 #include "dma.hpp"
 #include "kernels.hpp"
