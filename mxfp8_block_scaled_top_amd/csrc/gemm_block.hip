@@ -39,10 +39,10 @@
 //     past the buffer resource).
 //
 // Measured: 16384 rows over 8 experts of 28672 x 4096 1.80 to 1.92 ms (2.0 to 2.1
-// PFLOP/s, matrix cores 50% busy), of 4096 x 14336 0.87 ms (2.2); a library product
+// PFLOP/s, matrix cores 49 to 50% busy), of 4096 x 14336 0.87 ms (2.2); a library product
 // with one scale per tensor reaches 2.75 at 2048 x 28672 x 4096.  Bound by power: the
-// shader clock falls to 1.5 GHz behind the first call after a rest and settles at 2.1
-// of 2.4 some 20 calls later, and each change that saved cycles cost clock.  Timing variants of an
+// shader clock falls to 1.5 GHz behind the first call after a rest and settles at 2.0 to
+// 2.1 of 2.4 some 20 calls later, and each change that saved cycles cost clock.  Timing variants of an
 // earlier step (2170 us): without loads 1690, without fma 1830; of a later one (1830)
 // without stores 1700: y's 0.94 GB add their time at the memory's rate.  (The clock
 // depends on what ran before: figures that are compared are of one run, side by side.)

@@ -13,7 +13,7 @@
 //                                      as it is
 //
 // 4099 rows over 8 experts of 4096 x 14336, us, the clock settled: dy's codes 12,
-// dgrad 329, decoding 33, wgrad 476.
+// dgrad 329 to 338, decoding 33, wgrad 476 to 504 (the clock of two cards).
 #include "moe_mi355x.h"
 
 #include <hip/hip_runtime.h>

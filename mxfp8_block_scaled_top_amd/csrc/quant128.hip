@@ -2,8 +2,8 @@
 // weights in 128 x 128 blocks (with a transposed copy on request, the operand of
 // the data gradient), and rows back to bf16.
 //
-// All three are bound by HBM bytes: 8192 x 4096 rows 19 to 21 us (5.0 TB/s, a copy of
-// 1 GiB 5.1), 64 matrices of 2816 x 2048 in both orders 265 us (5.6), 4099 rows of
+// All three are bound by HBM bytes: 8192 x 4096 rows 19 to 21 us (4.9 to 5.2 TB/s, a copy
+// of 1 GiB 5.1), 64 matrices of 2816 x 2048 in both orders 266 us (5.5), 4099 rows of
 // 14336 decoded 33 us (5.5).
 #include "block8.hpp"
 #include "common.hpp"

@@ -20,7 +20,7 @@
 // Measured (a copy of 1 GiB: 5.1 TB/s): forward of 8192 x 4096 bf16 with residual, y
 // and codes 54 us (5.6 TB/s), into an fp32 stream 85, of fp32 rows 99; 4096 x 16384 bf16
 // 110, fp32 193 (all 5.1 to 5.5 TB/s).  Backward of 16384 x 2048 over an fp32 stream, with
-// the residual's gradient and the bf16 copy, 103 + 5 us (5.2 TB/s); 8192 x 4096 bf16 45.
+// the residual's gradient and the bf16 copy, 103 to 104 + 5 us (5.2 TB/s); 8192 x 4096 bf16 45.
 // Above 8192 columns gamma's gradient reads dy and h again: 4096 x 16384 bf16 117 us for
 // 68 without it, fp32 with residual 242 for 174.  One row of 4096: 2.9 us, the time
 // of an empty launch and a read after it.
